@@ -30,6 +30,9 @@ SPEC_BF16 = 1
 SPEC_SCHED_EARLY_STOP = 0
 SPEC_SCHED_GLOBAL = 1
 SPEC_VERIFY_LEFT_TO_RIGHT = 0x100
+SPEC_DISTILL_KL = 0
+SPEC_DISTILL_TV = 1
+SPEC_DISTILL_SAVED = 6
 
 REQ_BAD_TOKEN = 1
 REQ_BAD_TEMPERATURE = 2
@@ -39,6 +42,7 @@ REQ_BAD_TOPK = 16
 REQ_BAD_CONFIDENCE = 32
 REQ_OVER_BUDGET = 64
 REQ_BAD_ROWS = 128
+REQ_BAD_LIST = 256
 
 # name -> (restype, argtypes)
 _P = ctypes.c_void_p
@@ -75,6 +79,15 @@ EXPORTS = {
     "spec_sts_workspace_size": (_Z, [_I, _I, _I]),
     "spec_sts_fit": (_I, [_I, _I, _P, _P, _I, _P, _I, _P, _P, _P, _P, _Z, _P]),
     "spec_sts_apply": (_I, [_I, _I, _P, _P, _P, _P]),
+    "spec_teacher_workspace_size": (_Z, [_I, _I, _I, _I]),
+    "spec_teacher_topk": (_I, [_I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    "spec_distill_workspace_size": (_Z, [_I, _I, _I, _I]),
+    "spec_distill_loss": (_I, [_I, _I, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    "spec_distill_loss_backward": (_I, [_I, _I, _I, _I, _P, _I, _P, _P, _I, _P, _P, _P, _P, _P]),
+    "spec_head_xent_workspace_size": (_Z, [_I, _I, _I, _I]),
+    "spec_head_xent": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    "spec_head_xent_backward_workspace_size": (_Z, [_I, _I, _I, _I]),
+    "spec_head_xent_backward": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
 }
 
 _lib_handle = None
@@ -137,6 +150,14 @@ def _launch(stream, allocated, call):
             if t is not None:
                 t.record_stream(s)
     return code
+
+
+def _launch_on(device, stream, allocated, call):
+    """_launch with `device` current: its current stream by default, and a stream of that device only."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.device(device):
+        return _launch(stream, allocated, call)
 
 
 def _check(fn, code):
@@ -746,3 +767,250 @@ def philox_uniforms(seed: torch.Tensor, request: torch.Tensor, position: torch.T
         n, _ptr(seed), _ptr(request), _ptr(position), _ptr(ua), _ptr(ue), sp))
     _check("spec_philox_uniforms", code)
     return ua, ue
+
+
+def _device_workspace(nbytes, device, workspace, allocated):
+    """_workspace, with a caller's own checked to be a contiguous tensor on `device`."""
+    if workspace is not None:
+        _dev(workspace, "workspace")
+        _on(device, workspace=workspace)
+    return _workspace(nbytes, device, workspace, allocated)
+
+
+def _list_size(K):
+    if isinstance(K, bool) or not isinstance(K, int):
+        raise TypeError("K must be an int")
+    return K
+
+
+def teacher_topk(target: torch.Tensor, K: int, lengths: Optional[torch.Tensor] = None,
+                 temperature: Optional[torch.Tensor] = None, out: Optional[dict] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """spec_teacher_topk: the K largest logits of every target row k < L_i and the row's normaliser.
+
+    target [B, gamma+1, V] (float32 or bfloat16; row gamma is not read), lengths [B] int32 or None,
+    temperature [B] float32 (default ones, > 0).  Returns dict(ids [B, gamma, K] int32, values
+    [B, gamma, K] float32, lse [B, gamma] float32, status [B] int32).
+    """
+    lib = load_library()
+    if not isinstance(target, torch.Tensor) or target.dim() != 3:
+        raise ValueError("target must be [B, gamma+1, V]")
+    B, G1, V = target.shape
+    G, K = G1 - 1, _list_size(K)
+    for name, t in (("lengths", lengths), ("temperature", temperature)):
+        _vec(t, name, B)
+    _dev(target, "target", (torch.float32, torch.bfloat16), 3)
+    _dev(lengths, "lengths", torch.int32, 1)
+    _dev(temperature, "temperature", torch.float32, 1)
+    dev = target.device
+    _on(dev, lengths=lengths, temperature=temperature)
+    mine = []
+
+    def call(sp):
+        return lib.spec_teacher_topk(
+            B, G, V, _logit_dtype(target), _ptr(target), K, _ptr(lengths), _ptr(temperature), _ptr(out["ids"]),
+            _ptr(out["values"]), _ptr(out.get("lse")), _ptr(out.get("status")), _ptr(ws),
+            ws.numel() * ws.element_size(), sp)
+    with torch.cuda.device(dev):
+        if temperature is None:
+            temperature = torch.ones(B, dtype=torch.float32, device=dev)
+            mine.append(temperature)
+        if out is None:
+            out = dict(ids=torch.empty((B, G, max(K, 0)), dtype=torch.int32, device=dev),
+                       values=torch.empty((B, G, max(K, 0)), dtype=torch.float32, device=dev),
+                       lse=torch.empty((B, G), dtype=torch.float32, device=dev),
+                       status=torch.empty(B, dtype=torch.int32, device=dev))
+            mine.extend(out.values())
+        else:
+            _check_out(out, dict(ids=((B, G, K), torch.int32, True), values=((B, G, K), torch.float32, True),
+                                 lse=((B, G), torch.float32, False), status=((B,), torch.int32, False)), dev)
+        ws = _device_workspace(int(lib.spec_teacher_workspace_size(B, G, V, K)), dev, workspace, mine)
+        _check("spec_teacher_topk", _launch_on(dev, stream, mine, call))
+    return out
+
+
+def _list_inputs(draft, ids, values, temperature):
+    if not isinstance(draft, torch.Tensor) or draft.dim() != 3:
+        raise ValueError("draft must be [B, gamma, V]")
+    B, G, V = draft.shape
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 3 or tuple(ids.shape[:2]) != (B, G):
+        raise ValueError("ids must be [B, gamma, K]")
+    K = ids.shape[2]
+    _shape(values, "values", (B, G, K))
+    _vec(temperature, "temperature", B)
+    _dev(draft, "draft", (torch.float32, torch.bfloat16), 3)
+    _dev(ids, "ids", torch.int32, 3)
+    _dev(values, "values", torch.float32, 3)
+    _dev(temperature, "temperature", torch.float32, 1)
+    _on(draft.device, ids=ids, values=values, temperature=temperature)
+    return B, G, V, K
+
+
+def distill_loss(draft: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
+                 teacher_lse: Optional[torch.Tensor] = None, mode: int = SPEC_DISTILL_KL,
+                 lengths: Optional[torch.Tensor] = None, temperature: Optional[torch.Tensor] = None,
+                 out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """spec_distill_loss: the distance of softmax(draft / T) from the teacher's top logits.
+
+    draft [B, gamma, V] (float32 or bfloat16); ids [B, gamma, K] int32 and values [B, gamma, K] float32
+    (teacher_topk's); teacher_lse [B, gamma] float32 keeps the teacher's mass outside the list as one
+    bucket (None: the list is renormalised); mode SPEC_DISTILL_KL or SPEC_DISTILL_TV; lengths [B] int32;
+    temperature [B] float32 (default ones, > 0).  Returns dict(loss [B, gamma] float32, saved (for
+    distill_loss_backward), status [B] int32).
+    """
+    lib = load_library()
+    B, G, V, K = _list_inputs(draft, ids, values, temperature)
+    _shape(teacher_lse, "teacher_lse", (B, G))
+    _vec(lengths, "lengths", B)
+    _dev(teacher_lse, "teacher_lse", torch.float32, 2)
+    _dev(lengths, "lengths", torch.int32, 1)
+    dev = draft.device
+    _on(dev, teacher_lse=teacher_lse, lengths=lengths)
+    mine = []
+
+    def call(sp):
+        return lib.spec_distill_loss(
+            B, G, V, _logit_dtype(draft), _ptr(draft), K, _ptr(ids), _ptr(values), _ptr(teacher_lse), int(mode),
+            _ptr(lengths), _ptr(temperature), _ptr(out["loss"]), _ptr(out["saved"]), _ptr(out.get("status")),
+            _ptr(ws), ws.numel() * ws.element_size(), sp)
+    with torch.cuda.device(dev):
+        if temperature is None:
+            temperature = torch.ones(B, dtype=torch.float32, device=dev)
+            mine.append(temperature)
+        if out is None:
+            out = dict(loss=torch.empty((B, G), dtype=torch.float32, device=dev),
+                       saved=torch.empty((B, G, SPEC_DISTILL_SAVED), dtype=torch.float64, device=dev),
+                       status=torch.empty(B, dtype=torch.int32, device=dev))
+            mine.extend(out.values())
+        else:
+            _check_out(out, dict(loss=((B, G), torch.float32, True),
+                                 saved=((B, G, SPEC_DISTILL_SAVED), torch.float64, True),
+                                 status=((B,), torch.int32, False)), dev)
+        ws = _device_workspace(int(lib.spec_distill_workspace_size(B, G, V, K)), dev, workspace, mine)
+        _check("spec_distill_loss", _launch_on(dev, stream, mine, call))
+    return out
+
+
+def distill_loss_backward(draft: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, saved: torch.Tensor,
+                          grad_loss: torch.Tensor, mode: int = SPEC_DISTILL_KL,
+                          temperature: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                          stream=None, in_place: bool = False) -> torch.Tensor:
+    """spec_distill_loss_backward: grad_loss [B, gamma] float32 times the gradient of distill_loss with
+    respect to the draft logits, [B, gamma, V] in draft's dtype.
+
+    draft, ids, values, mode and temperature as given to distill_loss, `saved` its output.  in_place
+    writes the gradient over `draft`.
+    """
+    lib = load_library()
+    B, G, V, K = _list_inputs(draft, ids, values, temperature)
+    _shape(saved, "saved", (B, G, SPEC_DISTILL_SAVED))
+    _shape(grad_loss, "grad_loss", (B, G))
+    _shape(out, "out", (B, G, V))
+    _dev(saved, "saved", torch.float64, 3)
+    _dev(grad_loss, "grad_loss", torch.float32, 2)
+    _dev(out, "out", draft.dtype, 3)
+    dev = draft.device
+    _on(dev, saved=saved, grad_loss=grad_loss, out=out)
+    if in_place and out is not None:
+        raise ValueError("pass out or in_place, not both")
+    mine = []
+    with torch.cuda.device(dev):
+        if temperature is None:
+            temperature = torch.ones(B, dtype=torch.float32, device=dev)
+            mine.append(temperature)
+        if in_place:
+            out = draft
+        elif out is None:
+            out = torch.empty_like(draft)
+            mine.append(out)
+        code = _launch_on(dev, stream, mine, lambda sp: lib.spec_distill_loss_backward(
+            B, G, V, _logit_dtype(draft), _ptr(draft), K, _ptr(ids), _ptr(values), int(mode), _ptr(temperature),
+            _ptr(saved), _ptr(grad_loss), _ptr(out), sp))
+        _check("spec_distill_loss_backward", code)
+    return out
+
+
+def _head_inputs(hidden, weight, labels):
+    if not isinstance(hidden, torch.Tensor) or hidden.dim() != 2:
+        raise ValueError("hidden must be [N, d]")
+    N, d = hidden.shape
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2 or weight.shape[1] != d:
+        raise ValueError("weight must be [V, d] with hidden's d")
+    V = weight.shape[0]
+    _vec(labels, "labels", N)
+    _dev(hidden, "hidden", (torch.float32, torch.bfloat16), 2)
+    _dev(weight, "weight", hidden.dtype, 2)
+    _dev(labels, "labels", torch.int32, 1)
+    _on(hidden.device, weight=weight, labels=labels)
+    return N, V, d
+
+
+def head_xent(hidden: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor, out: Optional[dict] = None,
+              workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """spec_head_xent: cross entropy of softmax(hidden @ weight.T) against labels, per row.
+
+    hidden [N, d] and weight [V, d] (both float32 or both bfloat16; rows of a multiple of 16 bytes),
+    labels [N] int32 (-1: the row is left out, loss 0).  The logits are not stored.  Returns dict(loss
+    [N] float32, lse [N] float32 (for head_xent_backward), status [N] int32).
+    """
+    lib = load_library()
+    N, V, d = _head_inputs(hidden, weight, labels)
+    dev, dt = hidden.device, _logit_dtype(hidden)
+    mine = []
+
+    def call(sp):
+        return lib.spec_head_xent(N, V, d, dt, _ptr(hidden), _ptr(weight), _ptr(labels), _ptr(out["loss"]),
+                                  _ptr(out["lse"]), _ptr(out.get("status")), _ptr(ws),
+                                  ws.numel() * ws.element_size(), sp)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = dict(loss=torch.empty(N, dtype=torch.float32, device=dev),
+                       lse=torch.empty(N, dtype=torch.float32, device=dev),
+                       status=torch.empty(N, dtype=torch.int32, device=dev))
+            mine.extend(out.values())
+        else:
+            _check_out(out, dict(loss=((N,), torch.float32, True), lse=((N,), torch.float32, True),
+                                 status=((N,), torch.int32, False)), dev)
+        ws = _device_workspace(int(lib.spec_head_xent_workspace_size(N, V, d, dt)), dev, workspace, mine)
+        _check("spec_head_xent", _launch_on(dev, stream, mine, call))
+    return out
+
+
+def head_xent_backward(hidden: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor, lse: torch.Tensor,
+                       grad_loss: torch.Tensor, need_hidden: bool = True, need_weight: bool = True,
+                       out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """spec_head_xent_backward: the gradients of (grad_loss * loss).sum(), grad_loss [N] float32.
+
+    hidden, weight and labels as given to head_xent, `lse` its output.  Returns dict(grad_hidden [N, d],
+    grad_weight [V, d]) in hidden's dtype; need_hidden / need_weight (or an `out` holding only one of
+    them) leave the other out.
+    """
+    lib = load_library()
+    N, V, d = _head_inputs(hidden, weight, labels)
+    _vec(lse, "lse", N)
+    _vec(grad_loss, "grad_loss", N)
+    _dev(lse, "lse", torch.float32, 1)
+    _dev(grad_loss, "grad_loss", torch.float32, 1)
+    dev, dt = hidden.device, _logit_dtype(hidden)
+    _on(dev, lse=lse, grad_loss=grad_loss)
+    mine = []
+
+    def call(sp):
+        return lib.spec_head_xent_backward(N, V, d, dt, _ptr(hidden), _ptr(weight), _ptr(labels), _ptr(lse),
+                                           _ptr(grad_loss), _ptr(out.get("grad_hidden")),
+                                           _ptr(out.get("grad_weight")), _ptr(ws), ws.numel() * ws.element_size(),
+                                           sp)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = {}
+            if need_hidden:
+                out["grad_hidden"] = torch.empty_like(hidden)
+            if need_weight:
+                out["grad_weight"] = torch.empty_like(weight)
+            mine.extend(out.values())
+        else:
+            _check_out(out, dict(grad_hidden=((N, d), hidden.dtype, False),
+                                 grad_weight=((V, d), hidden.dtype, False)), dev)
+        ws = _device_workspace(int(lib.spec_head_xent_backward_workspace_size(N, V, d, dt)), dev, workspace, mine)
+        _check("spec_head_xent_backward", _launch_on(dev, stream, mine, call))
+    return out

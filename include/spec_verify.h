@@ -20,7 +20,11 @@
  *                               sequential sampler and the confidence head
  *                               (paper §3.1, §3.2.1);
  *   - spec_sts_fit / _apply  -- Sequential Temperature Scaling of the
- *                               confidences (paper §3.2.1).
+ *                               confidences (paper §3.2.1);
+ *   - spec_teacher_topk, spec_distill_loss / _backward,
+ *     spec_head_xent / _backward -- the drafter's training losses (paper §3.3:
+ *                               cross entropy and total variation) and their
+ *                               gradients.
  *
  * Conventions shared by every entry point
  *   - Every array argument is a DEVICE pointer (hipMalloc'd or a torch CUDA
@@ -94,11 +98,22 @@ enum {
 #define SPEC_REQ_BAD_CONFIDENCE 32  /* scheduler: a confidence outside [0, 1] or NaN */
 #define SPEC_REQ_OVER_BUDGET 64     /* spec_verify_bounded: the request's rows did not fit the token cap */
 #define SPEC_REQ_BAD_ROWS 128      /* spec_verify_flat: the request's rows lie past the row counts passed */
+#define SPEC_REQ_BAD_LIST 256      /* spec_distill_loss: a token id named twice in one row's teacher list */
 
 /* Limits of this library. */
 #define SPEC_MAX_GAMMA 64
 #define SPEC_MAX_V 524288           /* bf16; fp32 rows are limited to SPEC_MAX_V / 2 */
 #define SPEC_MAX_SCHED_CANDIDATES 16384 /* B * gamma for spec_schedule_lengths */
+#define SPEC_MAX_TEACHER_K 256      /* entries of a teacher list */
+#define SPEC_MAX_HEAD_ROWS 1048576  /* rows of spec_head_xent */
+#define SPEC_MAX_HEAD_WIDTH 16384   /* hidden width of spec_head_xent */
+
+/* Distillation loss (spec_distill_loss). */
+enum {
+    SPEC_DISTILL_KL = 0, /* KL(teacher || draft) */
+    SPEC_DISTILL_TV = 1  /* total variation distance, 1 - the overlap mass */
+};
+#define SPEC_DISTILL_SAVED 6 /* float64 words per position that the forward call leaves for the backward */
 
 int32_t spec_abi_version(void);
 const char* spec_status_string(int32_t status);
@@ -543,6 +558,161 @@ int32_t spec_sts_fit(int32_t N, int32_t gamma, const float* conf_logits, const u
  */
 int32_t spec_sts_apply(int32_t B, int32_t gamma, const float* conf_logits, const double* tau, float* conf_out,
                        void* stream);
+
+/*
+ * Training the drafter on the target's distributions (DSpark paper, §3.3: the
+ * block's cross entropy and total variation losses, weighted by position; the
+ * weights come in through grad_loss).  The target's rows are reduced to their
+ * top logits once (spec_teacher_topk), which stand in for the V logits when the
+ * draft is trained (spec_distill_loss and its gradient); the cross entropy
+ * against token labels is taken from hidden states and the vocabulary head
+ * without storing logits (spec_head_xent and its gradients).
+ *
+ * spec_teacher_topk -- per draft position, the K largest target logits and the
+ * log normaliser of the whole row.
+ *
+ * Arguments (device pointers)
+ *   B, gamma, V, dtype, target_logits [B, gamma+1, V] (row gamma is not read),
+ *   lengths [B] or NULL, as for spec_overlap_mass
+ *   1 <= K <= SPEC_MAX_TEACHER_K
+ *   temperature  [B] float32, > 0 (0, the greedy rule, has no distribution and
+ *                is SPEC_REQ_BAD_TEMPERATURE here)
+ * Outputs
+ *   ids_out      [B, gamma, K] int32: token ids by logit descending, equal
+ *                logits by id ascending; -1 past the row's finite logits
+ *                (a logit of -inf is never listed)
+ *   values_out   [B, gamma, K] float32: their raw logits; -inf where the id is -1
+ *   lse_out      [B, gamma] float32 or NULL: ln sum_v exp(z_v / T_i) over the row
+ *                (exponentials fp32, sums fp64)
+ *   status       [B] int32 or NULL: BAD_LENGTH, BAD_TEMPERATURE, NONFINITE (a row
+ *                k < L_i with a NaN or +inf, or with no finite logit)
+ *   Positions k >= L_i get ids -1, values -inf and lse -inf; every position of a
+ *   request with a status gets ids -1, values NaN and lse NaN.
+ *   workspace    at least spec_teacher_workspace_size(B, gamma, V, K) bytes,
+ *                256-byte aligned, owned by the caller, busy until the call's
+ *                kernels finish on `stream`.
+ * Errors: as for spec_overlap_mass; SPEC_ERR_INVALID_ARG for K; and
+ * SPEC_ERR_UNSUPPORTED when a launch would pass 2^32 work-items (512 per row
+ * and per 64 KB of a row).
+ */
+size_t spec_teacher_workspace_size(int32_t B, int32_t gamma, int32_t V, int32_t K);
+
+int32_t spec_teacher_topk(int32_t B, int32_t gamma, int32_t V, int32_t dtype, const void* target_logits, int32_t K,
+                          const int32_t* lengths, const float* temperature, int32_t* ids_out, float* values_out,
+                          float* lse_out, int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * spec_distill_loss -- distance of the draft distribution from a teacher's top
+ * logits, per draft position.
+ *
+ * For position k < L_i of request i, with the list's entries e (token id_e,
+ * logit v_e; an entry with id -1 or logit -inf is unused), q = softmax(z / T_i)
+ * over the whole draft row z, and S the listed tokens:
+ *   p_e = exp(v_e / T_i - t), t = ln sum_e exp(v_e / T_i) without teacher_lse
+ *         (the list renormalised), t = teacher_lse[i, k] with it;
+ *   r_t = max(0, 1 - sum_e p_e) with teacher_lse, else 0;  r_s = sum_{v not in S} q_v
+ *         (the two tails: one bucket for every token outside the list);
+ *   KL: loss = sum_e p_e (ln p_e - ln q_e) + r_t (ln r_t - ln r_s)
+ *   TV: loss = sum_e max(p_e - q_e, 0) + max(r_t - r_s, 0)
+ *       (without teacher_lse this is the total variation distance of the
+ *       renormalised list from q, 1 - their overlap mass)
+ * with 0 ln 0 = 0; a KL loss is +inf where q has no mass and p has.  A row
+ * without a used entry, and every position k >= L_i, has loss 0 and is not read.
+ *
+ * Arguments (device pointers)
+ *   B, gamma, V, dtype as for spec_verify; draft_logits [B, gamma, V]
+ *   1 <= K <= SPEC_MAX_TEACHER_K; teacher_ids [B, gamma, K] int32 and
+ *   teacher_values [B, gamma, K] float32 (spec_teacher_topk's, in any order);
+ *   teacher_lse  [B, gamma] float32 or NULL (spec_teacher_topk's lse_out)
+ *   mode         SPEC_DISTILL_KL or SPEC_DISTILL_TV
+ *   lengths      [B] or NULL; temperature [B] float32, > 0
+ * Outputs
+ *   loss_out     [B, gamma] float32 (NaN for a request with a status)
+ *   saved_out    [B, gamma, SPEC_DISTILL_SAVED] float64: what spec_distill_loss_backward reads
+ *   status       [B] int32 or NULL: BAD_LENGTH, BAD_TEMPERATURE, BAD_TOKEN (an id
+ *                outside [-1, V)), BAD_LIST (an id named by two used entries of a
+ *                row), NONFINITE (a NaN or +inf in a used entry's logit or
+ *                in a draft row that is read, a draft row with no finite logit,
+ *                a teacher_lse that is not finite where the row has a used entry)
+ *   workspace    at least spec_distill_workspace_size(B, gamma, V, K) bytes, as above
+ * Errors: as for spec_teacher_topk; SPEC_ERR_INVALID_ARG for the mode.
+ *
+ * spec_distill_loss_backward -- the gradient with respect to the draft logits,
+ *   grad_out[i, k, v] = grad_loss[i, k] * d loss[i, k] / d z_{i,k,v}
+ * rounded once to `dtype`.  draft_logits, the list, mode and temperature are
+ * those of the forward call, `saved` its output.  Where a TV loss has no
+ * derivative (p = q) that term counts as 0.  Rows that the forward call did not
+ * read, and every row of a request with a status, get zeros.
+ *   grad_loss    [B, gamma] float32
+ *   grad_out     [B, gamma, V] dtype, 16-byte aligned; may be draft_logits
+ *                itself (each logit is read before its gradient is written)
+ * No workspace; one kernel.  Errors: as above.
+ */
+size_t spec_distill_workspace_size(int32_t B, int32_t gamma, int32_t V, int32_t K);
+
+int32_t spec_distill_loss(int32_t B, int32_t gamma, int32_t V, int32_t dtype, const void* draft_logits, int32_t K,
+                          const int32_t* teacher_ids, const float* teacher_values, const float* teacher_lse,
+                          int32_t mode, const int32_t* lengths, const float* temperature, float* loss_out,
+                          double* saved_out, int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
+int32_t spec_distill_loss_backward(int32_t B, int32_t gamma, int32_t V, int32_t dtype, const void* draft_logits,
+                                   int32_t K, const int32_t* teacher_ids, const float* teacher_values, int32_t mode,
+                                   const float* temperature, const double* saved, const float* grad_loss,
+                                   void* grad_out, void* stream);
+
+/*
+ * spec_head_xent -- softmax cross entropy of a vocabulary head against token
+ * labels, in pieces of the vocabulary, without storing the logits:
+ *   z_n = W h_n (fp32 accumulation);  lse_n = ln sum_v exp(z_{n,v});
+ *   loss_n = lse_n - z_{n,label_n}.
+ * The rows are flat: a drafter passes its B * gamma positions, and for a Markov
+ * head (Eq. 5) the rows [h_k ; W1[x_{k-1}]] against [W_head | W2t].
+ *
+ * Arguments (device pointers)
+ *   1 <= N <= SPEC_MAX_HEAD_ROWS, 1 <= V <= SPEC_MAX_V (either dtype),
+ *   1 <= d <= SPEC_MAX_HEAD_WIDTH with d * element size a multiple of 16
+ *   dtype        SPEC_BF16 or SPEC_F32: hidden and weight
+ *   hidden       [N, d], weight [V, d], both 16-byte aligned
+ *   labels       [N] int32; -1 leaves the row out (loss 0, no gradient)
+ * Outputs
+ *   loss_out     [N] float32
+ *   lse_out      [N] float32: spec_head_xent_backward's input (written for every
+ *                row, also those left out)
+ *   status       [N] int32 or NULL, per row: BAD_TOKEN (a label outside [-1, V)),
+ *                NONFINITE (a NaN or +inf logit, or no finite one; not looked at
+ *                when the label is -1); such a row has loss NaN, and lse NaN for
+ *                NONFINITE
+ *   workspace    at least spec_head_xent_workspace_size(N, V, d, dtype) bytes,
+ *                256-byte aligned, owned by the caller, busy until the call's
+ *                kernels finish on `stream`.
+ *
+ * spec_head_xent_backward -- the gradients of sum_n grad_loss_n * loss_n:
+ *   G = (softmax(z) - onehot(label)) * grad_loss (rounded to `dtype`, the type
+ *   of the matrix products; products accumulated in fp32)
+ *   grad_hidden [N, d] = G W and grad_weight [V, d] = G^T H, rounded once to
+ *   `dtype`; either may be NULL.  The logits are formed again, a piece of the
+ *   vocabulary at a time.  A row left out, with a bad label or with an lse that
+ *   is not finite adds nothing to grad_weight and gets a zero row of grad_hidden.
+ *   Results do not depend on scheduling (no atomics).
+ *   grad_loss    [N] float32
+ *   grad_hidden, grad_weight: 16-byte aligned, distinct from the inputs
+ *   workspace    at least spec_head_xent_backward_workspace_size(N, V, d, dtype)
+ * Errors: SPEC_ERR_INVALID_ARG (shape, dtype, alignment, null pointer, both
+ * gradients NULL), SPEC_ERR_WORKSPACE, SPEC_ERR_UNSUPPORTED (a launch past 2^32
+ * work-items).
+ */
+size_t spec_head_xent_workspace_size(int32_t N, int32_t V, int32_t d, int32_t dtype);
+
+int32_t spec_head_xent(int32_t N, int32_t V, int32_t d, int32_t dtype, const void* hidden, const void* weight,
+                       const int32_t* labels, float* loss_out, float* lse_out, int32_t* status, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+size_t spec_head_xent_backward_workspace_size(int32_t N, int32_t V, int32_t d, int32_t dtype);
+
+int32_t spec_head_xent_backward(int32_t N, int32_t V, int32_t d, int32_t dtype, const void* hidden,
+                                const void* weight, const int32_t* labels, const float* lse, const float* grad_loss,
+                                void* grad_hidden, void* grad_weight, void* workspace, size_t workspace_bytes,
+                                void* stream);
 
 /*
  * spec_read_ceiling -- measurement aid, not part of verification: reads

@@ -29,6 +29,8 @@ from the DSpark pages:
   * `sts_fit`, `sts_apply` -- Sequential Temperature Scaling of the
                        confidences (DSpark paper, §3.2.1, post-hoc
                        calibration);
+  * `teacher_topk`, `distill_loss`, `head_xent` -- the drafter's training
+                       losses and their gradients (DSpark paper, §3.3);
   * `philox`        -- the counter-based generator the draws come from
                        (Philox4x64-10, Salmon et al., SC'11).
 
@@ -55,6 +57,7 @@ from .verification import (  # noqa: F401
 from .overlap import overlap_mass  # noqa: F401
 from .drafting import markov_draft, round_bf16  # noqa: F401
 from .calibration import ece, sts_apply, sts_fit  # noqa: F401
+from .training import STATUS_BAD_LIST, distill_loss, head_xent, teacher_topk  # noqa: F401
 from .scheduling import (  # noqa: F401
     capacity,
     survival,

@@ -28,15 +28,15 @@
 namespace spec {
 namespace {
 
+constexpr double kLn2Seg = 0.69314718055994530942;
 constexpr int kFlagBad = 1;    // NaN or +inf outside the list
 constexpr int kFlagTwice = 2;  // a token id named twice
 constexpr int kFlagToken = 4;  // an id outside [-1, V)
 constexpr int kListWords = kSegThreads * kSegVecs * 8 / 32;   // bitmap of a bf16 segment
 
 struct DistillSeg {
-  double sum;     // sum of exp((z - m) / T) over the segment's tokens outside the list
-  float m;        // the largest of their logits
-  int32_t flags;
+  double sum, ref;   // sum of exp(z / T) over the segment's tokens outside the list: sum * 2^ref
+  int32_t flags, pad;
 };
 
 struct DistillArgs {
@@ -65,8 +65,7 @@ void distill_stream_kernel(DistillArgs a) {
   constexpr int EPV = Seg::EPV;
   __shared__ uint32_t bits[kListWords];
   __shared__ uint32_t xbits;
-  __shared__ float sm[kSegWaves];
-  __shared__ double ss[kSegWaves];
+  __shared__ SegSumShared ss;
   __shared__ int sflags;
   const int r = (int)(blockIdx.x / (unsigned)a.nseg), seg = (int)(blockIdx.x - (unsigned)r * a.nseg);
   const int i = r / a.G, k = r - i * a.G;
@@ -104,76 +103,62 @@ void distill_stream_kernel(DistillArgs a) {
   lds_barrier();
   float c_hi, c_lo;
   split_scale(T, c_hi, c_lo);
-  g.mask(d);
   if (tid < g.nx && ((xbits >> tid) & 1u)) x = -INFINITY;
-  float zm = x;
+  RunningSum sum{kNoReference, 0.f, 0};
   const uint8_t* bytes = reinterpret_cast<const uint8_t*>(bits);
-#pragma unroll
-  for (int j = 0; j < kSegVecs; ++j) {
+  // vector j without its listed tokens
+  auto unlisted = [&](uint4 v, int j) -> uint4 {
     const int lv = j * kSegThreads + tid;
     uint32_t w;
     if constexpr (BF16) w = bytes[lv];
     else w = (bytes[lv >> 1] >> ((lv & 1) * 4)) & 15u;
-    if (w) {   // listed tokens leave the vector
+    if (w) {
       if constexpr (BF16) {
-        uint32_t q[4] = {d[j].x, d[j].y, d[j].z, d[j].w};
+        uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           if (w & (1u << (2 * h))) q[h] = (q[h] & 0xffff0000u) | 0xff80u;
           if (w & (2u << (2 * h))) q[h] = (q[h] & 0xffffu) | 0xff800000u;
         }
-        d[j] = make_uint4(q[0], q[1], q[2], q[3]);
+        v = make_uint4(q[0], q[1], q[2], q[3]);
       } else {
-        if (w & 1u) d[j].x = 0xff800000u;
-        if (w & 2u) d[j].y = 0xff800000u;
-        if (w & 4u) d[j].z = 0xff800000u;
-        if (w & 8u) d[j].w = 0xff800000u;
+        if (w & 1u) v.x = 0xff800000u;
+        if (w & 2u) v.y = 0xff800000u;
+        if (w & 4u) v.z = 0xff800000u;
+        if (w & 8u) v.w = 0xff800000u;
       }
     }
-    float z[EPV];
-    Seg::unpack(d[j], z);
-#pragma unroll
-    for (int e = 0; e < EPV; ++e) zm = fmaxf(zm, z[e]);
-  }
-  forget(d);
-  const float wm = wave_max(zm);
-  if (lane == 0) sm[wave] = wm;
-  __syncthreads();
-  float m = sm[0];
-#pragma unroll
-  for (int w = 1; w < kSegWaves; ++w) m = fmaxf(m, sm[w]);
-  const float mr = m > -INFINITY ? m : 0.f;
-  float S = exp_term(x, mr, c_hi, c_lo);
+    return v;
+  };
 #pragma unroll
   for (int j = 0; j < kSegVecs; ++j) {
-    float z[EPV];
-    Seg::unpack(d[j], z);
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < EPV; ++e) s += exp_term(z[e], mr, c_hi, c_lo);
-    S += s;
+    if (g.vb + j * kSegThreads < g.ve) {
+      uint4 v = unlisted(d[j], j);
+      if (g.vb + j * kSegThreads + tid >= g.ve) v = make_uint4(Seg::kNegInf, Seg::kNegInf, Seg::kNegInf, Seg::kNegInf);
+      float z[EPV];
+      Seg::unpack(v, z);
+      add_terms<EPV>(sum, z, c_hi, c_lo);
+    }
+    asm volatile("" : "+v"(sum.S));   // one vector's values at a time: registers
   }
-  if (__ballot(!(S < INFINITY)) && lane == 0) atomicOr(&sflags, kFlagBad);
-  const double ws = wave_sum((double)S);
-  if (lane == 0) ss[wave] = ws;
-  __syncthreads();
-  if (tid == 0) {
-    double s = 0.0;
-#pragma unroll
-    for (int w = 0; w < kSegWaves; ++w) s += ss[w];
-    a.segs[(size_t)r * a.nseg + seg] = DistillSeg{s, mr, sflags | (m < INFINITY ? 0 : kFlagBad)};
+  if (g.nx > 0) {
+    const float z1[1] = {x};
+    add_terms<1>(sum, z1, c_hi, c_lo);
   }
+  int bad;
+  const SegSum t = segment_sum<BF16>(ss, sum, [&](int j) { return unlisted(g.reload(row, j), j); }, x, c_hi, c_lo, bad);
+  if (tid == 0) a.segs[(size_t)r * a.nseg + seg] = DistillSeg{t.sum, t.ref, sflags | (bad ? kFlagBad : 0), 0};
 }
 
 __device__ __forceinline__ double wave_max_d(double x) {
   return wave_reduce(x, [](double p, double q) { return fmax(p, q); });
 }
 
-constexpr int kFinishWaves = 16;
-constexpr int kLaneEntries = SPEC_MAX_TEACHER_K / SPEC_WAVE;
+// Waves of a workgroup at most; entries of a list per lane (one for K <= 64, else four).
+constexpr int finish_waves(int entries) { return entries == 1 ? 16 : 8; }
 
-template <bool BF16>
-__global__ __launch_bounds__(kFinishWaves * SPEC_WAVE) void distill_finish_kernel(DistillArgs a) {
+template <bool BF16, int kLaneEntries>
+__global__ __launch_bounds__(finish_waves(kLaneEntries) * SPEC_WAVE) void distill_finish_kernel(DistillArgs a) {
   __shared__ int sst;
   const int i = (int)blockIdx.x, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int nw = (int)blockDim.x >> 6;
@@ -192,83 +177,80 @@ __global__ __launch_bounds__(kFinishWaves * SPEC_WAVE) void distill_finish_kerne
     bool live = st == 0 && k < L;
     double loss = 0.0;
     if (live) {
+      // every load of the row at once: a lane's entries, and a segment per lane (at most 16)
       const DistillSeg* p = a.segs + r * a.nseg;
       int id[kLaneEntries];
-      double tv[kLaneEntries], zq[kLaneEntries];
-      int rst = 0, any = 0, nused = 0;
-      double tmax = -INFINITY, zmax = -INFINITY;
+      float val[kLaneEntries];
 #pragma unroll
       for (int u = 0; u < kLaneEntries; ++u) {
-        const int e = lane + u * SPEC_WAVE;
-        id[u] = -1;
-        tv[u] = zq[u] = -INFINITY;
-        if (e < K) {
-          const int t = a.ids[r * K + e];
-          const float v = a.values[r * K + e];
-          if (used_entry(t, v)) {
-            any = 1;
-            if (t < 0 || t >= V) {
-              rst |= SPEC_REQ_BAD_TOKEN;
-            } else {
-              const float z = load_elem<BF16>(reinterpret_cast<const char*>(a.draft) +
-                                                  r * (size_t)V * (BF16 ? 2 : 4), t);
-              id[u] = t;
-              ++nused;
-              if (!(v < INFINITY) || !(z < INFINITY)) rst |= SPEC_REQ_NONFINITE;
-              tv[u] = (double)v / Td;
-              zq[u] = (double)z;
-              tmax = fmax(tmax, tv[u]);
-              zmax = fmax(zmax, zq[u]);
-            }
-          }
-        }
+        const int e = min(lane + u * SPEC_WAVE, K - 1);
+        id[u] = a.ids[r * K + e];
+        val[u] = a.values[r * K + e];
+      }
+      const DistillSeg mine = p[min(lane, a.nseg - 1)];
+      const float tl = a.teacher_lse ? a.teacher_lse[r] : 0.f;
+      int rst = 0, any = 0, nused = 0;
+      float zv[kLaneEntries];
+#pragma unroll
+      for (int u = 0; u < kLaneEntries; ++u) {
+        const bool used = lane + u * SPEC_WAVE < K && used_entry(id[u], val[u]);
+        any |= used;
+        if (used && (id[u] < 0 || id[u] >= V)) rst |= SPEC_REQ_BAD_TOKEN;
+        if (!used || id[u] < 0 || id[u] >= V) id[u] = -1;
+        zv[u] = load_elem<BF16>(reinterpret_cast<const char*>(a.draft) + r * (size_t)V * (BF16 ? 2 : 4),
+                                max(id[u], 0));
       }
       live = __ballot(any) != 0;
       if (live) {
-        rst = wave_or_i(rst);
-        nused = wave_sum_i(nused);
+        const double c = kLog2eSeg / Td;   // exponents in powers of two
+        double tv[kLaneEntries], zq[kLaneEntries], tmax = -INFINITY, zmax = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kLaneEntries; ++u) {
+          const bool on = id[u] >= 0;
+          if (on && (!(val[u] < INFINITY) || !(zv[u] < INFINITY))) rst |= SPEC_REQ_NONFINITE;
+          nused += on;
+          tv[u] = on ? (double)val[u] * c : -INFINITY;
+          zq[u] = on ? (double)zv[u] * c : -INFINITY;
+          tmax = fmax(tmax, tv[u]);
+          zmax = fmax(zmax, zq[u]);
+        }
+        const bool seg_on = lane < a.nseg && mine.sum > 0.0;
+        if (lane < a.nseg) {
+          if (mine.flags & kFlagBad) rst |= SPEC_REQ_NONFINITE;
+          if (mine.flags & kFlagToken) rst |= SPEC_REQ_BAD_TOKEN;
+          if (mine.flags & kFlagTwice) rst |= SPEC_REQ_BAD_LIST;
+        }
+        // outside the list: out * 2^mo, lo its log2
+        const double mo = wave_max_d(seg_on ? mine.ref : -INFINITY);
+        const bool outside = mo > -INFINITY;
         tmax = wave_max_d(tmax);
-        zmax = wave_max_d(zmax);
-        int flags = 0;
-        for (int s = 0; s < a.nseg; ++s) {
-          flags |= p[s].flags;
-          if (p[s].sum > 0.0) zmax = fmax(zmax, (double)p[s].m);
-        }
-        if (flags & kFlagBad) rst |= SPEC_REQ_NONFINITE;
-        if (flags & kFlagToken) rst |= SPEC_REQ_BAD_TOKEN;
-        if (flags & kFlagTwice) rst |= SPEC_REQ_BAD_LIST;
+        zmax = fmax(wave_max_d(zmax), mo);
+        nused = wave_sum_i(nused);
         const bool tail = a.teacher_lse != nullptr;
-        double t = 0.0;
-        if (tail) {
-          t = (double)a.teacher_lse[r];
-          if (!(fabs(t) < INFINITY)) rst |= SPEC_REQ_NONFINITE;
-        }
+        if (tail && !(fabsf(tl) < INFINITY)) rst |= SPEC_REQ_NONFINITE;
         if (!(zmax > -INFINITY)) rst |= SPEC_REQ_NONFINITE;
+        rst = wave_or_i(rst);
         if (rst == 0) {
-          // outside the list: mo the largest logit, out = sum exp((z - mo) / T), lo = ln of its sum
-          // against zmax (in logs: the tail may lie hundreds of nats below the list)
-          double mo = -INFINITY, out = 0.0, lsum = 0.0, tsum = 0.0;
-          for (int s = 0; s < a.nseg; ++s)
-            if (p[s].sum > 0.0) mo = fmax(mo, (double)p[s].m);
-          for (int s = 0; s < a.nseg; ++s)
-            if (p[s].sum > 0.0) out += p[s].sum * exp(((double)p[s].m - mo) / Td);
-          const double lout = log(out);
-          const double lo = out > 0.0 ? (mo - zmax) / Td + lout : -INFINITY;
-          double el[kLaneEntries], te[kLaneEntries];
+          const double out = wave_sum(seg_on ? mine.sum * exp2(mine.ref - mo) : 0.0);
+          double el[kLaneEntries], te[kLaneEntries], lsum = 0.0, tsum = 0.0;
 #pragma unroll
           for (int u = 0; u < kLaneEntries; ++u) {
-            el[u] = id[u] >= 0 ? exp((zq[u] - zmax) / Td) : 0.0;
+            el[u] = te[u] = 0.0;
+            if (u * SPEC_WAVE < K) {
+              el[u] = exp2(zq[u] - zmax);
+              te[u] = exp2(tv[u] - tmax);
+            }
             lsum += el[u];
-            te[u] = id[u] >= 0 ? exp(tv[u] - tmax) : 0.0;
             tsum += te[u];
           }
           lsum = wave_sum(lsum);
           tsum = wave_sum(tsum);
-          const double tot = exp(lo) + lsum, lt = log(tot);
-          if (!tail) t = tmax + log(tsum);
-          // te against exp(-(t - tmax)): p_e; the tail is what the list leaves of 1
-          const double ps = exp(tmax - t);
-          const double lrs = lo - lt, rs = exp(lrs);
+          // in logs: the tail may lie hundreds of nats below the list
+          const double lo = outside ? mo - zmax + log2(out) : -INFINITY;
+          const double tot = exp2(lo) + lsum, lt = log2(tot);
+          const double t = tail ? (double)tl * kLog2eSeg : tmax + log2(tsum);   // log2 of p's normaliser
+          const double ps = exp2(tmax - t);
+          const double lrs = lo - lt, rs = exp2(lrs);
           const double rt = (tail && nused < V) ? fmax(0.0, 1.0 - tsum * ps) : 0.0;
           double ars, bv;   // a r_s: q a = (q / r_s) (a r_s) outside the list, finite however small r_s
           double sum = 0.0, qs = 0.0;
@@ -277,7 +259,7 @@ __global__ __launch_bounds__(kFinishWaves * SPEC_WAVE) void distill_finish_kerne
             if (id[u] < 0) continue;
             const double pe = te[u] * ps, qe = el[u] / tot;
             if (a.mode == SPEC_DISTILL_KL) {
-              if (pe > 0.0) sum += pe * ((tv[u] - t) - ((zq[u] - zmax) / Td - lt));
+              if (pe > 0.0) sum += pe * ((tv[u] - t) - (zq[u] - zmax - lt));
             } else if (pe > qe) {
               sum += pe - qe;
               qs += qe;
@@ -287,7 +269,8 @@ __global__ __launch_bounds__(kFinishWaves * SPEC_WAVE) void distill_finish_kerne
           if (a.mode == SPEC_DISTILL_KL) {
             bv = 1.0;
             ars = rs - rt;
-            if (rt > 0.0) loss += rt * (log(rt) - lrs);   // +inf when the draft leaves no mass there
+            if (rt > 0.0) loss += rt * (log2(rt) - lrs);   // +inf when the draft leaves no mass there
+            loss *= kLn2Seg;
           } else {
             const bool up = rt > rs;
             if (up) loss += rt - rs;
@@ -295,12 +278,14 @@ __global__ __launch_bounds__(kFinishWaves * SPEC_WAVE) void distill_finish_kerne
             ars = (bv - (up ? 1.0 : 0.0)) * rs;
           }
           if (lane == 0) {
-            sv[0] = out > 0.0 ? mo : 0.0;
-            sv[1] = out > 0.0 ? lout * kLog2eSeg : 0.0;
-            sv[2] = out > 0.0 ? ars : 0.0;
+            // q / r_s = exp2((z - m) c - sv[1]): the logit nearest the largest exponent as reference
+            const float m = outside ? (float)(mo / c) : 0.f;
+            sv[0] = (double)m;
+            sv[1] = outside ? mo - (double)m * c + log2(out) : 0.0;
+            sv[2] = outside ? ars : 0.0;
             sv[3] = bv;
             sv[4] = t;
-            sv[5] = zmax / Td + lt;
+            sv[5] = zmax + lt;
           }
         } else if (lane == 0) {
           atomicOr(&sst, rst);
@@ -409,7 +394,8 @@ __global__ __launch_bounds__(kSegThreads) void distill_grad_kernel(DistillArgs a
   memory_barrier();   // the segment's stores are done: the listed tokens' go over them
   if (id >= 0) {
     const double Td = (double)T;
-    const double q = exp((double)ze / Td - sv[5]), p = exp((double)val / Td - sv[4]);
+    const double c2 = kLog2eSeg / Td;
+    const double q = exp2((double)ze * c2 - sv[5]), p = exp2((double)val * c2 - sv[4]);
     const double c = a.mode == SPEC_DISTILL_KL ? p : (p > q ? q : 0.0);
     store_elem<BF16>(out, id, (float)(s * (q * sv[3] - c)));
   }
@@ -446,19 +432,22 @@ extern "C" int32_t spec_distill_loss(int32_t B, int32_t gamma, int32_t V, int32_
   a.nseg = row_segments(V, dtype);
   const uint64_t rows = (uint64_t)B * gamma;
   if (rows * a.nseg * kSegThreads > 0xffffffffull) return SPEC_ERR_UNSUPPORTED;
-  const int waves = gamma < kFinishWaves ? gamma : kFinishWaves;
+  const int entries = K <= SPEC_WAVE ? 1 : SPEC_MAX_TEACHER_K / SPEC_WAVE;
+  const int waves = gamma < finish_waves(entries) ? gamma : finish_waves(entries);
   if ((uint64_t)B * waves * SPEC_WAVE > 0xffffffffull) return SPEC_ERR_UNSUPPORTED;
   a.draft = draft_logits; a.ids = teacher_ids; a.values = teacher_values; a.teacher_lse = teacher_lse;
   a.lengths = lengths; a.temperature = temperature; a.loss = loss_out; a.saved = saved_out; a.status = status;
   a.segs = reinterpret_cast<DistillSeg*>(workspace);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const dim3 grid((unsigned)(rows * a.nseg));
+  const dim3 grid((unsigned)(rows * a.nseg)), fgrid((unsigned)B), fblock((unsigned)(waves * SPEC_WAVE));
   if (dtype == SPEC_BF16) {
     hipLaunchKernelGGL(distill_stream_kernel<true>, grid, dim3(kSegThreads), 0, s, a);
-    hipLaunchKernelGGL(distill_finish_kernel<true>, dim3(B), dim3(waves * SPEC_WAVE), 0, s, a);
+    if (entries == 1) hipLaunchKernelGGL((distill_finish_kernel<true, 1>), fgrid, fblock, 0, s, a);
+    else hipLaunchKernelGGL((distill_finish_kernel<true, 4>), fgrid, fblock, 0, s, a);
   } else {
     hipLaunchKernelGGL(distill_stream_kernel<false>, grid, dim3(kSegThreads), 0, s, a);
-    hipLaunchKernelGGL(distill_finish_kernel<false>, dim3(B), dim3(waves * SPEC_WAVE), 0, s, a);
+    if (entries == 1) hipLaunchKernelGGL((distill_finish_kernel<false, 1>), fgrid, fblock, 0, s, a);
+    else hipLaunchKernelGGL((distill_finish_kernel<false, 4>), fgrid, fblock, 0, s, a);
   }
   return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
 }

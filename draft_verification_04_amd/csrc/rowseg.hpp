@@ -63,6 +63,12 @@ struct RowSeg {
     for (int j = 0; j < kSegVecs; ++j)
       if (vb + j * kSegThreads + (int)threadIdx.x >= ve) d[j] = make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
   }
+  // the thread's vector j read once more
+  __device__ __forceinline__ uint4 reload(const char* row, int j) const {
+    const int v = vb + j * kSegThreads + (int)threadIdx.x;
+    return v < ve ? reinterpret_cast<const uint4*>(row + (size_t)head * ES)[v]
+                  : make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
+  }
   __device__ __forceinline__ float load_scalar(const char* row) const {
     return (int)threadIdx.x < nx ? load_elem<BF16>(row, id_of_scalar(threadIdx.x)) : -INFINITY;
   }
@@ -95,11 +101,147 @@ __device__ __forceinline__ void split_scale(float T, float& c_hi, float& c_lo) {
   c_lo = fmaxf((float)(c - (double)c_hi), 1.4e-45f);
 }
 
-// exp2((z - m) c): the difference to the reference first, so that its size, not the logit's, sets
-// the rounding (at most about 2^-24 |z - m| c relative, weighed by e^-|z - m|/T).
+// A thread's running sum of exp(z / T) as S 2^M.  M is an integer that only rises, so a rescale is an
+// exact power of two, and the exponent z c - M is formed with one rounding at its own size:
+// fma(z, c_lo, fma(z, c_hi, -M)).  A vector's sum past 2^32 (NaN included) takes the slow branch: M
+// moves up to the vector's largest exponent.  `odd` is set where that cannot be held (NaN, +inf, or an
+// exponent past 2^22, whose neighbours an fp32 reference no longer tells apart): the segment is then
+// summed again by exp_term.
+struct RunningSum {
+  float M, S;
+  int odd;
+};
+
+constexpr float kWideExponent = 0x1p22f;
+
+template <int N>
+__device__ __forceinline__ float exp_sum(const float (&z)[N], float c_hi, float c_lo, float M) {
+  float e[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) e[j] = __builtin_amdgcn_exp2f(fmaf(z[j], c_lo, fmaf(z[j], c_hi, -M)));
+#pragma unroll
+  for (int w = 1; w < N; w <<= 1)
+#pragma unroll
+    for (int j = 0; j + w < N; j += 2 * w) e[j] += e[j + w];
+  return e[0];
+}
+
+template <int N>
+__device__ __forceinline__ void add_terms(RunningSum& r, const float (&z)[N], float c_hi, float c_lo) {
+  float s = exp_sum<N>(z, c_hi, c_lo, r.M);
+  if (!(s <= 0x1p32f)) {
+    float vm = z[0];
+#pragma unroll
+    for (int j = 1; j < N; ++j) vm = fmaxf(vm, z[j]);
+    const float mc = ceilf(vm * c_hi);
+    s = 0.f;
+    if (!(fabsf(mc) < kWideExponent)) {
+      r.odd = 1;
+    } else {
+      if (mc > r.M) {
+        const float d = r.M - mc;
+        r.S = d < -126.f ? 0.f : ldexpf(r.S, (int)d);
+        r.M = mc;
+      }
+      s = exp_sum<N>(z, c_hi, c_lo, r.M);
+      if (!(s <= 0x1p32f)) {   // a NaN beside finite values
+        r.odd = 1;
+        s = 0.f;
+      }
+    }
+  }
+  r.S += s;
+}
+
+constexpr float kNoReference = -0x1p24f;   // below every exponent that is summed: the first term raises it
+
+// exp2((z - m) c) against the segment's largest value m: the difference first, so that it, not the
+// value, sets the rounding, whatever the values' size.
 __device__ __forceinline__ float exp_term(float z, float m, float c_hi, float c_lo) {
   const float dz = z - m;
   return __builtin_amdgcn_exp2f(fmaf(dz, c_lo, dz * c_hi));
+}
+
+// A segment's sum of exp(z / T): sum * 2^ref, fp64.
+struct SegSum {
+  double sum, ref;
+};
+
+// Scratch of segment_sum.
+struct SegSumShared {
+  double s[kSegWaves];
+  float m[kSegWaves];
+  int odd[kSegWaves];
+};
+
+// The workgroup's sum (and whether a NaN or +inf was among the values) from its threads' running sums;
+// every thread gets the result.  again(j) reads the thread's vector j once more (-inf where there is
+// none) and x is its scalar: used only when a sum was odd.
+template <bool BF16, class Again>
+__device__ __forceinline__ SegSum segment_sum(SegSumShared& sh, const RunningSum& r, Again again, float x, float c_hi,
+                                              float c_lo, int& bad) {
+  using Seg = RowSeg<BF16>;
+  const int wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
+  const float wm = wave_max(r.M);
+  const double ws = wave_sum(ldexp((double)r.S, (int)fmaxf(r.M - wm, -2000.f)));
+  const int wo = __ballot(r.odd) != 0;
+  if (lane == 0) {
+    sh.s[wave] = ws;
+    sh.m[wave] = wm;
+    sh.odd[wave] = wo;
+  }
+  __syncthreads();
+  float M = sh.m[0];
+  int odd = sh.odd[0];
+#pragma unroll
+  for (int w = 1; w < kSegWaves; ++w) {
+    M = fmaxf(M, sh.m[w]);
+    odd |= sh.odd[w];
+  }
+  SegSum t{0.0, (double)M};
+  bad = 0;
+  // no term raised the reference: every value is -inf or lies below it (rows of a type's lowest value)
+  odd |= M == kNoReference;
+  if (!odd) {
+#pragma unroll
+    for (int w = 0; w < kSegWaves; ++w) t.sum += ldexp(sh.s[w], (int)fmaxf(sh.m[w] - M, -2000.f));
+    return t;
+  }
+  __syncthreads();
+  float m = x;
+#pragma unroll 1
+  for (int j = 0; j < kSegVecs; ++j) {
+    float z[Seg::EPV];
+    Seg::unpack(again(j), z);
+#pragma unroll
+    for (int e = 0; e < Seg::EPV; ++e) m = fmaxf(m, z[e]);
+  }
+  m = wave_max(m);
+  if (lane == 0) sh.m[wave] = m;
+  __syncthreads();
+  for (int w = 0; w < kSegWaves; ++w) m = fmaxf(m, sh.m[w]);
+  const float mr = m > -INFINITY ? m : 0.f;
+  float S = exp_term(x, mr, c_hi, c_lo);
+#pragma unroll 1
+  for (int j = 0; j < kSegVecs; ++j) {
+    float z[Seg::EPV];
+    Seg::unpack(again(j), z);
+#pragma unroll
+    for (int e = 0; e < Seg::EPV; ++e) S += exp_term(z[e], mr, c_hi, c_lo);
+  }
+  const int wb = __ballot(!(S < INFINITY) || !(m < INFINITY)) != 0;
+  const double s2 = wave_sum((double)S);
+  if (lane == 0) {
+    sh.s[wave] = s2;
+    sh.odd[wave] = wb;
+  }
+  __syncthreads();
+  for (int w = 0; w < kSegWaves; ++w) {
+    t.sum += sh.s[w];
+    bad |= sh.odd[w];
+  }
+  t.ref = (double)mr * ((double)c_hi + (double)c_lo);
+  return t;
 }
 
 // Order-preserving 32-bit key of a float (larger float -> larger key).

@@ -8,10 +8,10 @@
 //       smallest of these over the waves is a bound tau that at least K values of the segment reach,
 //       so the values >= tau hold the segment's K largest.  They go to the workspace as 64-bit keys
 //       (ordered value, complemented id); when more than `cap` reach tau (ties, mostly) the exact
-//       K-th key is found by bisection, reading the segment again (from cache), instead.  exp2 of the values against the
-//       segment's maximum is summed in fp32 per thread (64 terms) and in fp64 beyond.
-//   teacher_merge_kernel -- one workgroup per row drops the keys below the largest tau, sorts the
-//       rest in LDS (bitonic) and writes the first K, the log normaliser and the status.
+//       K-th key is found by bisection, reading the segment again (from cache), instead.  The terms
+//       exp(z / T) are summed in fp32 per thread (64 terms) and in fp64 beyond.
+//   teacher_merge_kernel -- one wave per row drops the keys below the largest tau, keeps the K largest
+//       of the rest in order, and writes them, the log normaliser and the status.
 #include "common.hpp"
 #include "rowseg.hpp"
 #include "spec_verify.h"
@@ -19,16 +19,15 @@
 namespace spec {
 namespace {
 
-constexpr int kMergeThreads = 256;
-constexpr int kHitCap = 2 * SPEC_MAX_TEACHER_K + 96;   // >= list_cap
-constexpr int kMergeKeys = 8192;   // keys a merge workgroup holds at most (64 KB of LDS)
+constexpr int kHitCap = 3 * SPEC_MAX_TEACHER_K + 96;
+constexpr int kMergeWaves = 4;      // rows per workgroup of the merge
+constexpr int kMergeRegs = 32;      // keys of the lists a lane of it holds at most
 
 struct TeacherSeg {
-  double sum;     // sum of exp((z - m) / T) over the segment
-  float m;        // its largest logit
-  int32_t bad;    // NaN or +inf seen
-  uint32_t tau;   // key that at least K of the segment's values reach (that of -inf: no bound)
-  int32_t n;      // keys listed
+  double sum, ref;  // sum of exp(z / T) over the segment: sum * 2^ref
+  int32_t bad;      // NaN or +inf seen
+  uint32_t tau;     // key that at least K of the segment's values reach (that of -inf: no bound)
+  int32_t n, pad;   // keys listed
 };
 
 struct TeacherArgs {
@@ -49,9 +48,7 @@ __device__ __forceinline__ uint64_t pack_key(float z, int id) {
 }
 
 struct SegShared {
-  float m[kSegWaves];
-  double s[kSegWaves];
-  int bad[kSegWaves];
+  SegSumShared sum;
   uint32_t t[kSegWaves];
   int cnt[2][kSegWaves];
   int n, nhit;
@@ -74,23 +71,34 @@ void teacher_segment_kernel(TeacherArgs a) {
   const Seg g(row, a.V, seg, a.nseg);
   uint4 d[kSegVecs];
   g.load(row, d);
-  float x = g.load_scalar(row);
-  g.mask(d);
+  const float x = g.load_scalar(row);
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   if (tid == 0) sh.n = sh.nhit = 0;
   float c_hi, c_lo;
   split_scale(T, c_hi, c_lo);
 
-  float zm = x;
+  RunningSum sum{kNoReference, 0.f, 0};
+  float vm[kSegVecs], zm = x;   // the vectors' largest values
 #pragma unroll
   for (int j = 0; j < kSegVecs; ++j) {
-    float z[EPV];
-    Seg::unpack(d[j], z);
+    vm[j] = -INFINITY;
+    if (g.vb + j * kSegThreads < g.ve) {
+      uint4 v = d[j];
+      if (g.vb + j * kSegThreads + tid >= g.ve) v = make_uint4(Seg::kNegInf, Seg::kNegInf, Seg::kNegInf, Seg::kNegInf);
+      float z[EPV];
+      Seg::unpack(v, z);
+      add_terms<EPV>(sum, z, c_hi, c_lo);
+      vm[j] = z[0];
 #pragma unroll
-    for (int e = 0; e < EPV; ++e) zm = fmaxf(zm, z[e]);
-    asm volatile("" : "+v"(zm));
+      for (int e = 1; e < EPV; ++e) vm[j] = fmaxf(vm[j], z[e]);
+      zm = fmaxf(zm, vm[j]);
+    }
+    asm volatile("" : "+v"(sum.S), "+v"(vm[j]));   // one vector's values at a time: registers
   }
-  forget(d);
+  if (g.nx > 0) {
+    const float z1[1] = {x};
+    add_terms<1>(sum, z1, c_hi, c_lo);
+  }
   // the wave's ceil(K / W)-th largest lane maximum, over the W waves whose lanes all hold a vector
   // (bitwise from the top; bf16 keys end at bit 16)
   const uint32_t key = order_key(zm);
@@ -105,36 +113,16 @@ void teacher_segment_kernel(TeacherArgs a) {
     }
     if (BF16 && t < 0x80000000u) t |= 0xffffu;
   }
-  const float wm = wave_max(zm);
-  if (lane == 0) {
-    sh.m[wave] = wm;
-    sh.t[wave] = t;
-  }
+  if (lane == 0) sh.t[wave] = t;
   __syncthreads();
-  float m = sh.m[0];
   uint32_t tau = sh.t[0];
 #pragma unroll
-  for (int w = 1; w < kSegWaves; ++w) {
-    m = fmaxf(m, sh.m[w]);
-    tau = min(tau, sh.t[w]);
-  }
+  for (int w = 1; w < kSegWaves; ++w) tau = min(tau, sh.t[w]);
   const size_t slot0 = ((size_t)r * a.nseg + seg) * a.cap;
   const float tz = key_value(tau);
-  float S = 0.f;
-  const float mr = m > -INFINITY ? m : 0.f;   // an empty segment sums to 0
 #pragma unroll
   for (int j = 0; j < kSegVecs; ++j) {
-    float z[EPV];
-    Seg::unpack(d[j], z);
-    float s = 0.f, vm = z[0];
-#pragma unroll
-    for (int e = 0; e < EPV; ++e) {
-      s += exp_term(z[e], mr, c_hi, c_lo);
-      vm = fmaxf(vm, z[e]);
-    }
-    S += s;
-    asm volatile("" : "+v"(S));   // one vector's values at a time: registers
-    if (vm >= tz && vm > -INFINITY) {   // copied whole; its values are looked at one by one below
+    if (vm[j] >= tz && vm[j] > -INFINITY) {   // copied whole; its values are looked at one by one below
       const int h = atomicAdd(&sh.nhit, 1);
       if (h < kHitCap) {
         sh.hit[h] = d[j];
@@ -142,15 +130,8 @@ void teacher_segment_kernel(TeacherArgs a) {
       }
     }
   }
-  S += exp_term(x, mr, c_hi, c_lo);
-  const int bad = !(S < INFINITY) || !(m < INFINITY);
-  const double ws = wave_sum((double)S);
-  const int wb = wave_or_i(bad);
-  if (lane == 0) {
-    sh.s[wave] = ws;
-    sh.bad[wave] = wb;
-  }
-  __syncthreads();
+  int bad;
+  const SegSum total = segment_sum<BF16>(sh.sum, sum, [&](int j) { return g.reload(row, j); }, x, c_hi, c_lo, bad);
   const int nhit = sh.nhit;
   auto list = [&](float z, int id) {
     if (z >= tz && z > -INFINITY) {
@@ -225,121 +206,194 @@ void teacher_segment_kernel(TeacherArgs a) {
     n = min(sh.n, a.cap);
     tau = th;
   }
-  if (tid == 0) {
-    double s = 0.0;
-    int b = 0;
-#pragma unroll
-    for (int w = 0; w < kSegWaves; ++w) {
-      s += sh.s[w];
-      b |= sh.bad[w];
-    }
-    a.segs[(size_t)r * a.nseg + seg] = TeacherSeg{s, mr, b, tau, n};
-  }
+  if (tid == 0) a.segs[(size_t)r * a.nseg + seg] = TeacherSeg{total.sum, total.ref, bad, tau, n, 0};
 }
 
-__global__ __launch_bounds__(kMergeThreads) void teacher_merge_kernel(TeacherArgs a) {
-  extern __shared__ __attribute__((aligned(16))) uint64_t keys[];
-  __shared__ int sbad, sn;
-  const int r = (int)blockIdx.x, i = r / a.G, k = r - i * a.G, tid = threadIdx.x;
+__device__ __forceinline__ double wave_max_d(double x) {
+  return wave_reduce(x, [](double p, double q) { return fmax(p, q); });
+}
+
+// One wave per row.  The keys kept so far and as many segments' lists as fit are held in registers; the K-th largest value is found bit by bit, of the values equal
+// to it the lowest ids, and the survivors go to LDS.  In the end every key's place is the number of
+// larger ones.
+__global__ __launch_bounds__(kMergeWaves * SPEC_WAVE) void teacher_merge_kernel(TeacherArgs a, int key_bits) {
+  __shared__ uint64_t kept[kMergeWaves][SPEC_MAX_TEACHER_K];
+  const int wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
+  const long long row = (long long)blockIdx.x * kMergeWaves + wave;
+  if (row >= (long long)a.B * a.G) return;
+  const int r = (int)row, i = r / a.G, k = r - i * a.G, K = a.K;
   const int L = a.lengths ? a.lengths[i] : a.G;
   const float T = a.temperature[i];
-  const size_t o = (size_t)r * a.K;
+  const size_t o = (size_t)r * K;
+  const TeacherSeg* p = a.segs + (size_t)r * a.nseg;
   int st = 0;
-  if (L < 0 || L > a.G) {
-    st = SPEC_REQ_BAD_LENGTH;
-  } else {
-    if (!(T > 0.f && T < INFINITY)) st |= SPEC_REQ_BAD_TEMPERATURE;
-    if (st == 0) {
-      // every row of the request: a bad or an empty one marks the request
-      if (tid == 0) sbad = sn = 0;
-      __syncthreads();
-      if (tid < L) {
-        const TeacherSeg* p = a.segs + ((size_t)i * a.G + tid) * a.nseg;
-        int bad = 0, some = 0;
-        for (int s = 0; s < a.nseg; ++s) {
-          bad |= p[s].bad;
-          some |= p[s].sum > 0.0;
-        }
-        if (bad || !some) sbad = 1;
-      }
-      __syncthreads();
-      if (sbad) st |= SPEC_REQ_NONFINITE;
+  if (L < 0 || L > a.G) st = SPEC_REQ_BAD_LENGTH;
+  else if (!(T > 0.f && T < INFINITY)) st = SPEC_REQ_BAD_TEMPERATURE;
+  if (st == 0 && L > 0) {
+    // every row of the request: a bad or an empty one marks the request
+    const TeacherSeg* q = a.segs + ((size_t)i * a.G + min(lane, L - 1)) * a.nseg;
+    int bad = 0, some = 0;
+    for (int s = 0; s < a.nseg; ++s) {
+      bad |= q[s].bad;
+      some |= q[s].sum > 0.0;
     }
+    if (__ballot(bad || !some)) st = SPEC_REQ_NONFINITE;
   }
-  if (a.status && k == 0 && tid == 0) a.status[i] = st;
+  if (a.status && k == 0 && lane == 0) a.status[i] = st;
   if (st != 0 || k >= L) {
     const float fill = st != 0 ? NAN : -INFINITY;
-    for (int e = tid; e < a.K; e += kMergeThreads) {
+    for (int e = lane; e < K; e += SPEC_WAVE) {
       a.ids[o + e] = -1;
       a.values[o + e] = fill;
     }
-    if (a.lse && tid == 0) a.lse[r] = fill;
+    if (a.lse && lane == 0) a.lse[r] = fill;
     return;
   }
-  const TeacherSeg* p = a.segs + (size_t)r * a.nseg;
-  uint32_t tau = kNegInfKey;
-  for (int s = 0; s < a.nseg; ++s) tau = max(tau, p[s].tau);
-  for (int s = 0; s < a.nseg; ++s) {
-    const uint64_t* src = a.keys + ((size_t)r * a.nseg + s) * a.cap;
-    for (int e = tid; e < p[s].n; e += kMergeThreads) {
-      const uint64_t key = src[e];
-      if ((uint32_t)(key >> 32) >= tau) keys[atomicAdd(&sn, 1)] = key;
+  const TeacherSeg mine = p[min(lane, a.nseg - 1)];   // nseg <= 16
+  const bool on = lane < a.nseg;
+  const uint32_t tau = (uint32_t)wave_max_i(on ? (int)(mine.tau ^ 0x80000000u) : INT32_MIN) ^ 0x80000000u;
+  uint64_t* list = kept[wave];
+  int cur = 0, s0 = 0;
+  constexpr int KR = SPEC_MAX_TEACHER_K / SPEC_WAVE;   // registers of the keys kept so far
+  while (s0 < a.nseg) {
+    // a round: registers 0 .. KR - 1 hold the kept keys, each further one 64 keys of one segment's list
+    uint32_t hi[KR + kMergeRegs], lo[KR + kMergeRegs];
+#pragma unroll
+    for (int u = 0; u < KR; ++u) {
+      const uint64_t key = lane + u * SPEC_WAVE < cur ? list[lane + u * SPEC_WAVE] : 0;
+      hi[u] = (uint32_t)(key >> 32);
+      lo[u] = (uint32_t)key;
     }
-  }
-  __syncthreads();
-  const int n = sn;
-  int N = 2;
-  while (N < n) N <<= 1;
-  for (int e = n + tid; e < N; e += kMergeThreads) keys[e] = 0;
-  __syncthreads();
-  for (int size = 2; size <= N; size <<= 1) {
-    for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      for (int e = tid; e < N / 2; e += kMergeThreads) {
-        const int lo = 2 * e - (e & (stride - 1)), hi = lo + stride;
-        const uint64_t x = keys[lo], y = keys[hi];
-        const bool desc = (lo & size) == 0;
-        if ((x < y) == desc) {
-          keys[lo] = y;
-          keys[hi] = x;
+    int used = 0, s1 = s0;
+    while (s1 < a.nseg) {
+      const int n = max(1, (read_lane(mine.n, s1) + SPEC_WAVE - 1) / SPEC_WAVE);   // an empty one takes a register too
+      if (used + n > kMergeRegs) break;
+      used += n;
+      ++s1;
+    }
+    int s = s0, off = 0;
+#pragma unroll
+    for (int g = 0; g < kMergeRegs; g += 8) {
+      if (g < used) {   // eight loads at once, clamped in bounds
+        uint64_t key[8];
+        bool in[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int sc = min(s, s1 - 1), n = read_lane(mine.n, sc), e = off + lane;
+          in[u] = s < s1 && e < n;
+          key[u] = a.keys[((size_t)r * a.nseg + sc) * a.cap + min(e, a.cap - 1)];
+          off += SPEC_WAVE;
+          if (off >= n) {
+            off = 0;
+            ++s;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const bool take = in[u] && (uint32_t)(key[u] >> 32) >= tau;
+          hi[KR + g + u] = take ? (uint32_t)(key[u] >> 32) : 0;
+          lo[KR + g + u] = (uint32_t)key[u];
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) hi[KR + g + u] = lo[KR + g + u] = 0;
+      }
+    }
+    auto count = [&](auto pred) -> int {
+      int c = 0;
+      if (cur > 0) {
+#pragma unroll
+        for (int u = 0; u < KR; ++u) c += (int)__popcll(__ballot(pred(hi[u], lo[u])));
+      }
+#pragma unroll
+      for (int g = 0; g < kMergeRegs; g += 8)
+        if (g < used) {
+#pragma unroll
+          for (int u = KR + g; u < KR + g + 8; ++u) c += (int)__popcll(__ballot(pred(hi[u], lo[u])));
+        }
+      return c;
+    };
+    uint32_t th = 0;   // the largest value key that at least K keys reach (0: fewer than K keys)
+#pragma unroll 1
+    for (int bit = 31; bit >= 32 - key_bits; --bit) {
+      const uint32_t trial = th | (1u << bit);
+      if (count([&](uint32_t h, uint32_t) { return h >= trial; }) >= K) th = trial;
+    }
+    uint32_t tl = 0;   // of the keys at th, the largest low words (lowest ids) that fill up K
+    // bf16 keys of negative values end in 16 ones: th stands for them with zeros there
+    const uint32_t top = th | (key_bits < 32 ? 0xffffu : 0u);
+    if (th > 0) {
+      const int above = count([&](uint32_t h, uint32_t) { return h > top; });
+      if (count([&](uint32_t h, uint32_t) { return h >= th; }) > K) {
+        tl = 0xfff00000u;
+#pragma unroll 1
+        for (int bit = 19; bit >= 0; --bit) {
+          const uint32_t trial = tl | (1u << bit);
+          if (count([&](uint32_t h, uint32_t l) { return h >= th && h <= top && l >= trial; }) >= K - above) tl = trial;
         }
       }
-      __syncthreads();
+    }
+    int kept_n = 0;
+#pragma unroll
+    for (int u = 0; u < KR + kMergeRegs; ++u) {
+      if (u < KR ? cur > 0 : u - KR < used) {
+        const bool take = hi[u] > 0 && (hi[u] > top || (hi[u] >= th && lo[u] >= tl));
+        const unsigned long long m = __ballot(take);
+        const int e = kept_n + (int)__popcll(m & ((1ull << lane) - 1));
+        if (take && e < SPEC_MAX_TEACHER_K) list[e] = ((uint64_t)hi[u] << 32) | lo[u];
+        kept_n += (int)__popcll(m);
+      }
+    }
+    cur = min(kept_n, K);
+    s0 = s1;
+  }
+  uint64_t key[SPEC_MAX_TEACHER_K / SPEC_WAVE];
+  int place[SPEC_MAX_TEACHER_K / SPEC_WAVE];
+#pragma unroll
+  for (int u = 0; u < SPEC_MAX_TEACHER_K / SPEC_WAVE; ++u) {
+    key[u] = lane + u * SPEC_WAVE < cur ? list[lane + u * SPEC_WAVE] : 0;
+    place[u] = 0;
+  }
+  if (cur <= SPEC_WAVE) {
+#pragma unroll 8
+    for (int e = 0; e < cur; ++e) place[0] += list[e] > key[0] ? 1 : 0;
+  } else {
+#pragma unroll 4
+    for (int e = 0; e < cur; ++e) {
+      const uint64_t x = list[e];
+#pragma unroll
+      for (int u = 0; u < SPEC_MAX_TEACHER_K / SPEC_WAVE; ++u) place[u] += x > key[u] ? 1 : 0;
     }
   }
-  for (int e = tid; e < a.K; e += kMergeThreads) {
-    const bool on = e < n;
-    const uint64_t key = on ? keys[e] : 0;
-    a.ids[o + e] = on ? (int)~(uint32_t)key : -1;
-    a.values[o + e] = on ? key_value((uint32_t)(key >> 32)) : -INFINITY;
+#pragma unroll
+  for (int u = 0; u < SPEC_MAX_TEACHER_K / SPEC_WAVE; ++u) {
+    const int e = lane + u * SPEC_WAVE;
+    if (e < cur) {
+      a.ids[o + place[u]] = (int)~(uint32_t)key[u];
+      a.values[o + place[u]] = key_value((uint32_t)(key[u] >> 32));
+    } else if (e < K) {
+      a.ids[o + e] = -1;
+      a.values[o + e] = -INFINITY;
+    }
   }
-  if (a.lse && tid == 0) {
-    float m = -INFINITY;
-    for (int s = 0; s < a.nseg; ++s)
-      if (p[s].sum > 0.0) m = fmaxf(m, p[s].m);
-    double S = 0.0;
-    for (int s = 0; s < a.nseg; ++s)
-      if (p[s].sum > 0.0) S += p[s].sum * exp(((double)p[s].m - (double)m) / (double)T);
-    a.lse[r] = (float)((double)m / (double)T + log(S));
+  if (a.lse) {
+    const bool some = on && mine.sum > 0.0;
+    const double ref = wave_max_d(some ? mine.ref : -INFINITY);
+    const double S = wave_sum(some ? mine.sum * exp2(mine.ref - ref) : 0.0);
+    if (lane == 0) a.lse[r] = (float)(0.69314718055994530942 * (ref + log2(S)));
   }
 }
 
-// Keys a segment may list: about K reach tau, rarely 2 K + 96; rows of one segment may have no full
-// wave to take tau from (at most 64 vectors and 14 scalars, all listed then).
-int list_cap(int K, int nseg) {
-  const int c = 2 * K + 96 + (nseg == 1 ? 512 : 0), most = kMergeKeys / nseg;
-  return c < most ? c : most;   // nseg <= 16: at least 512 >= 2 K
-}
+// Keys a segment may list: 22 (K = 1) to 460 (K = 256) reach tau on Gaussian rows, 700 at most seen of
+// 160 segments; rows of one segment may have no full wave to take tau from (at most 64 vectors and 14
+// scalars, all listed then).
+int list_cap(int K, int nseg) { return 3 * K + 96 + (nseg == 1 ? 512 : 0); }
+static_assert(3 * SPEC_MAX_TEACHER_K + 96 + 512 <= SPEC_WAVE * kMergeRegs, "a segment's list fits a round");
 
 size_t workspace_of(size_t rows, int V, int K, int dtype) {
   const int nseg = row_segments(V, dtype);
   return round256(rows * nseg * sizeof(TeacherSeg)) +
          round256(rows * nseg * (size_t)list_cap(K, nseg) * sizeof(uint64_t));
-}
-
-int pow2_at_least(int n) {
-  int p = 2;
-  while (p < n) p <<= 1;
-  return p;
 }
 
 }  // namespace
@@ -380,7 +434,7 @@ extern "C" int32_t spec_teacher_topk(int32_t B, int32_t gamma, int32_t V, int32_
     hipLaunchKernelGGL(teacher_segment_kernel<true>, grid, dim3(kSegThreads), 0, s, a);
   else
     hipLaunchKernelGGL(teacher_segment_kernel<false>, grid, dim3(kSegThreads), 0, s, a);
-  const unsigned lds = (unsigned)(pow2_at_least(a.nseg * a.cap) * sizeof(uint64_t));
-  hipLaunchKernelGGL(teacher_merge_kernel, dim3((unsigned)rows), dim3(kMergeThreads), lds, s, a);
+  hipLaunchKernelGGL(teacher_merge_kernel, dim3((unsigned)((rows + kMergeWaves - 1) / kMergeWaves)),
+                     dim3(kMergeWaves * SPEC_WAVE), 0, s, a, dtype == SPEC_BF16 ? 16 : 32);
   return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
 }

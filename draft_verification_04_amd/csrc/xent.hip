@@ -48,13 +48,13 @@ struct GemmArgs {
   const char* B;     // [rowsB] rows ldb bytes apart
   size_t lda, ldb;
   int rowsA, rowsB;
-  int kbytes;        // of a row (a multiple of 16); split i of `splits` takes ksplit bytes of it
-  int ksplit, splits;
+  int kbytes;        // of a row (a multiple of 16)
   int ti, tj;        // tiles
+  int whole, parts;  // tiles taken by one workgroup each; the rest by `parts` workgroups each (kAcc)
   // kStats, kGradZ
   const int32_t* labels;
   int v0;            // vocabulary index of A's first row
-  float2* part;      // [strips, rowsB] (largest logit, sum of exp against it)
+  float2* part;      // [strips, rowsB] (largest logit, sum of exp against it), from A's first strip
   float* zlab;       // [rowsB]
   const float* lse;
   const float* grad_loss;
@@ -64,7 +64,8 @@ struct GemmArgs {
   size_t ldgn, ldgt;
   int vpad, npad;    // columns of gn and gt that are written (zeros past the valid ones)
   // kAcc, kStore
-  float* acc;        // [splits, rowsB, rowsA]
+  float* acc;        // [rowsB, rowsA]: whole tiles and the first part of the others
+  float* acc_parts;  // [rest tiles, parts - 1, tile]: their further parts
   int accumulate;
   char* out;         // [rowsB, ldo bytes]
   size_t ldo;
@@ -90,6 +91,17 @@ __device__ __forceinline__ void wait_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// Scheduling of a half step: R LDS reads spread over its M matrix instructions.
+template <int R, int M>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, M / R > 0 ? M / R : 1, 0);   // matrix instructions
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                       // then an LDS read
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, M % R, 0);
+}
+
 // A row takes part in the gradient: a label in range and a finite normaliser.
 __device__ __forceinline__ bool live_row(int label, float lse, int V) {
   return label >= 0 && label < V && fabsf(lse) < INFINITY;
@@ -113,14 +125,21 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
   const int wi = wave % WM, wj = wave / WM;
   const int l16 = lane & 15, q = lane >> 4;
 
-  int tile = xcd_tile((int)blockIdx.x, g.ti * g.tj * g.splits);
-  const int split = tile / (g.ti * g.tj);
-  tile -= split * (g.ti * g.tj);
+  int tile, part = 0, steps = (g.kbytes + kStepBytes - 1) / kStepBytes, step0 = 0;
+  if ((int)blockIdx.x < g.whole) {
+    tile = xcd_tile((int)blockIdx.x, g.whole);
+  } else {
+    const int u = (int)blockIdx.x - g.whole;
+    tile = g.whole + u / g.parts;
+    part = u % g.parts;
+    step0 = (int)((long long)steps * part / g.parts);
+    steps = (int)((long long)steps * (part + 1) / g.parts);
+  }
   const int band = tile / (8 * g.ti), in = tile - band * 8 * g.ti;
   const int bw = min(8, g.tj - band * 8);
   const int i0 = in / bw * BM, j0 = (band * 8 + in % bw) * BN;
 
-  const int kb = split * g.ksplit, kbytes = max(0, min(g.ksplit, g.kbytes - kb));   // a last split may be empty
+  const int kb = step0 * kStepBytes, kbytes = min(steps * kStepBytes, g.kbytes) - kb;
   const int full = kbytes / kStepBytes, rem = kbytes - full * kStepBytes;
   const int nk = full + (rem > 0);
   const char* A = g.A + (size_t)i0 * g.lda + kb;
@@ -135,56 +154,90 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
 #pragma unroll
   for (int u = 0; u < CB; ++u) vb[u] = (uint32_t)min((u * NW + wave) * 8 + lr, g.rowsB - 1 - j0) * (uint32_t)g.ldb + lc;
 
-  auto issue = [&](int t) {
+  auto issue_whole = [&](int t) {   // a step of 128 bytes
     char* dst = lds + (t % ST) * STAGE + wave * 1024;
+    // scalar base + 32-bit lane offset (the compiler would otherwise keep 64-bit lane pointers in registers)
+    size_t off = (size_t)t * kStepBytes;
+    asm("" : "+s"(off));
+    const char* a = A + off;
+    const char* b = B + off;
+#pragma unroll
+    for (int u = 0; u < CA; ++u)
+      __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(a + va[u]), (SPEC_LDS void*)(dst + u * NW * 1024), 16,
+                                       0, 0);
+#pragma unroll
+    for (int u = 0; u < CB; ++u)
+      __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(b + vb[u]),
+                                       (SPEC_LDS void*)(dst + BM * kStepBytes + u * NW * 1024), 16, 0, 0);
+  };
+  auto issue_rest = [&](int t) {   // the last step of a row that is no multiple of 128 bytes: zeros behind its end
+    char* dst = lds + (t % ST) * STAGE + wave * 1024 + lane * 16;
     const char* a = A + (size_t)t * kStepBytes;
     const char* b = B + (size_t)t * kStepBytes;
-    if (t < full) {
+    const v4u32 zero = {};
 #pragma unroll
-      for (int u = 0; u < CA; ++u)
-        __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(a + va[u]), (SPEC_LDS void*)(dst + u * NW * 1024), 16,
-                                         0, 0);
+    for (int u = 0; u < CA; ++u)
+      *reinterpret_cast<v4u32*>(dst + u * NW * 1024) = lc < rem ? *reinterpret_cast<const v4u32*>(a + va[u]) : zero;
 #pragma unroll
-      for (int u = 0; u < CB; ++u)
-        __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(b + vb[u]),
-                                         (SPEC_LDS void*)(dst + BM * kStepBytes + u * NW * 1024), 16, 0, 0);
-    } else {   // the last step of a row that is no multiple of 128 bytes: zeros behind its end
-      const bool on = lc < rem;
-      const v4u32 zero = {};
-#pragma unroll
-      for (int u = 0; u < CA; ++u)
-        *reinterpret_cast<v4u32*>(dst + u * NW * 1024 + lane * 16) =
-            on ? *reinterpret_cast<const v4u32*>(a + va[u]) : zero;
-#pragma unroll
-      for (int u = 0; u < CB; ++u)
-        *reinterpret_cast<v4u32*>(dst + BM * kStepBytes + u * NW * 1024 + lane * 16) =
-            on ? *reinterpret_cast<const v4u32*>(b + vb[u]) : zero;
-    }
+    for (int u = 0; u < CB; ++u)
+      *reinterpret_cast<v4u32*>(dst + BM * kStepBytes + u * NW * 1024) =
+          lc < rem ? *reinterpret_cast<const v4u32*>(b + vb[u]) : zero;
+  };
+  auto issue = [&](int t) {
+    if (t < full) issue_whole(t);
+    else if (t < nk) issue_rest(t);
   };
 
   f32x4 c[MT][NT] = {};
   const int ra = (wi * MT * 16 + l16) * kStepBytes, rb = BM * kStepBytes + (wj * NT * 16 + l16) * kStepBytes;
+  struct Frag {
+    v4u32 a[MT], b[NT];
+  };
+  auto fetch = [&](Frag& f, int t, int kk) {
+    const char* src = lds + (t % ST) * STAGE + ((kk * 4 + q) ^ (lane & 7)) * 16;
 #pragma unroll
-  for (int t = 0; t < ST - 1; ++t)
-    if (t < nk) issue(t);
-  for (int t = 0; t < nk; ++t) {
-    if (t + ST - 1 <= nk) wait_barrier<(ST - 2) * (CA + CB)>();
+    for (int m = 0; m < MT; ++m) f.a[m] = *reinterpret_cast<const v4u32*>(src + ra + m * 16 * kStepBytes);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) f.b[n] = *reinterpret_cast<const v4u32*>(src + rb + n * 16 * kStepBytes);
+  };
+  auto multiply = [&](const Frag& f) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) c[m][n] = mma<ES>(f.a[m], f.b[n], c[m][n]);
+  };
+  // Half a step ahead: while one half step's operands are multiplied the next one's are read from LDS.
+  // The barrier stands in the middle of a step: behind it step t's buffer is free (every wave has read
+  // its second half) and step t + 1's has landed.
+#pragma unroll
+  for (int t = 0; t < ST; ++t) issue(t);
+  if (nk > 0) {
+    Frag f0, f1;
+    if (nk >= ST) wait_barrier<(ST - 1) * (CA + CB)>();
     else wait_barrier<0>();
-    if (t + ST - 1 < nk) issue(t + ST - 1);   // over the buffer of step t - 1, which every wave has left
-    const char* src = lds + (t % ST) * STAGE;
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const int ph = ((kk * 4 + q) ^ (lane & 7)) * 16;
-      v4u32 a[MT], b[NT];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) a[m] = *reinterpret_cast<const v4u32*>(src + ra + m * 16 * kStepBytes + ph);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) b[n] = *reinterpret_cast<const v4u32*>(src + rb + n * 16 * kStepBytes + ph);
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) c[m][n] = mma<ES>(a[m], b[n], c[m][n]);
+    fetch(f0, 0, 0);
+    int t = 0;
+    for (; t + ST < full; ++t) {
+      fetch(f1, t, 1);
+      multiply(f0);
+      interleave<MT + NT, MT * NT * (ES == 2 ? 1 : 4)>();
+      wait_barrier<(ST - 2) * (CA + CB)>();
+      issue_whole(t + ST);
+      fetch(f0, t + 1, 0);
+      multiply(f1);
+      interleave<MT + NT, MT * NT * (ES == 2 ? 1 : 4)>();
     }
+    for (; t + 1 < nk; ++t) {
+      fetch(f1, t, 1);
+      multiply(f0);
+      wait_barrier<0>();
+      issue(t + ST);
+      fetch(f0, t + 1, 0);
+      multiply(f1);
+    }
+    fetch(f1, t, 1);
+    multiply(f0);
+    multiply(f1);
   }
 
   // c[m][n][x]: row i = iw + 16 m + x of A (consecutive in x), row j of B = jw + 16 n
@@ -214,7 +267,7 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
       s += __shfl_xor(s, 32);
       if (j < g.rowsB) {
         if (q == 0) g.part[(size_t)(i0 / (BM / WM) + wi) * g.rowsB + j] = make_float2(mx, s);
-        const int rel = g.labels[j] - iw;   // the lane that holds the label's logit writes it
+        const int rel = g.labels[j] - g.v0 - iw;   // the lane that holds the label's logit writes it
         if (rel >= 0 && rel < MT * 16 && (rel & 15) < 4 && iw + rel < g.rowsA) {
           float z = 0.f;
 #pragma unroll
@@ -274,7 +327,10 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
         if (i >= g.rowsA) continue;   // rowsA is a multiple of 4
         f32x4 o = c[m][n];
         if constexpr (KIND == kAcc) {
-          f32x4* p = reinterpret_cast<f32x4*>(g.acc + ((size_t)split * g.rowsB + j) * g.rowsA + i);
+          f32x4* p = reinterpret_cast<f32x4*>(
+              part == 0 ? g.acc + (size_t)j * g.rowsA + i
+                        : g.acc_parts + ((size_t)((tile - g.whole) * (g.parts - 1) + part - 1) * BN + (j - j0)) * BM +
+                              (i - i0));
           if (g.accumulate) o += *p;
           *p = o;
         } else if constexpr (ES == 2) {
@@ -290,45 +346,58 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
   }
 }
 
-// Strips -> lse, loss and status per row: 16 rows per workgroup, 64 threads share a row's strips
-// (each a running maximum and fp64 sum), joined in LDS.
+// Strips -> lse, loss and status per row: R rows per workgroup, 1024 / R threads share a row's strips
+// (each a running maximum and fp64 sum; R = 16 reads whole lines, R = 1 spreads few rows over the chip).
 constexpr int kCombineThreads = 1024;
 
+template <int R>
 __global__ __launch_bounds__(kCombineThreads) void xent_combine_kernel(const float2* part, int strips, int N, int V,
                                                                        const int32_t* labels, const float* zlab,
                                                                        float* loss, float* lse, int32_t* status) {
-  __shared__ float sm[64][17];
-  __shared__ double ss[64][17];
-  const int r = threadIdx.x & 15, h = threadIdx.x >> 4;
-  const int n = (int)blockIdx.x * 16 + r, nc = min(n, N - 1);
+  constexpr int H = kCombineThreads / R, U = 4;
+  __shared__ float sm[R][H + 1];
+  __shared__ double ss[R][H + 1];
+  const int r = threadIdx.x % R, h = threadIdx.x / R;
+  const int n = (int)blockIdx.x * R + r, nc = min(n, N - 1);
   float m = -INFINITY;
   double s = 0.0;
-  for (int t = h; t < strips; t += 64) {
-    const float2 p = part[(size_t)t * N + nc];
-    if (p.x > m) {
-      s = s * (double)__builtin_amdgcn_exp2f((m - p.x) * kLog2eF) + (double)p.y;
-      m = p.x;
-    } else {
-      s += p.x > -INFINITY ? (double)p.y * (double)__builtin_amdgcn_exp2f((p.x - m) * kLog2eF) : (double)p.y;
+  for (int t = h; t < strips; t += U * H) {
+    float2 p[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) p[u] = part[(size_t)min(t + u * H, strips - 1) * N + nc];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (t + u * H >= strips) break;
+      const float M = fmaxf(m, p[u].x), d = M > -INFINITY ? M : 0.f;
+      s = s * (double)__builtin_amdgcn_exp2f((m - d) * kLog2eF) +
+          (double)p[u].y * (double)__builtin_amdgcn_exp2f((p[u].x > -INFINITY ? p[u].x - d : 0.f) * kLog2eF);
+      m = M;
     }
   }
-  sm[h][r] = m;
-  ss[h][r] = s;
+  sm[r][h] = m;
+  ss[r][h] = s;
   __syncthreads();
-  if (h == 0 && n < N) {
-    float M = -INFINITY;
-    for (int t = 0; t < 64; ++t) M = fmaxf(M, sm[t][r]);
-    double S = 0.0;
-    for (int t = 0; t < 64; ++t) S += sm[t][r] > -INFINITY ? ss[t][r] * exp((double)sm[t][r] - (double)M) : ss[t][r];
+  // a wave per row joins its H values
+  const int wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
+  if (wave >= R || (int)blockIdx.x * R + wave >= N) return;
+  const int row = (int)blockIdx.x * R + wave;
+  float M = -INFINITY;
+  for (int t = lane; t < H; t += SPEC_WAVE) M = fmaxf(M, sm[wave][t]);
+  M = wave_max(M);
+  double S = 0.0;
+  for (int t = lane; t < H; t += SPEC_WAVE)
+    S += sm[wave][t] > -INFINITY ? ss[wave][t] * exp((double)sm[wave][t] - (double)M) : ss[wave][t];
+  S = wave_sum(S);
+  if (lane == 0) {
     const bool fin = M < INFINITY && M > -INFINITY && S > 0.0 && S < INFINITY;   // NaN sums fail too
     const double l = (double)M + log(S);
-    const int label = labels[n];
+    const int label = labels[row];
     int st = 0;
     if (label < -1 || label >= V) st |= SPEC_REQ_BAD_TOKEN;
     if (label != -1 && !fin) st |= SPEC_REQ_NONFINITE;
-    lse[n] = fin ? (float)l : NAN;
-    loss[n] = label == -1 ? 0.f : (st ? NAN : (float)(l - (double)zlab[n]));
-    if (status) status[n] = st;
+    lse[row] = fin ? (float)l : NAN;
+    loss[row] = label == -1 ? 0.f : (st ? NAN : (float)(l - (double)zlab[row]));
+    if (status) status[row] = st;
   }
 }
 
@@ -364,16 +433,25 @@ __global__ __launch_bounds__(256) void xent_transpose_kernel(const char* in, siz
   }
 }
 
-// grad_hidden = the sum of the splits, rounded once; zeros for the rows left out.
+// grad_hidden = the sums, the parts of a shared tile added in order, rounded once; zeros for the rows
+// left out.
 template <int ES>
-__global__ __launch_bounds__(256) void xent_finish_kernel(const float* acc, int splits, int N, int d, char* out,
+__global__ __launch_bounds__(256) void xent_finish_kernel(GemmArgs g, int bm, int bn, char* out,
                                                           const int32_t* labels, const float* lse, int V) {
-  const size_t n4 = (size_t)N * d / 4, t = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (t >= n4) return;
-  const int n = (int)(t * 4 / d);
+  const int d = g.rowsA, N = g.rowsB, d4 = d / 4;
+  const size_t t = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (t >= (size_t)N * d4) return;
+  const int n = (int)(t / d4), i = (int)(t - (size_t)n * d4) * 4;
   f32x4 s = {};
-  if (live_row(labels[n], lse[n], V))
-    for (int i = 0; i < splits; ++i) s += reinterpret_cast<const f32x4*>(acc + (size_t)i * N * d)[t];
+  if (live_row(labels[n], lse[n], V)) {
+    s = reinterpret_cast<const f32x4*>(g.acc)[t];
+    const int ti = i / bm, tj = n / bn, band = tj / 8;
+    const int rest = band * 8 * g.ti + ti * min(8, g.tj - band * 8) + tj % 8 - g.whole;
+    if (rest >= 0)
+      for (int p = 0; p < g.parts - 1; ++p)
+        s += *reinterpret_cast<const f32x4*>(g.acc_parts + ((size_t)(rest * (g.parts - 1) + p) * bn + (n - tj * bn)) * bm +
+                                             (i - ti * bm));
+  }
   if constexpr (ES == 2) {
     bf16x4 h;
 #pragma unroll
@@ -389,23 +467,71 @@ __global__ __launch_bounds__(256) void xent_finish_kernel(const float* acc, int 
 inline int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 inline long long round_to(long long a, long long b) { return (a + b - 1) / b * b; }
 
-// Tile shapes of the product: 256 x 256 (8 waves) when such tiles fill the 256 CUs, 128 x 128 (4 waves,
-// two workgroups per CU) below that, 128 x 64 when B has at most 64 rows.
+// Tile shapes of the product: 256 x 256 (8 waves, one workgroup per CU), 128 x 128 (4 waves, two per CU),
+// 128 x 64 (4 waves, two per CU; rowsB of at most 64).
 enum { kBig = 0, kMid = 1, kThin = 2 };
 
-inline int pick_tile(long long rowsA, long long rowsB, int splits) {
-  if (rowsB <= 64) return kThin;
-  return (long long)ceil_div(rowsA, 256) * ceil_div(rowsB, 256) * splits >= 256 ? kBig : kMid;
-}
 inline int tile_m(int t) { return t == kBig ? 256 : 128; }
 inline int tile_n(int t) { return t == kBig ? 256 : t == kMid ? 128 : 64; }
-inline int strip_rows(int t) { return t == kBig ? 128 : 64; }
+inline int strip_rows(int t) { return t == kBig ? 128 : 64; }   // of kStats
+inline int tile_slots(int t) { return t == kBig ? 256 : 512; }  // workgroups the chip holds at once
+
+// Microseconds of one step of 128 bytes of k on a chip full of tiles, and on one with a tile per CU.
+// Measured on N = 4096, V = 151936, d = 4352 (bf16): 4.08 ms in 256 x 256 tiles, 5.24 in 128 x 128, 6.83
+// in 128 x 64.  fp32 is bound by the matrix units (a sixteenth of the bf16 rate): tiles cost their area.
+inline double step_us(int t, bool full, int es) {
+  if (es == 4) return t == kBig ? 7.2 : t == kMid ? (full ? 3.7 : 1.9) : (full ? 1.9 : 1.0);
+  return t == kBig ? 1.6 : t == kMid ? (full ? 1.04 : 0.62) : (full ? 0.68 : 0.4);
+}
+inline double tiles_us(long long tiles, int t, int steps, int es) {
+  const long long slots = tile_slots(t), rounds = tiles / slots, rest = tiles % slots;
+  return steps * (rounds * step_us(t, true, es) + (rest > 256 ? step_us(t, true, es) : rest > 0 ? step_us(t, false, es) : 0));
+}
+
+// How a product's rows are shared out: the first `head` rows of the longer side in 256 x 256 tiles, the
+// others in `tail` tiles (head = 0: one shape for all).  A last round that fills a quarter of the chip
+// with 256 x 256 tiles costs as much as a full one: its rows go to smaller tiles instead.
+struct Shape {
+  bool along_a;     // the rows shared out are A's
+  long long head;
+  int tail;
+};
+
+Shape pick_shape(long long rowsA, long long rowsB, int kbytes, int es) {
+  const int steps = ceil_div(kbytes, kStepBytes);
+  auto cost = [&](long long a, long long b, int t) {
+    return a && b ? tiles_us((long long)ceil_div(a, tile_m(t)) * ceil_div(b, tile_n(t)), t, steps, es) : 0.0;
+  };
+  Shape best{rowsA >= rowsB, 0, rowsB <= 64 ? kThin : kMid};
+  double us = cost(rowsA, rowsB, best.tail);
+  if (rowsB <= 64) return best;
+  if (cost(rowsA, rowsB, kBig) <= us) {
+    best.tail = kBig;
+    us = cost(rowsA, rowsB, kBig);
+  }
+  const long long len = best.along_a ? rowsA : rowsB, other = best.along_a ? rowsB : rowsA;
+  const long long across = ceil_div(other, 256);
+  const long long rounds = (long long)ceil_div(len, 256) * across / 256;
+  const long long head = rounds * 256 / across * 256;   // rows whose tiles fill whole rounds
+  if (rounds > 0 && head < len) {
+    const double mixed = cost(best.along_a ? head : rowsA, best.along_a ? rowsB : head, kBig) +
+                         cost(best.along_a ? len - head : rowsA, best.along_a ? rowsB : len - head, kMid) + 4.0;
+    if (mixed < us) {
+      best.head = head;
+      best.tail = kMid;
+    }
+  }
+  return best;
+}
 
 template <int ES, int KIND>
-void launch_gemm(GemmArgs& g, int tile, hipStream_t s) {
+void launch_tiles(GemmArgs& g, int tile, int whole, int parts, hipStream_t s) {
   g.ti = ceil_div(g.rowsA, tile_m(tile));
   g.tj = ceil_div(g.rowsB, tile_n(tile));
-  const dim3 grid((unsigned)(g.ti * g.tj * g.splits));   // within head_fits
+  const int tiles = g.ti * g.tj;   // within head_fits
+  g.whole = whole < tiles ? whole : tiles;
+  g.parts = parts;
+  const dim3 grid((unsigned)(g.whole + (tiles - g.whole) * parts));
   if (tile == kBig)
     hipLaunchKernelGGL((xent_gemm_kernel<ES, 256, 256, 2, 4, 2, KIND>), grid, dim3(512), 0, s, g);
   else if (tile == kMid)
@@ -414,12 +540,52 @@ void launch_gemm(GemmArgs& g, int tile, hipStream_t s) {
     hipLaunchKernelGGL((xent_gemm_kernel<ES, 128, 64, 2, 2, 3, KIND>), grid, dim3(256), 0, s, g);
 }
 
-// Every launch's work-items fit the 32-bit grid size of the dispatch packet (tiles below 256 x 256 are
-// taken only where fewer than 256 such tiles would do, and contraction splits only below 512 tiles).
+// A product in the shapes of pick_shape: kStats and kGradZ share out A's rows (the vocabulary), kStore
+// the longer side of either.
+template <int ES, int KIND>
+void launch_gemm(const GemmArgs& g, hipStream_t s) {
+  const Shape sh = pick_shape(g.rowsA, g.rowsB, g.kbytes, ES);
+  const bool split = sh.head > 0 && (sh.along_a || KIND == kStore);
+  GemmArgs h = g;
+  if (split) {
+    GemmArgs f = g;
+    (sh.along_a ? f.rowsA : f.rowsB) = (int)sh.head;
+    if (KIND == kGradZ) f.vpad = (int)sh.head;
+    launch_tiles<ES, KIND>(f, kBig, INT32_MAX, 1, s);
+    if (sh.along_a) {
+      h.A += (size_t)sh.head * g.lda;
+      h.rowsA -= (int)sh.head;
+      if (KIND == kStats || KIND == kGradZ) h.v0 += (int)sh.head;
+      if (KIND == kStats) h.part += (size_t)(sh.head / strip_rows(kBig)) * g.rowsB;
+      if (KIND == kGradZ) {
+        h.gn += (size_t)sh.head * ES;
+        h.gt += (size_t)sh.head * g.ldgt;
+        h.vpad -= (int)sh.head;
+      }
+      if (KIND == kStore) h.out += (size_t)sh.head * ES;
+    } else {
+      h.B += (size_t)sh.head * g.ldb;
+      h.rowsB -= (int)sh.head;
+      h.out += (size_t)sh.head * g.ldo;
+    }
+  }
+  launch_tiles<ES, KIND>(h, split || sh.head == 0 ? sh.tail : kBig, INT32_MAX, 1, s);
+}
+
+// Strips of kStats over V rows of A.
+int stat_strips(long long V, long long N, int kbytes, int es) {
+  const Shape sh = pick_shape(V, N, kbytes, es);
+  const long long head = sh.along_a ? sh.head : 0;
+  const int tail = sh.along_a || sh.head == 0 ? sh.tail : kBig;
+  return (int)(head / strip_rows(kBig)) + ceil_div(V - head, tile_m(tail)) * (tile_m(tail) / strip_rows(tail));
+}
+
+// Every launch's work-items fit the 32-bit grid size of the dispatch packet, whatever the tiles (the
+// parts of kAcc add at most 16 times the tiles of two rounds).
 bool head_fits(long long N, long long V, long long d) {
-  const long long most = 0xffffffffll;
-  return (long long)ceil_div(V, 256) * ceil_div(N, 256) * 512 <= most && N * d / 4 + 256 <= most &&
-         (long long)ceil_div(V, 256) * ceil_div(d, 256) * 512 <= most;
+  const long long most = 0xffffffffll - 256ll * 1024 * 32;
+  return (long long)ceil_div(V, 128) * ceil_div(N, 64) * 256 <= most && N * d / 4 + 256 <= most &&
+         (long long)ceil_div(V, 128) * ceil_div(d, 64) * 256 <= most;
 }
 
 bool head_ok(int N, int V, int d, int dtype) {
@@ -433,12 +599,13 @@ struct BackPlan {
   int es, step;          // element size, elements per 128 bytes
   int pieces, vc;        // vocabulary pieces of vc tokens (a multiple of 256; the last may be shorter)
   long long npad;
-  int splits, ksplit;    // of the contraction of dH over a piece
-  size_t gn, gt, wt, ht, acc;   // bytes
-  size_t total() const { return gn + gt + wt + ht + acc; }
+  int tile, whole, parts;   // of dH: tiles taken whole, and the workgroups that share each of the others
+  size_t gn, gt, wt, ht, acc, acc_parts;   // bytes
+  size_t total() const { return gn + gt + wt + ht + acc + acc_parts; }
 };
 
 constexpr long long kPieceBytes = 128ll << 20;   // of G (and of W^T) per piece
+constexpr int kMaxParts = 16, kPartSteps = 8;    // workgroups per tile at most; steps of one at least
 
 BackPlan back_plan(int N, int V, int d, int dtype) {
   BackPlan p{};
@@ -451,37 +618,55 @@ BackPlan back_plan(int N, int V, int d, int dtype) {
   p.pieces = ceil_div(V, vmax);
   p.vc = (int)round_to(ceil_div(V, p.pieces), 256);
   p.pieces = ceil_div(V, p.vc);
-  const int tile = N <= 64 ? kThin : kMid;
-  const long long tiles = (long long)ceil_div(d, tile_m(tile)) * ceil_div(N, tile_n(tile));
+  // dH has few tiles and a long contraction: whole rounds of tiles are taken a workgroup each, and each
+  // tile of the last, partial round is shared by `parts` workgroups along the contraction (272 tiles of
+  // 256 x 256 on 256 CUs: one round and 16 tiles by 16 workgroups, 1.06 rounds in place of 2)
   const int steps = p.vc / p.step;
-  long long s = tiles >= 512 ? 1 : 512 / tiles;
-  if (s > 16) s = 16;
-  if (s > steps / 4) s = steps / 4 > 0 ? steps / 4 : 1;
-  p.ksplit = ceil_div(steps, s) * kStepBytes;
-  p.splits = ceil_div((long long)p.vc * p.es, p.ksplit);
+  double best = 1e300;
+  for (int t = N <= 64 ? kThin : kBig; t <= (N <= 64 ? kThin : kMid); ++t) {
+    const long long tiles = (long long)ceil_div(d, tile_m(t)) * ceil_div(N, tile_n(t));
+    const long long whole = tiles / tile_slots(t) * tile_slots(t), rest = tiles - whole;
+    for (int parts = 1; parts <= kMaxParts && (parts == 1 || steps / parts >= kPartSteps); ++parts) {
+      // a part costs its share of the steps, and about 6 steps to start and to store
+      const double us = tiles_us(whole, t, steps + 6, p.es) + tiles_us(rest * parts, t, ceil_div(steps, parts) + 6, p.es);
+      if (us < best) {
+        best = us;
+        p.tile = t;
+        p.whole = (int)whole;
+        p.parts = parts;
+        p.acc_parts = round256((size_t)rest * (parts - 1) * tile_m(t) * tile_n(t) * sizeof(float));
+      }
+    }
+  }
   p.gn = round256((size_t)N * p.vc * p.es);
   p.gt = round256((size_t)p.vc * p.npad * p.es);
   p.wt = round256((size_t)d * p.vc * p.es);
   p.ht = round256((size_t)d * p.npad * p.es);
-  p.acc = round256((size_t)p.splits * N * d * sizeof(float));
+  p.acc = round256((size_t)N * d * sizeof(float));
   return p;
 }
 
 template <int ES>
 int32_t run_forward(int N, int V, int d, const void* hidden, const void* weight, const int32_t* labels, float* loss,
                     float* lse, int32_t* status, char* ws, hipStream_t s) {
-  const int tile = pick_tile(V, N, 1);
-  const int strips = ceil_div(V, tile_m(tile)) * (tile_m(tile) / strip_rows(tile));
+  const int strips = stat_strips(V, N, d * ES, ES);
   GemmArgs g{};
   g.A = reinterpret_cast<const char*>(weight); g.B = reinterpret_cast<const char*>(hidden);
   g.lda = g.ldb = (size_t)d * ES;
-  g.rowsA = V; g.rowsB = N; g.kbytes = d * ES; g.ksplit = g.kbytes; g.splits = 1;
+  g.rowsA = V; g.rowsB = N; g.kbytes = d * ES;
   g.labels = labels; g.V = V;
   g.part = reinterpret_cast<float2*>(ws);
   g.zlab = reinterpret_cast<float*>(ws + round256((size_t)strips * N * sizeof(float2)));
-  launch_gemm<ES, kStats>(g, tile, s);
-  hipLaunchKernelGGL(xent_combine_kernel, dim3(ceil_div(N, 16)), dim3(kCombineThreads), 0, s, g.part, strips, N, V,
-                     labels, g.zlab, loss, lse, status);
+  launch_gemm<ES, kStats>(g, s);
+  if (N >= 2048)
+    hipLaunchKernelGGL(xent_combine_kernel<16>, dim3(ceil_div(N, 16)), dim3(kCombineThreads), 0, s, g.part, strips, N,
+                       V, labels, g.zlab, loss, lse, status);
+  else if (N >= 512)
+    hipLaunchKernelGGL(xent_combine_kernel<4>, dim3(ceil_div(N, 4)), dim3(kCombineThreads), 0, s, g.part, strips, N, V,
+                       labels, g.zlab, loss, lse, status);
+  else
+    hipLaunchKernelGGL(xent_combine_kernel<1>, dim3(N), dim3(kCombineThreads), 0, s, g.part, strips, N, V, labels,
+                       g.zlab, loss, lse, status);
   return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
 }
 
@@ -495,6 +680,10 @@ int32_t run_backward(int N, int V, int d, int dtype, const void* hidden, const v
   char* wt = gt + p.gt;
   char* ht = wt + p.wt;
   float* acc = reinterpret_cast<float*>(ht + p.ht);
+  GemmArgs h{};   // dH
+  h.A = wt; h.lda = (size_t)p.vc * ES; h.rowsA = d;
+  h.B = gn; h.ldb = (size_t)p.vc * ES; h.rowsB = N;
+  h.acc = acc; h.acc_parts = reinterpret_cast<float*>(ht + p.ht + p.acc);
   const size_t ld = (size_t)d * ES;
   if (grad_weight)
     hipLaunchKernelGGL(xent_transpose_kernel<ES>, dim3(ceil_div(p.npad, 64), ceil_div(d, 64)), dim3(256), 0, s,
@@ -507,33 +696,30 @@ int32_t run_backward(int N, int V, int d, int dtype, const void* hidden, const v
     GemmArgs g{};
     g.A = w; g.B = reinterpret_cast<const char*>(hidden);
     g.lda = g.ldb = ld;
-    g.rowsA = nv; g.rowsB = N; g.kbytes = d * ES; g.ksplit = g.kbytes; g.splits = 1;
+    g.rowsA = nv; g.rowsB = N; g.kbytes = d * ES;
     g.labels = labels; g.V = V; g.v0 = v0; g.lse = lse; g.grad_loss = grad_loss;
     g.gn = gn; g.ldgn = (size_t)p.vc * ES; g.vpad = vpad;
     g.gt = gt; g.ldgt = (size_t)p.npad * ES; g.npad = (int)p.npad;
-    launch_gemm<ES, kGradZ>(g, pick_tile(nv, N, 1), s);
+    launch_gemm<ES, kGradZ>(g, s);
     if (grad_hidden) {
       hipLaunchKernelGGL(xent_transpose_kernel<ES>, dim3(ceil_div(vpad, 64), ceil_div(d, 64)), dim3(256), 0, s, w, ld,
                          nv, d, wt, (size_t)p.vc * ES, vpad, nullptr, nullptr, 0);
-      GemmArgs h{};
-      h.A = wt; h.lda = (size_t)p.vc * ES; h.rowsA = d;
-      h.B = gn; h.ldb = (size_t)p.vc * ES; h.rowsB = N;
-      h.kbytes = vpad * ES; h.ksplit = p.ksplit; h.splits = p.splits;   // every split is written
-      h.acc = acc; h.accumulate = c > 0;
-      launch_gemm<ES, kAcc>(h, pick_tile(d, N, h.splits), s);
+      h.kbytes = vpad * ES;
+      h.accumulate = c > 0;
+      launch_tiles<ES, kAcc>(h, p.tile, p.whole, p.parts, s);
     }
     if (grad_weight) {
-      GemmArgs h{};
-      h.A = ht; h.lda = (size_t)p.npad * ES; h.rowsA = d;
-      h.B = gt; h.ldb = (size_t)p.npad * ES; h.rowsB = nv;
-      h.kbytes = (int)p.npad * ES; h.ksplit = h.kbytes; h.splits = 1;
-      h.out = reinterpret_cast<char*>(grad_weight) + (size_t)v0 * ld; h.ldo = ld;
-      launch_gemm<ES, kStore>(h, pick_tile(d, nv, 1), s);
+      GemmArgs w{};
+      w.A = ht; w.lda = (size_t)p.npad * ES; w.rowsA = d;
+      w.B = gt; w.ldb = (size_t)p.npad * ES; w.rowsB = nv;
+      w.kbytes = (int)p.npad * ES;
+      w.out = reinterpret_cast<char*>(grad_weight) + (size_t)v0 * ld; w.ldo = ld;
+      launch_gemm<ES, kStore>(w, s);
     }
   }
   if (grad_hidden)
-    hipLaunchKernelGGL(xent_finish_kernel<ES>, dim3(ceil_div((long long)N * d / 4, 256)), dim3(256), 0, s, acc,
-                       p.splits, N, d, reinterpret_cast<char*>(grad_hidden), labels, lse, V);
+    hipLaunchKernelGGL(xent_finish_kernel<ES>, dim3(ceil_div((long long)N * d / 4, 256)), dim3(256), 0, s, h,
+                       tile_m(p.tile), tile_n(p.tile), reinterpret_cast<char*>(grad_hidden), labels, lse, V);
   return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
 }
 
@@ -544,8 +730,7 @@ using namespace spec;
 
 extern "C" size_t spec_head_xent_workspace_size(int32_t N, int32_t V, int32_t d, int32_t dtype) {
   if (!head_ok(N, V, d, dtype)) return 0;
-  const int tile = pick_tile(V, N, 1);
-  const size_t strips = (size_t)ceil_div(V, tile_m(tile)) * (tile_m(tile) / strip_rows(tile));
+  const size_t strips = (size_t)stat_strips(V, N, d * (dtype == SPEC_BF16 ? 2 : 4), dtype == SPEC_BF16 ? 2 : 4);
   return round256(strips * N * sizeof(float2)) + round256((size_t)N * sizeof(float));
 }
 

@@ -153,7 +153,13 @@ def _launch(stream, allocated, call):
 
 
 def _launch_on(device, stream, allocated, call):
-    """_launch with `device` current: its current stream by default, and a stream of that device only."""
+    """_launch with `device` current: its current stream by default, and a stream of that device only.
+
+    On the current device's current stream (where the binding allocated) the raw handle is all that is
+    needed: the stream and device objects of the general path cost more than a small call's kernels.
+    """
+    if stream is None and torch.cuda.current_device() == device.index:
+        return call(ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index)))
     if stream is not None and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     with torch.cuda.device(device):
@@ -811,21 +817,20 @@ def teacher_topk(target: torch.Tensor, K: int, lengths: Optional[torch.Tensor] =
             B, G, V, _logit_dtype(target), _ptr(target), K, _ptr(lengths), _ptr(temperature), _ptr(out["ids"]),
             _ptr(out["values"]), _ptr(out.get("lse")), _ptr(out.get("status")), _ptr(ws),
             ws.numel() * ws.element_size(), sp)
-    with torch.cuda.device(dev):
-        if temperature is None:
-            temperature = torch.ones(B, dtype=torch.float32, device=dev)
-            mine.append(temperature)
-        if out is None:
-            out = dict(ids=torch.empty((B, G, max(K, 0)), dtype=torch.int32, device=dev),
-                       values=torch.empty((B, G, max(K, 0)), dtype=torch.float32, device=dev),
-                       lse=torch.empty((B, G), dtype=torch.float32, device=dev),
-                       status=torch.empty(B, dtype=torch.int32, device=dev))
-            mine.extend(out.values())
-        else:
-            _check_out(out, dict(ids=((B, G, K), torch.int32, True), values=((B, G, K), torch.float32, True),
-                                 lse=((B, G), torch.float32, False), status=((B,), torch.int32, False)), dev)
-        ws = _device_workspace(int(lib.spec_teacher_workspace_size(B, G, V, K)), dev, workspace, mine)
-        _check("spec_teacher_topk", _launch_on(dev, stream, mine, call))
+    if temperature is None:
+        temperature = torch.ones(B, dtype=torch.float32, device=dev)
+        mine.append(temperature)
+    if out is None:
+        out = dict(ids=torch.empty((B, G, max(K, 0)), dtype=torch.int32, device=dev),
+                   values=torch.empty((B, G, max(K, 0)), dtype=torch.float32, device=dev),
+                   lse=torch.empty((B, G), dtype=torch.float32, device=dev),
+                   status=torch.empty(B, dtype=torch.int32, device=dev))
+        mine.extend(out.values())
+    else:
+        _check_out(out, dict(ids=((B, G, K), torch.int32, True), values=((B, G, K), torch.float32, True),
+                             lse=((B, G), torch.float32, False), status=((B,), torch.int32, False)), dev)
+    ws = _device_workspace(int(lib.spec_teacher_workspace_size(B, G, V, K)), dev, workspace, mine)
+    _check("spec_teacher_topk", _launch_on(dev, stream, mine, call))
     return out
 
 
@@ -873,21 +878,20 @@ def distill_loss(draft: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
             B, G, V, _logit_dtype(draft), _ptr(draft), K, _ptr(ids), _ptr(values), _ptr(teacher_lse), int(mode),
             _ptr(lengths), _ptr(temperature), _ptr(out["loss"]), _ptr(out["saved"]), _ptr(out.get("status")),
             _ptr(ws), ws.numel() * ws.element_size(), sp)
-    with torch.cuda.device(dev):
-        if temperature is None:
-            temperature = torch.ones(B, dtype=torch.float32, device=dev)
-            mine.append(temperature)
-        if out is None:
-            out = dict(loss=torch.empty((B, G), dtype=torch.float32, device=dev),
-                       saved=torch.empty((B, G, SPEC_DISTILL_SAVED), dtype=torch.float64, device=dev),
-                       status=torch.empty(B, dtype=torch.int32, device=dev))
-            mine.extend(out.values())
-        else:
-            _check_out(out, dict(loss=((B, G), torch.float32, True),
-                                 saved=((B, G, SPEC_DISTILL_SAVED), torch.float64, True),
-                                 status=((B,), torch.int32, False)), dev)
-        ws = _device_workspace(int(lib.spec_distill_workspace_size(B, G, V, K)), dev, workspace, mine)
-        _check("spec_distill_loss", _launch_on(dev, stream, mine, call))
+    if temperature is None:
+        temperature = torch.ones(B, dtype=torch.float32, device=dev)
+        mine.append(temperature)
+    if out is None:
+        out = dict(loss=torch.empty((B, G), dtype=torch.float32, device=dev),
+                   saved=torch.empty((B, G, SPEC_DISTILL_SAVED), dtype=torch.float64, device=dev),
+                   status=torch.empty(B, dtype=torch.int32, device=dev))
+        mine.extend(out.values())
+    else:
+        _check_out(out, dict(loss=((B, G), torch.float32, True),
+                             saved=((B, G, SPEC_DISTILL_SAVED), torch.float64, True),
+                             status=((B,), torch.int32, False)), dev)
+    ws = _device_workspace(int(lib.spec_distill_workspace_size(B, G, V, K)), dev, workspace, mine)
+    _check("spec_distill_loss", _launch_on(dev, stream, mine, call))
     return out
 
 
@@ -914,19 +918,18 @@ def distill_loss_backward(draft: torch.Tensor, ids: torch.Tensor, values: torch.
     if in_place and out is not None:
         raise ValueError("pass out or in_place, not both")
     mine = []
-    with torch.cuda.device(dev):
-        if temperature is None:
-            temperature = torch.ones(B, dtype=torch.float32, device=dev)
-            mine.append(temperature)
-        if in_place:
-            out = draft
-        elif out is None:
-            out = torch.empty_like(draft)
-            mine.append(out)
-        code = _launch_on(dev, stream, mine, lambda sp: lib.spec_distill_loss_backward(
-            B, G, V, _logit_dtype(draft), _ptr(draft), K, _ptr(ids), _ptr(values), int(mode), _ptr(temperature),
-            _ptr(saved), _ptr(grad_loss), _ptr(out), sp))
-        _check("spec_distill_loss_backward", code)
+    if temperature is None:
+        temperature = torch.ones(B, dtype=torch.float32, device=dev)
+        mine.append(temperature)
+    if in_place:
+        out = draft
+    elif out is None:
+        out = torch.empty_like(draft)
+        mine.append(out)
+    code = _launch_on(dev, stream, mine, lambda sp: lib.spec_distill_loss_backward(
+        B, G, V, _logit_dtype(draft), _ptr(draft), K, _ptr(ids), _ptr(values), int(mode), _ptr(temperature),
+        _ptr(saved), _ptr(grad_loss), _ptr(out), sp))
+    _check("spec_distill_loss_backward", code)
     return out
 
 
@@ -962,17 +965,16 @@ def head_xent(hidden: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor, 
         return lib.spec_head_xent(N, V, d, dt, _ptr(hidden), _ptr(weight), _ptr(labels), _ptr(out["loss"]),
                                   _ptr(out["lse"]), _ptr(out.get("status")), _ptr(ws),
                                   ws.numel() * ws.element_size(), sp)
-    with torch.cuda.device(dev):
-        if out is None:
-            out = dict(loss=torch.empty(N, dtype=torch.float32, device=dev),
-                       lse=torch.empty(N, dtype=torch.float32, device=dev),
-                       status=torch.empty(N, dtype=torch.int32, device=dev))
-            mine.extend(out.values())
-        else:
-            _check_out(out, dict(loss=((N,), torch.float32, True), lse=((N,), torch.float32, True),
-                                 status=((N,), torch.int32, False)), dev)
-        ws = _device_workspace(int(lib.spec_head_xent_workspace_size(N, V, d, dt)), dev, workspace, mine)
-        _check("spec_head_xent", _launch_on(dev, stream, mine, call))
+    if out is None:
+        out = dict(loss=torch.empty(N, dtype=torch.float32, device=dev),
+                   lse=torch.empty(N, dtype=torch.float32, device=dev),
+                   status=torch.empty(N, dtype=torch.int32, device=dev))
+        mine.extend(out.values())
+    else:
+        _check_out(out, dict(loss=((N,), torch.float32, True), lse=((N,), torch.float32, True),
+                             status=((N,), torch.int32, False)), dev)
+    ws = _device_workspace(int(lib.spec_head_xent_workspace_size(N, V, d, dt)), dev, workspace, mine)
+    _check("spec_head_xent", _launch_on(dev, stream, mine, call))
     return out
 
 
@@ -1000,17 +1002,16 @@ def head_xent_backward(hidden: torch.Tensor, weight: torch.Tensor, labels: torch
                                            _ptr(grad_loss), _ptr(out.get("grad_hidden")),
                                            _ptr(out.get("grad_weight")), _ptr(ws), ws.numel() * ws.element_size(),
                                            sp)
-    with torch.cuda.device(dev):
-        if out is None:
-            out = {}
-            if need_hidden:
-                out["grad_hidden"] = torch.empty_like(hidden)
-            if need_weight:
-                out["grad_weight"] = torch.empty_like(weight)
-            mine.extend(out.values())
-        else:
-            _check_out(out, dict(grad_hidden=((N, d), hidden.dtype, False),
-                                 grad_weight=((V, d), hidden.dtype, False)), dev)
-        ws = _device_workspace(int(lib.spec_head_xent_backward_workspace_size(N, V, d, dt)), dev, workspace, mine)
-        _check("spec_head_xent_backward", _launch_on(dev, stream, mine, call))
+    if out is None:
+        out = {}
+        if need_hidden:
+            out["grad_hidden"] = torch.empty_like(hidden)
+        if need_weight:
+            out["grad_weight"] = torch.empty_like(weight)
+        mine.extend(out.values())
+    else:
+        _check_out(out, dict(grad_hidden=((N, d), hidden.dtype, False),
+                             grad_weight=((V, d), hidden.dtype, False)), dev)
+    ws = _device_workspace(int(lib.spec_head_xent_backward_workspace_size(N, V, d, dt)), dev, workspace, mine)
+    _check("spec_head_xent_backward", _launch_on(dev, stream, mine, call))
     return out

@@ -14,11 +14,12 @@
 // nearly all of q the difference has no correct digit, and a and ln r_s hang on it.
 //
 // The work is one read of the rows (forward) and one read and one write (backward):
-//   distill_stream_kernel -- one workgroup per (row, segment of at most 64 KB, in registers): marks the
-//       listed tokens of its segment in an LDS bitmap (a byte per 16-byte vector of bf16, so a vector
-//       without a listed token costs one LDS byte), takes them out and sums exp of the rest.
-//   distill_finish_kernel -- one workgroup per request, a wave per row: list terms in fp64, loss,
-//       the coefficients the backward reads, status.
+//   distill_stream_kernel -- one workgroup per row (or segment, when there are few rows): marks the
+//       listed tokens in an LDS bitmap (a byte per 16-byte vector of bf16, so a vector without a listed
+//       token costs one LDS byte), takes them out and sums exp of the rest; then, when the row is
+//       whole, its first wave forms the list's terms in fp64 (finish_row).
+//   distill_finish_kernel -- the same last step over a row's segments.
+//   distill_status_kernel -- one wave per request: the rows' findings, and NaN for a failed request.
 //   distill_grad_kernel -- one workgroup per (row, segment): q a of every token as (q / r_s) (a r_s),
 //       then, behind a barrier, the listed tokens' own values over it.
 #include "common.hpp"
@@ -31,8 +32,6 @@ namespace {
 constexpr double kLn2Seg = 0.69314718055994530942;
 constexpr int kFlagBad = 1;    // NaN or +inf outside the list
 constexpr int kFlagTwice = 2;  // a token id named twice
-constexpr int kFlagToken = 4;  // an id outside [-1, V)
-constexpr int kListWords = kSegThreads * kSegVecs * 8 / 32;   // bitmap of a bf16 segment
 
 struct DistillSeg {
   double sum, ref;   // sum of exp(z / T) over the segment's tokens outside the list: sum * 2^ref
@@ -51,6 +50,7 @@ struct DistillArgs {
   double* saved;
   int32_t* status;
   DistillSeg* segs;        // [B * G, nseg]
+  int32_t* row_status;     // [B * G]
   const float* grad_loss;  // backward
   void* grad;
 };
@@ -58,21 +58,168 @@ struct DistillArgs {
 // A used entry names a token and has a logit above -inf (a NaN logit is used, and bad).
 __device__ __forceinline__ bool used_entry(int id, float v) { return id != -1 && !(v == -INFINITY); }
 
+__device__ __forceinline__ double wave_max_d(double x) {
+  return wave_reduce(x, [](double p, double q) { return fmax(p, q); });
+}
+
+// A row's list beside its draft logits, for finish_row.
+struct ListShared {
+  int32_t id[SPEC_MAX_TEACHER_K];
+  float val[SPEC_MAX_TEACHER_K], z[SPEC_MAX_TEACHER_K];
+  double el[SPEC_MAX_TEACHER_K], te[SPEC_MAX_TEACHER_K];
+};
+
+// The last step of a row, by one wave: the list (K entries, z the draft's logits at the tokens) and, in lanes
+// s < nseg, the sums seg * 2^ref of exp(z / T) outside the list (0 in the other lanes).  All in powers of
+// two.  One wave, not the row's eight: the fp64 reductions cost a wave the same whatever it holds, and they
+// were a quarter of the whole call by eight.  exp2 and log2 stand in few places (the code runs once per
+// row and is cold then); log2 takes its four arguments from four lanes.
+__device__ __forceinline__ void finish_row(ListShared& sh, const DistillArgs& a, size_t r, double seg, double ref, int rst,
+                                           float T) {
+  const int lane = (int)threadIdx.x & 63, K = a.K;
+  const double c = scale_of(T);
+  const bool tail = a.teacher_lse != nullptr;
+  const float tl = tail ? a.teacher_lse[r] : 0.f;
+  float vmax = -INFINITY, dmax = -INFINITY;
+  int nused = 0;
+#pragma unroll 1
+  for (int e0 = 0; e0 < K; e0 += SPEC_WAVE) {
+    const int e = e0 + lane;
+    bool used = false;
+    if (e < K) {
+      const int id = sh.id[e];
+      const float v = sh.val[e], z = sh.z[e];
+      used = used_entry(id, v);
+      if (used) {
+        if (id < 0 || id >= a.V) {
+          rst |= SPEC_REQ_BAD_TOKEN;
+        } else {
+          if (!(v < INFINITY) || !(z < INFINITY)) rst |= SPEC_REQ_NONFINITE;
+          vmax = fmaxf(vmax, v);
+          dmax = fmaxf(dmax, z);
+        }
+      }
+    }
+    nused += (int)__popcll(__ballot(used));
+  }
+  const bool seg_on = seg > 0.0;
+  const double mo = wave_max_d(seg_on ? ref : -INFINITY);   // the largest reference outside the list
+  const bool outside = mo > -INFINITY;
+  const double tmax = (double)wave_max(vmax) * c, zmax = fmax((double)wave_max(dmax) * c, mo);
+  if (tail && !(fabsf(tl) < INFINITY)) rst |= SPEC_REQ_NONFINITE;
+  if (!(zmax > -INFINITY)) rst |= SPEC_REQ_NONFINITE;
+  rst = wave_or_i(rst);
+  double* sv = a.saved + r * SPEC_DISTILL_SAVED;
+  if (nused == 0 || rst != 0) {   // no entry: the row is not read
+    if (lane == 0) {
+      a.loss[r] = nused == 0 ? 0.f : NAN;
+      sv[0] = NAN;
+      a.row_status[r] = nused == 0 ? 0 : rst;
+    }
+    return;
+  }
+  double t = (double)tl * kLog2eSeg;   // log2 of p's normaliser (with a tail)
+  double lsum = 0.0, tsum = 0.0;
+#pragma unroll 1
+  for (int e0 = 0; e0 < K; e0 += SPEC_WAVE) {
+    const int e = e0 + lane;
+    double x = -INFINITY, y = -INFINITY;
+    if (e < K && used_entry(sh.id[e], sh.val[e])) {
+      x = (double)sh.z[e] * c - zmax;
+      y = (double)sh.val[e] * c - tmax;
+    }
+    x = exp2(x);
+    y = exp2(y);
+    if (e < K) {
+      sh.el[e] = x;
+      sh.te[e] = y;
+    }
+    lsum += x;
+    tsum += y;
+  }
+  lsum = wave_sum(lsum);
+  tsum = wave_sum(tsum);
+  // lanes s the segments' shares exp2(ref - mo), lane 62 exp2(tmax - t), lane 63 exp2(mo - zmax)
+  static_assert(kMaxSegs <= 62, "lanes of the segments");
+  const double sc = exp2(lane == 62 ? tmax - t : lane == 63 ? mo - zmax : ref - mo);
+  const double out = wave_sum(seg_on ? seg * sc : 0.0);
+  const double rest = outside ? out * read_lane(sc, 63) : 0.0;   // outside the list, against zmax
+  const double tot = rest + lsum, itot = 1.0 / tot;
+  const double ps = tail ? read_lane(sc, 62) : 1.0 / tsum;
+  const double rt = (tail && nused < a.V) ? fmax(0.0, 1.0 - tsum * ps) : 0.0;
+  const double rs = rest * itot;
+  const int which = lane & 3;
+  const double lg = log2(which == 0 ? out : which == 1 ? tot : which == 2 ? tsum : rt);
+  const double lout = read_lane(lg, 0), lt = read_lane(lg, 1), lrt = read_lane(lg, 3);
+  if (!tail) t = tmax + read_lane(lg, 2);
+  double loss = 0.0, bv = 0.0;
+#pragma unroll 1
+  for (int e = lane; e < K; e += SPEC_WAVE) {
+    const double pe = sh.te[e] * ps, qe = sh.el[e] * itot;
+    if (a.mode == SPEC_DISTILL_KL) {
+      if (pe > 0.0) loss += pe * (((double)sh.val[e] * c - t) - ((double)sh.z[e] * c - zmax - lt));
+    } else if (pe > qe) {
+      loss += pe - qe;
+      bv += qe;
+    }
+  }
+  loss = wave_sum(loss);
+  double ars;   // a r_s: q a = (q / r_s) (a r_s) outside the list, finite however small r_s
+  if (a.mode == SPEC_DISTILL_KL) {
+    bv = 1.0;
+    ars = rs - rt;
+    // in logs (the tail may lie hundreds of nats below the list); +inf when the draft leaves no mass there
+    if (rt > 0.0) loss += rt * (lrt - (outside ? mo - zmax + lout - lt : -INFINITY));
+    loss *= kLn2Seg;
+  } else {
+    bv = wave_sum(bv);
+    const bool up = rt > rs;
+    if (up) {
+      loss += rt - rs;
+      bv += rs;
+    }
+    ars = (bv - (up ? 1.0 : 0.0)) * rs;
+  }
+  if (lane != 0) return;
+  // q / r_s = exp2((z - m) c - sv[1]): the logit nearest the largest exponent as reference
+  const float m = outside ? (float)(mo / c) : 0.f;
+  sv[0] = (double)m;
+  sv[1] = outside ? mo - (double)m * c + lout : 0.0;
+  sv[2] = outside ? ars : 0.0;
+  sv[3] = bv;
+  sv[4] = t;
+  sv[5] = zmax + lt;
+  a.loss[r] = (float)loss;
+  a.row_status[r] = 0;
+}
+
+__device__ __forceinline__ int row_flags(int f) {
+  return (f & kFlagBad ? SPEC_REQ_NONFINITE : 0) | (f & kFlagTwice ? SPEC_REQ_BAD_LIST : 0);
+}
+
 template <bool BF16>
 __global__ __launch_bounds__(kSegThreads) __attribute__((amdgpu_waves_per_eu(8)))
 void distill_stream_kernel(DistillArgs a) {
   using Seg = RowSeg<BF16>;
   constexpr int EPV = Seg::EPV;
-  __shared__ uint32_t bits[kListWords];
+  extern __shared__ __attribute__((aligned(16))) uint32_t bits[];   // listed tokens of the segment
   __shared__ uint32_t xbits;
   __shared__ SegSumShared ss;
+  __shared__ ListShared ls;
   __shared__ int sflags;
   const int r = (int)(blockIdx.x / (unsigned)a.nseg), seg = (int)(blockIdx.x - (unsigned)r * a.nseg);
   const int i = r / a.G, k = r - i * a.G;
   const int L = a.lengths ? a.lengths[i] : a.G;
   const float T = a.temperature[i];
-  if (k >= L || L > a.G || !(T > 0.f && T < INFINITY)) return;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int tid = threadIdx.x;
+  if (k >= L || L > a.G || !(T > 0.f && T < INFINITY)) {
+    if (a.nseg == 1 && tid == 0) {
+      a.loss[r] = 0.f;
+      a.saved[(size_t)r * SPEC_DISTILL_SAVED] = NAN;
+      a.row_status[r] = 0;
+    }
+    return;
+  }
   const int e0 = min(tid, a.K - 1);
   const int id = a.ids[(size_t)r * a.K + e0];
   const float val = a.values[(size_t)r * a.K + e0];
@@ -81,230 +228,148 @@ void distill_stream_kernel(DistillArgs a) {
   uint4 d[kSegVecs];
   float x = g.load_scalar(row);
   g.load(row, d);
-  for (int w = tid; w < kListWords; w += kSegThreads) bits[w] = 0;
+  const int words = ((g.ve - g.vb) * EPV + 127) / 128;   // 16 bytes each
+  for (int w = tid; w < words; w += kSegThreads) reinterpret_cast<uint4*>(bits)[w] = make_uint4(0, 0, 0, 0);
   if (tid == 0) xbits = sflags = 0;
   lds_barrier();
-  if (tid < a.K && used_entry(id, val)) {
-    if (id < 0 || id >= a.V) {
-      if (seg == 0) atomicOr(&sflags, kFlagToken);
-    } else {
-      const int body = id - g.head, rel = body - g.vb * EPV;
-      if (id < g.head || id >= g.tail0) {
-        if (seg == 0) {
-          const uint32_t bit = 1u << (id < g.head ? id : g.head + (id - g.tail0));
-          if (atomicOr(&xbits, bit) & bit) atomicOr(&sflags, kFlagTwice);
-        }
-      } else if (rel >= 0 && body < g.ve * EPV) {
-        const uint32_t bit = 1u << (rel & 31);
-        if (atomicOr(&bits[rel >> 5], bit) & bit) atomicOr(&sflags, kFlagTwice);
+  const bool listed = tid < a.K && used_entry(id, val) && id >= 0 && id < a.V;
+  if (tid < a.K && a.nseg == 1) {
+    ls.id[tid] = id;
+    ls.val[tid] = val;
+    ls.z[tid] = load_elem<BF16>(row, listed ? id : 0);
+  }
+  if (listed) {
+    const int body = id - g.head, rel = body - g.vb * EPV;
+    if (id < g.head || id >= g.tail0) {
+      if (seg == 0) {
+        const uint32_t bit = 1u << (id < g.head ? id : g.head + (id - g.tail0));
+        if (atomicOr(&xbits, bit) & bit) atomicOr(&sflags, kFlagTwice);
       }
+    } else if (rel >= 0 && body < g.ve * EPV) {
+      const uint32_t bit = 1u << (rel & 31);
+      if (atomicOr(&bits[rel >> 5], bit) & bit) atomicOr(&sflags, kFlagTwice);
     }
   }
   lds_barrier();
-  float c_hi, c_lo;
-  split_scale(T, c_hi, c_lo);
   if (tid < g.nx && ((xbits >> tid) & 1u)) x = -INFINITY;
-  RunningSum sum{kNoReference, 0.f, 0};
   const uint8_t* bytes = reinterpret_cast<const uint8_t*>(bits);
-  // vector j without its listed tokens
-  auto unlisted = [&](uint4 v, int j) -> uint4 {
-    const int lv = j * kSegThreads + tid;
+  // vector v (in the body) without its listed tokens
+  auto unlisted = [&](uint4 q, int v) -> uint4 {
+    const int lv = v - g.vb;
     uint32_t w;
     if constexpr (BF16) w = bytes[lv];
     else w = (bytes[lv >> 1] >> ((lv & 1) * 4)) & 15u;
     if (w) {
-      if constexpr (BF16) {
-        uint32_t q[4] = {v.x, v.y, v.z, v.w};
+      uint32_t p[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          if (w & (1u << (2 * h))) q[h] = (q[h] & 0xffff0000u) | 0xff80u;
-          if (w & (2u << (2 * h))) q[h] = (q[h] & 0xffffu) | 0xff800000u;
-        }
-        v = make_uint4(q[0], q[1], q[2], q[3]);
-      } else {
-        if (w & 1u) v.x = 0xff800000u;
-        if (w & 2u) v.y = 0xff800000u;
-        if (w & 4u) v.z = 0xff800000u;
-        if (w & 8u) v.w = 0xff800000u;
+      for (int h = 0; h < 4; ++h) {
+        uint32_t m;   // ones over the listed values of the word
+        if constexpr (BF16)
+          m = ((uint32_t)__builtin_amdgcn_sbfe((int)w, 2 * h, 1) & 0xffffu) |
+              ((uint32_t)__builtin_amdgcn_sbfe((int)w, 2 * h + 1, 1) & 0xffff0000u);
+        else
+          m = (uint32_t)__builtin_amdgcn_sbfe((int)w, h, 1);
+        p[h] = (p[h] & ~m) | (Seg::kNegInf & m);
       }
+      q = make_uint4(p[0], p[1], p[2], p[3]);
     }
-    return v;
+    return q;
   };
+  float zm = x;
 #pragma unroll
   for (int j = 0; j < kSegVecs; ++j) {
-    if (g.vb + j * kSegThreads < g.ve) {
-      uint4 v = unlisted(d[j], j);
-      if (g.vb + j * kSegThreads + tid >= g.ve) v = make_uint4(Seg::kNegInf, Seg::kNegInf, Seg::kNegInf, Seg::kNegInf);
+    const int v = g.vb + j * kSegThreads + tid;
+    if (v - tid < g.ve) {
       float z[EPV];
-      Seg::unpack(v, z);
-      add_terms<EPV>(sum, z, c_hi, c_lo);
+      Seg::unpack(unlisted(d[j], min(v, g.ve - 1)), z);
+#pragma unroll
+      for (int e = 0; e < EPV; ++e) zm = fmaxf(zm, z[e]);   // past the end: the last vector again
     }
-    asm volatile("" : "+v"(sum.S));   // one vector's values at a time: registers
+    asm volatile("" : "+v"(zm));
   }
+  forget(d);
+  const Reference rf = pick_reference(ss, zm, T);
+  float S = 0.f;
+  g.walk(row, d, [&](int v, const uint4& q) {
+    float z[EPV];
+    Seg::unpack(unlisted(q, min(v, g.ve - 1)), z);
+    S += exp_sum<EPV>(z, rf.c_f, rf.M);
+    asm volatile("" : "+v"(S));   // one vector's values at a time: registers
+  });
   if (g.nx > 0) {
     const float z1[1] = {x};
-    add_terms<1>(sum, z1, c_hi, c_lo);
+    S += exp_sum<1>(z1, rf.c_f, rf.M);
   }
   int bad;
-  const SegSum t = segment_sum<BF16>(ss, sum, [&](int j) { return unlisted(g.reload(row, j), j); }, x, c_hi, c_lo, bad);
-  if (tid == 0) a.segs[(size_t)r * a.nseg + seg] = DistillSeg{t.sum, t.ref, sflags | (bad ? kFlagBad : 0), 0};
+  const SegSum t = segment_sum<BF16>(
+      ss, S, rf, T, g,
+      [&](int v) { return unlisted(reinterpret_cast<const uint4*>(row + (size_t)g.head * Seg::ES)[v], v); }, x, bad);
+  const int flags = sflags | (bad ? kFlagBad : 0);
+  if (a.nseg == 1) {
+    if (tid < SPEC_WAVE) finish_row(ls, a, (size_t)r, tid == 0 ? t.sum : 0.0, t.ref, row_flags(flags), T);
+  } else if (tid == 0) {
+    a.segs[(size_t)r * a.nseg + seg] = DistillSeg{t.sum, t.ref, flags, 0};
+  }
 }
 
-__device__ __forceinline__ double wave_max_d(double x) {
-  return wave_reduce(x, [](double p, double q) { return fmax(p, q); });
-}
+// One wave per row of several segments.
+constexpr int kFinishWaves = 4;
 
-// Waves of a workgroup at most; entries of a list per lane (one for K <= 64, else four).
-constexpr int finish_waves(int entries) { return entries == 1 ? 16 : 8; }
-
-template <bool BF16, int kLaneEntries>
-__global__ __launch_bounds__(finish_waves(kLaneEntries) * SPEC_WAVE) void distill_finish_kernel(DistillArgs a) {
-  __shared__ int sst;
-  const int i = (int)blockIdx.x, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int nw = (int)blockDim.x >> 6;
-  const int G = a.G, K = a.K, V = a.V;
-  const int L = a.lengths ? a.lengths[i] : G;
+template <bool BF16>
+__global__ __launch_bounds__(kFinishWaves * SPEC_WAVE) void distill_finish_kernel(DistillArgs a) {
+  __shared__ ListShared ls[kFinishWaves];
+  const int wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
+  const int64_t r = (int64_t)blockIdx.x * kFinishWaves + wave;
+  if (r >= (int64_t)a.B * a.G) return;
+  const int i = (int)(r / a.G), k = (int)(r - (int64_t)i * a.G);
+  const int L = a.lengths ? a.lengths[i] : a.G;
   const float T = a.temperature[i];
-  int st = 0;
-  if (L < 0 || L > G) st = SPEC_REQ_BAD_LENGTH;
-  else if (!(T > 0.f && T < INFINITY)) st = SPEC_REQ_BAD_TEMPERATURE;
-  if (tid == 0) sst = st;
-  __syncthreads();
-  const double Td = (double)T;
-  for (int k = wave; k < G; k += nw) {
-    const size_t r = (size_t)i * G + k;
-    double* sv = a.saved + r * SPEC_DISTILL_SAVED;
-    bool live = st == 0 && k < L;
-    double loss = 0.0;
-    if (live) {
-      // every load of the row at once: a lane's entries, and a segment per lane (at most 16)
-      const DistillSeg* p = a.segs + r * a.nseg;
-      int id[kLaneEntries];
-      float val[kLaneEntries];
-#pragma unroll
-      for (int u = 0; u < kLaneEntries; ++u) {
-        const int e = min(lane + u * SPEC_WAVE, K - 1);
-        id[u] = a.ids[r * K + e];
-        val[u] = a.values[r * K + e];
-      }
-      const DistillSeg mine = p[min(lane, a.nseg - 1)];
-      const float tl = a.teacher_lse ? a.teacher_lse[r] : 0.f;
-      int rst = 0, any = 0, nused = 0;
-      float zv[kLaneEntries];
-#pragma unroll
-      for (int u = 0; u < kLaneEntries; ++u) {
-        const bool used = lane + u * SPEC_WAVE < K && used_entry(id[u], val[u]);
-        any |= used;
-        if (used && (id[u] < 0 || id[u] >= V)) rst |= SPEC_REQ_BAD_TOKEN;
-        if (!used || id[u] < 0 || id[u] >= V) id[u] = -1;
-        zv[u] = load_elem<BF16>(reinterpret_cast<const char*>(a.draft) + r * (size_t)V * (BF16 ? 2 : 4),
-                                max(id[u], 0));
-      }
-      live = __ballot(any) != 0;
-      if (live) {
-        const double c = kLog2eSeg / Td;   // exponents in powers of two
-        double tv[kLaneEntries], zq[kLaneEntries], tmax = -INFINITY, zmax = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < kLaneEntries; ++u) {
-          const bool on = id[u] >= 0;
-          if (on && (!(val[u] < INFINITY) || !(zv[u] < INFINITY))) rst |= SPEC_REQ_NONFINITE;
-          nused += on;
-          tv[u] = on ? (double)val[u] * c : -INFINITY;
-          zq[u] = on ? (double)zv[u] * c : -INFINITY;
-          tmax = fmax(tmax, tv[u]);
-          zmax = fmax(zmax, zq[u]);
-        }
-        const bool seg_on = lane < a.nseg && mine.sum > 0.0;
-        if (lane < a.nseg) {
-          if (mine.flags & kFlagBad) rst |= SPEC_REQ_NONFINITE;
-          if (mine.flags & kFlagToken) rst |= SPEC_REQ_BAD_TOKEN;
-          if (mine.flags & kFlagTwice) rst |= SPEC_REQ_BAD_LIST;
-        }
-        // outside the list: out * 2^mo, lo its log2
-        const double mo = wave_max_d(seg_on ? mine.ref : -INFINITY);
-        const bool outside = mo > -INFINITY;
-        tmax = wave_max_d(tmax);
-        zmax = fmax(wave_max_d(zmax), mo);
-        nused = wave_sum_i(nused);
-        const bool tail = a.teacher_lse != nullptr;
-        if (tail && !(fabsf(tl) < INFINITY)) rst |= SPEC_REQ_NONFINITE;
-        if (!(zmax > -INFINITY)) rst |= SPEC_REQ_NONFINITE;
-        rst = wave_or_i(rst);
-        if (rst == 0) {
-          const double out = wave_sum(seg_on ? mine.sum * exp2(mine.ref - mo) : 0.0);
-          double el[kLaneEntries], te[kLaneEntries], lsum = 0.0, tsum = 0.0;
-#pragma unroll
-          for (int u = 0; u < kLaneEntries; ++u) {
-            el[u] = te[u] = 0.0;
-            if (u * SPEC_WAVE < K) {
-              el[u] = exp2(zq[u] - zmax);
-              te[u] = exp2(tv[u] - tmax);
-            }
-            lsum += el[u];
-            tsum += te[u];
-          }
-          lsum = wave_sum(lsum);
-          tsum = wave_sum(tsum);
-          // in logs: the tail may lie hundreds of nats below the list
-          const double lo = outside ? mo - zmax + log2(out) : -INFINITY;
-          const double tot = exp2(lo) + lsum, lt = log2(tot);
-          const double t = tail ? (double)tl * kLog2eSeg : tmax + log2(tsum);   // log2 of p's normaliser
-          const double ps = exp2(tmax - t);
-          const double lrs = lo - lt, rs = exp2(lrs);
-          const double rt = (tail && nused < V) ? fmax(0.0, 1.0 - tsum * ps) : 0.0;
-          double ars, bv;   // a r_s: q a = (q / r_s) (a r_s) outside the list, finite however small r_s
-          double sum = 0.0, qs = 0.0;
-#pragma unroll
-          for (int u = 0; u < kLaneEntries; ++u) {
-            if (id[u] < 0) continue;
-            const double pe = te[u] * ps, qe = el[u] / tot;
-            if (a.mode == SPEC_DISTILL_KL) {
-              if (pe > 0.0) sum += pe * ((tv[u] - t) - (zq[u] - zmax - lt));
-            } else if (pe > qe) {
-              sum += pe - qe;
-              qs += qe;
-            }
-          }
-          loss = wave_sum(sum);
-          if (a.mode == SPEC_DISTILL_KL) {
-            bv = 1.0;
-            ars = rs - rt;
-            if (rt > 0.0) loss += rt * (log2(rt) - lrs);   // +inf when the draft leaves no mass there
-            loss *= kLn2Seg;
-          } else {
-            const bool up = rt > rs;
-            if (up) loss += rt - rs;
-            bv = wave_sum(qs) + (up ? rs : 0.0);
-            ars = (bv - (up ? 1.0 : 0.0)) * rs;
-          }
-          if (lane == 0) {
-            // q / r_s = exp2((z - m) c - sv[1]): the logit nearest the largest exponent as reference
-            const float m = outside ? (float)(mo / c) : 0.f;
-            sv[0] = (double)m;
-            sv[1] = outside ? mo - (double)m * c + log2(out) : 0.0;
-            sv[2] = outside ? ars : 0.0;
-            sv[3] = bv;
-            sv[4] = t;
-            sv[5] = zmax + lt;
-          }
-        } else if (lane == 0) {
-          atomicOr(&sst, rst);
-        }
-      }
-    }
+  if (k >= L || L > a.G || !(T > 0.f && T < INFINITY)) {
     if (lane == 0) {
-      a.loss[r] = (float)loss;
-      if (!live) sv[0] = NAN;
+      a.loss[r] = 0.f;
+      a.saved[(size_t)r * SPEC_DISTILL_SAVED] = NAN;
+      a.row_status[r] = 0;
+    }
+    return;
+  }
+  const DistillSeg mine = a.segs[(size_t)r * a.nseg + min(lane, a.nseg - 1)];
+  const bool on = lane < a.nseg;
+  const char* row = reinterpret_cast<const char*>(a.draft) + (size_t)r * (size_t)a.V * RowSeg<BF16>::ES;
+  int id[SPEC_MAX_TEACHER_K / SPEC_WAVE];
+  float val[SPEC_MAX_TEACHER_K / SPEC_WAVE];
+#pragma unroll
+  for (int u = 0; u < SPEC_MAX_TEACHER_K / SPEC_WAVE; ++u) {
+    const size_t e = (size_t)r * a.K + min(lane + u * SPEC_WAVE, a.K - 1);
+    id[u] = a.ids[e];
+    val[u] = a.values[e];
+  }
+#pragma unroll
+  for (int u = 0; u < SPEC_MAX_TEACHER_K / SPEC_WAVE; ++u) {
+    const float z = load_elem<BF16>(row, id[u] >= 0 && id[u] < a.V ? id[u] : 0);
+    if (lane + u * SPEC_WAVE < a.K) {
+      ls[wave].id[lane + u * SPEC_WAVE] = id[u];
+      ls[wave].val[lane + u * SPEC_WAVE] = val[u];
+      ls[wave].z[lane + u * SPEC_WAVE] = z;
     }
   }
-  __syncthreads();
-  st = sst;
-  if (tid == 0 && a.status) a.status[i] = st;
-  if (st)
-    for (int k = tid; k < G; k += (int)blockDim.x) {
-      a.loss[(size_t)i * G + k] = NAN;
-      a.saved[((size_t)i * G + k) * SPEC_DISTILL_SAVED] = NAN;
-    }
+  finish_row(ls[wave], a, (size_t)r, on ? mine.sum : 0.0, mine.ref, row_flags(on ? mine.flags : 0), T);
+}
+
+// One wave per request.
+__global__ __launch_bounds__(256) void distill_status_kernel(DistillArgs a) {
+  const int i = (int)blockIdx.x * 4 + ((int)threadIdx.x >> 6), k = (int)threadIdx.x & 63;
+  if (i >= a.B) return;
+  const int L = a.lengths ? a.lengths[i] : a.G;
+  const float T = a.temperature[i];
+  const size_t r = (size_t)i * a.G + min(k, a.G - 1);
+  int st = wave_or_i(a.row_status[r]);
+  if (L < 0 || L > a.G) st = SPEC_REQ_BAD_LENGTH;
+  else if (!(T > 0.f && T < INFINITY)) st = SPEC_REQ_BAD_TEMPERATURE;
+  if (k == 0 && a.status) a.status[i] = st;
+  if (st != 0 && k < a.G) {
+    a.loss[r] = NAN;
+    a.saved[r * SPEC_DISTILL_SAVED] = NAN;
+  }
 }
 
 // Workgroup barrier behind which every load and store issued before it is complete.
@@ -393,8 +458,7 @@ __global__ __launch_bounds__(kSegThreads) void distill_grad_kernel(DistillArgs a
   if (tid < g.nx) store_elem<BF16>(out, g.id_of_scalar(tid), grad_of(x));
   memory_barrier();   // the segment's stores are done: the listed tokens' go over them
   if (id >= 0) {
-    const double Td = (double)T;
-    const double c2 = kLog2eSeg / Td;
+    const double c2 = scale_of(T);
     const double q = exp2((double)ze * c2 - sv[5]), p = exp2((double)val * c2 - sv[4]);
     const double c = a.mode == SPEC_DISTILL_KL ? p : (p > q ? q : 0.0);
     store_elem<BF16>(out, id, (float)(s * (q * sv[3] - c)));
@@ -412,7 +476,8 @@ using namespace spec;
 
 extern "C" size_t spec_distill_workspace_size(int32_t B, int32_t gamma, int32_t V, int32_t K) {
   if (!list_ok(B, gamma, V, SPEC_BF16, K)) return 0;
-  return round256((size_t)B * gamma * row_segments(V, SPEC_F32) * sizeof(DistillSeg));
+  const size_t rows = (size_t)B * gamma;
+  return round256(rows * kMaxSegs * sizeof(DistillSeg)) + round256(rows * sizeof(int32_t));
 }
 
 extern "C" int32_t spec_distill_loss(int32_t B, int32_t gamma, int32_t V, int32_t dtype, const void* draft_logits,
@@ -429,26 +494,30 @@ extern "C" int32_t spec_distill_loss(int32_t B, int32_t gamma, int32_t V, int32_
     return SPEC_ERR_WORKSPACE;
   DistillArgs a{};
   a.B = B; a.G = gamma; a.V = V; a.K = K; a.mode = mode;
-  a.nseg = row_segments(V, dtype);
   const uint64_t rows = (uint64_t)B * gamma;
+  a.nseg = row_segments((int64_t)rows, V, dtype);
   if (rows * a.nseg * kSegThreads > 0xffffffffull) return SPEC_ERR_UNSUPPORTED;
-  const int entries = K <= SPEC_WAVE ? 1 : SPEC_MAX_TEACHER_K / SPEC_WAVE;
-  const int waves = gamma < finish_waves(entries) ? gamma : finish_waves(entries);
-  if ((uint64_t)B * waves * SPEC_WAVE > 0xffffffffull) return SPEC_ERR_UNSUPPORTED;
   a.draft = draft_logits; a.ids = teacher_ids; a.values = teacher_values; a.teacher_lse = teacher_lse;
   a.lengths = lengths; a.temperature = temperature; a.loss = loss_out; a.saved = saved_out; a.status = status;
   a.segs = reinterpret_cast<DistillSeg*>(workspace);
+  a.row_status = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(workspace) +
+                                            round256(rows * kMaxSegs * sizeof(DistillSeg)));
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const dim3 grid((unsigned)(rows * a.nseg)), fgrid((unsigned)B), fblock((unsigned)(waves * SPEC_WAVE));
+  const dim3 grid((unsigned)(rows * a.nseg));
+  const int elems = dtype == SPEC_BF16 ? 8 : 4, vecs = (V / elems + a.nseg - 1) / a.nseg;
+  const unsigned lds = (unsigned)((vecs * elems + 127) / 128 * 16 + 16);
   if (dtype == SPEC_BF16) {
-    hipLaunchKernelGGL(distill_stream_kernel<true>, grid, dim3(kSegThreads), 0, s, a);
-    if (entries == 1) hipLaunchKernelGGL((distill_finish_kernel<true, 1>), fgrid, fblock, 0, s, a);
-    else hipLaunchKernelGGL((distill_finish_kernel<true, 4>), fgrid, fblock, 0, s, a);
+    hipLaunchKernelGGL(distill_stream_kernel<true>, grid, dim3(kSegThreads), lds, s, a);
+    if (a.nseg > 1)
+      hipLaunchKernelGGL(distill_finish_kernel<true>, dim3((unsigned)((rows + kFinishWaves - 1) / kFinishWaves)),
+                         dim3(kFinishWaves * SPEC_WAVE), 0, s, a);
   } else {
-    hipLaunchKernelGGL(distill_stream_kernel<false>, grid, dim3(kSegThreads), 0, s, a);
-    if (entries == 1) hipLaunchKernelGGL((distill_finish_kernel<false, 1>), fgrid, fblock, 0, s, a);
-    else hipLaunchKernelGGL((distill_finish_kernel<false, 4>), fgrid, fblock, 0, s, a);
+    hipLaunchKernelGGL(distill_stream_kernel<false>, grid, dim3(kSegThreads), lds, s, a);
+    if (a.nseg > 1)
+      hipLaunchKernelGGL(distill_finish_kernel<false>, dim3((unsigned)((rows + kFinishWaves - 1) / kFinishWaves)),
+                         dim3(kFinishWaves * SPEC_WAVE), 0, s, a);
   }
+  hipLaunchKernelGGL(distill_status_kernel, dim3((unsigned)(B + 3) / 4), dim3(256), 0, s, a);
   return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
 }
 
@@ -464,7 +533,8 @@ extern "C" int32_t spec_distill_loss_backward(int32_t B, int32_t gamma, int32_t 
   if (!aligned16(draft_logits) || !aligned16(grad_out)) return SPEC_ERR_INVALID_ARG;
   DistillArgs a{};
   a.B = B; a.G = gamma; a.V = V; a.K = K; a.mode = mode;
-  a.nseg = row_segments(V, dtype);
+  const int vecs = V / (dtype == SPEC_BF16 ? 8 : 4);
+  a.nseg = vecs <= kSegChunk ? 1 : (vecs + kSegChunk - 1) / kSegChunk;   // a chunk each: held in registers
   const uint64_t rows = (uint64_t)B * gamma;
   if (rows * a.nseg * kSegThreads > 0xffffffffull) return SPEC_ERR_UNSUPPORTED;
   a.draft = draft_logits; a.ids = teacher_ids; a.values = teacher_values; a.temperature = temperature;

@@ -1,10 +1,10 @@
-// One segment of a logit row held in the registers of a workgroup (training kernels).
+// A logit row streamed by a workgroup (training kernels).
 //
-// A row's 16-byte body is cut into segments of at most kSegThreads * kSegVecs vectors (64 KB), one
-// workgroup each; every thread issues its kSegVecs loads at once and keeps the vectors, so a segment
-// is read from memory once however many passes its kernel makes over it.  The elements before the
-// first and after the last whole vector (at most 7 + 7, rows that do not start or end on a 16-byte
-// boundary) belong to segment 0, one per thread.
+// A row's 16-byte body is cut into `nseg` segments, one workgroup each; a workgroup walks its segment in
+// chunks of kSegThreads * kSegVecs vectors (64 KB), every thread holding kSegVecs of them in registers
+// and issuing the next chunk's load as soon as it takes a vector.  The elements before the first and
+// after the last whole vector (at most 7 + 7, rows that do not start or end on a 16-byte boundary)
+// belong to segment 0, one per thread.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -19,12 +19,24 @@ namespace spec {
 constexpr int kSegThreads = 512;
 constexpr int kSegWaves = kSegThreads / SPEC_WAVE;
 constexpr int kSegVecs = 8;   // 16-byte vectors per thread: 32 registers, 8 waves per SIMD
+constexpr int kSegWorkgroups = 512;   // a call's workgroups, at least, where rows are long enough
 constexpr double kLog2eSeg = 1.44269504088896340736;
 
-inline int row_segments(int V, int dtype) {
+constexpr int kSegChunk = kSegThreads * kSegVecs;
+constexpr int kMaxSegs = 16;
+constexpr int kMaxSegVecs = 5 * kSegChunk;   // of a segment (its bitmap of listed tokens takes 20 KB)
+
+// Segments of a row of V logits in a call of `rows` rows: two workgroups per CU at least, none shorter than a
+// chunk.  One segment per row where there are rows enough: a workgroup's setup, and the joining of a row's
+// segments, cost more than the idle CUs of a last round (lists of 256 on 672 rows of 129280 bf16: 84 us
+// whole, 123 us in three segments).
+inline int row_segments(int64_t rows, int V, int dtype) {
   const int vecs = V / (dtype == SPEC_BF16 ? 8 : 4);
-  const int cap = kSegThreads * kSegVecs;
-  return vecs <= cap ? 1 : (vecs + cap - 1) / cap;
+  const int least = (vecs + kMaxSegVecs - 1) / kMaxSegVecs, most = (vecs + kSegChunk - 1) / kSegChunk;
+  const int64_t want = (kSegWorkgroups + rows - 1) / rows;
+  int n = want > most ? most : (int)want;
+  if (n < least) n = least;
+  return n < 1 ? 1 : n;   // at most kMaxSegs: V <= SPEC_MAX_V (fp32: half)
 }
 
 template <bool BF16>
@@ -48,26 +60,40 @@ struct RowSeg {
   // token id of element e of body vector v, and of the thread's scalar element
   __device__ __forceinline__ int id_of(int v, int e) const { return head + v * EPV + e; }
   __device__ __forceinline__ int id_of_scalar(int t) const { return t < head ? t : tail0 + (t - head); }
-  // the thread's vectors (-inf past the segment); loads are issued together, clamped in bounds
+  // the thread's vectors of the first chunk; loads issued together, clamped to the last vector (-inf when
+  // the segment has none)
   __device__ __forceinline__ void load(const char* row, uint4 (&d)[kSegVecs]) const {
+    const uint4* vp = reinterpret_cast<const uint4*>(row + (size_t)head * ES);
+    if (vb < ve) {
+#pragma unroll
+      for (int j = 0; j < kSegVecs; ++j) d[j] = load_nt(vp + min(vb + j * kSegThreads + (int)threadIdx.x, ve - 1));
+    } else {
+#pragma unroll
+      for (int j = 0; j < kSegVecs; ++j) d[j] = make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
+    }
+  }
+  // take(v, x) for every vector v of the chunk at c that the thread holds, x its 16 bytes (-inf past the
+  // end); each register is refilled with the next chunk's vector.  The loads stand outside of every
+  // branch (clamped past the end): a load that only some paths issue makes each wait one for every load
+  // in flight
+  template <class Take>
+  __device__ __forceinline__ void walk_chunk(const char* row, int c, uint4 (&d)[kSegVecs], Take take) const {
     const uint4* vp = reinterpret_cast<const uint4*>(row + (size_t)head * ES);
 #pragma unroll
     for (int j = 0; j < kSegVecs; ++j) {
-      d[j] = make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
-      if (vb + j * kSegThreads < ve)
-        d[j] = load_nt(vp + min(vb + j * kSegThreads + (int)threadIdx.x, ve - 1));
+      const int v = c + j * kSegThreads + (int)threadIdx.x;
+      if (c + j * kSegThreads < ve) {
+        uint4 x = d[j];
+        if (c + (j + 1) * kSegThreads > ve && v >= ve) x = make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
+        take(v, x);
+      }
+      d[j] = load_nt(vp + min(v + kSegChunk, ve - 1));
     }
   }
-  __device__ __forceinline__ void mask(uint4 (&d)[kSegVecs]) const {
-#pragma unroll
-    for (int j = 0; j < kSegVecs; ++j)
-      if (vb + j * kSegThreads + (int)threadIdx.x >= ve) d[j] = make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
-  }
-  // the thread's vector j read once more
-  __device__ __forceinline__ uint4 reload(const char* row, int j) const {
-    const int v = vb + j * kSegThreads + (int)threadIdx.x;
-    return v < ve ? reinterpret_cast<const uint4*>(row + (size_t)head * ES)[v]
-                  : make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
+  template <class Take>
+  __device__ __forceinline__ void walk(const char* row, uint4 (&d)[kSegVecs], Take take) const {
+#pragma unroll 1
+    for (int c = vb; c < ve; c += kSegChunk) walk_chunk(row, c, d, take);
   }
   __device__ __forceinline__ float load_scalar(const char* row) const {
     return (int)threadIdx.x < nx ? load_elem<BF16>(row, id_of_scalar(threadIdx.x)) : -INFINITY;
@@ -93,67 +119,36 @@ __device__ __forceinline__ void forget(uint4 (&d)[kSegVecs]) {
   for (int j = 0; j < kSegVecs; ++j) asm volatile("" : "+v"(d[j].x), "+v"(d[j].y), "+v"(d[j].z), "+v"(d[j].w));
 }
 
-// log2(e) / T as a float pair, c_hi toward zero and c_lo > 0 (so that a logit of -inf gives an
-// exponent of -inf, never NaN); finite for every T > 0 (T towards 0 is the argmax).
+// log2(e) / T, finite in fp32 for every T > 0 (T towards 0 is the argmax); and as a float pair, c_hi toward
+// zero and c_lo > 0 (so that a logit of -inf gives an exponent of -inf, never NaN).
+__device__ __forceinline__ double scale_of(float T) { return fmin(kLog2eSeg / (double)T, 3.4028234663852886e38); }
+
 __device__ __forceinline__ void split_scale(float T, float& c_hi, float& c_lo) {
-  const double c = fmin(kLog2eSeg / (double)T, 3.4028234663852886e38);
+  const double c = scale_of(T);
   c_hi = __double2float_rz(c);
   c_lo = fmaxf((float)(c - (double)c_hi), 1.4e-45f);
 }
 
-// A thread's running sum of exp(z / T) as S 2^M.  M is an integer that only rises, so a rescale is an
-// exact power of two, and the exponent z c - M is formed with one rounding at its own size:
-// fma(z, c_lo, fma(z, c_hi, -M)).  A vector's sum past 2^32 (NaN included) takes the slow branch: M
-// moves up to the vector's largest exponent.  `odd` is set where that cannot be held (NaN, +inf, or an
-// exponent past 2^22, whose neighbours an fp32 reference no longer tells apart): the segment is then
-// summed again by exp_term.
-struct RunningSum {
-  float M, S;
-  int odd;
-};
-
-constexpr float kWideExponent = 0x1p22f;
-
+// Sum of exp2(z c_f - M) over a vector, c_f = log2(e) / T rounded to fp32: one multiply-add per term.  M is
+// an integer, the same for the whole segment: the ceiling of the largest exponent of its first chunk
+// (pick_reference, which keeps that largest logit m).  The rounding of c_f shifts every exponent by
+// z (c - c_f) = m (c - c_f) + (z - m)(c - c_f): the first part is common to the segment and goes into its
+// reference in fp64, the second is at most 2^-25 |z - m| c, and e^-|z - m|/T weighs it.  A later value may
+// pass M by 2^100 before the sum leaves fp32's range (one of 70 T nats more than the largest of 32768);
+// such a segment, one whose first chunk has no value, one with NaN or +inf and one with exponents past
+// 2^22 (an fp32 reference no longer tells their neighbours apart) is summed again by exp_term in
+// segment_sum.
 template <int N>
-__device__ __forceinline__ float exp_sum(const float (&z)[N], float c_hi, float c_lo, float M) {
+__device__ __forceinline__ float exp_sum(const float (&z)[N], float c_f, float M) {
   float e[N];
 #pragma unroll
-  for (int j = 0; j < N; ++j) e[j] = __builtin_amdgcn_exp2f(fmaf(z[j], c_lo, fmaf(z[j], c_hi, -M)));
+  for (int j = 0; j < N; ++j) e[j] = __builtin_amdgcn_exp2f(fmaf(z[j], c_f, -M));
 #pragma unroll
   for (int w = 1; w < N; w <<= 1)
 #pragma unroll
     for (int j = 0; j + w < N; j += 2 * w) e[j] += e[j + w];
   return e[0];
 }
-
-template <int N>
-__device__ __forceinline__ void add_terms(RunningSum& r, const float (&z)[N], float c_hi, float c_lo) {
-  float s = exp_sum<N>(z, c_hi, c_lo, r.M);
-  if (!(s <= 0x1p32f)) {
-    float vm = z[0];
-#pragma unroll
-    for (int j = 1; j < N; ++j) vm = fmaxf(vm, z[j]);
-    const float mc = ceilf(vm * c_hi);
-    s = 0.f;
-    if (!(fabsf(mc) < kWideExponent)) {
-      r.odd = 1;
-    } else {
-      if (mc > r.M) {
-        const float d = r.M - mc;
-        r.S = d < -126.f ? 0.f : ldexpf(r.S, (int)d);
-        r.M = mc;
-      }
-      s = exp_sum<N>(z, c_hi, c_lo, r.M);
-      if (!(s <= 0x1p32f)) {   // a NaN beside finite values
-        r.odd = 1;
-        s = 0.f;
-      }
-    }
-  }
-  r.S += s;
-}
-
-constexpr float kNoReference = -0x1p24f;   // below every exponent that is summed: the first term raises it
 
 // exp2((z - m) c) against the segment's largest value m: the difference first, so that it, not the
 // value, sets the rounding, whatever the values' size.
@@ -167,52 +162,72 @@ struct SegSum {
   double sum, ref;
 };
 
-// Scratch of segment_sum.
+// Scratch of pick_reference and segment_sum.
 struct SegSumShared {
   double s[kSegWaves];
   float m[kSegWaves];
   int odd[kSegWaves];
 };
 
-// The workgroup's sum (and whether a NaN or +inf was among the values) from its threads' running sums;
-// every thread gets the result.  again(j) reads the thread's vector j once more (-inf where there is
-// none) and x is its scalar: used only when a sum was odd.
+// A segment's scale and reference (see exp_sum).
+struct Reference {
+  double c;      // log2(e) / T
+  float c_f, M;
+  double ref;    // M and the shared part of c_f's rounding: the sum is S * 2^ref
+  bool ok;       // false: there is no reference
+};
+
+// From the workgroup's threads' largest values.
+__device__ __forceinline__ Reference pick_reference(SegSumShared& sh, float zm, float T) {
+  const int wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
+  zm = wave_max(zm);
+  if (lane == 0) sh.m[wave] = zm;
+  lds_barrier();
+#pragma unroll
+  for (int w = 0; w < kSegWaves; ++w) zm = fmaxf(zm, sh.m[w]);
+  Reference r;
+  r.c = scale_of(T);
+  r.c_f = (float)r.c;
+  r.M = ceilf(zm * r.c_f);
+  r.ok = fabsf(r.M) < 0x1p22f;
+  if (!r.ok) r.M = 0.f;
+  r.ref = (double)r.M + (r.ok ? (double)zm * (r.c - (double)r.c_f) : 0.0);
+  return r;
+}
+
+// The workgroup's sum (and whether a NaN or +inf was among the values) from its threads' sums S1; every
+// thread gets the result.  again(v) reads body vector v once more and x is the thread's scalar: used
+// only when a sum left the range, or without a reference.
 template <bool BF16, class Again>
-__device__ __forceinline__ SegSum segment_sum(SegSumShared& sh, const RunningSum& r, Again again, float x, float c_hi,
-                                              float c_lo, int& bad) {
+__device__ __forceinline__ SegSum segment_sum(SegSumShared& sh, float S1, const Reference& rf, float T,
+                                              const RowSeg<BF16>& g, Again again, float x, int& bad) {
   using Seg = RowSeg<BF16>;
   const int wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
-  const float wm = wave_max(r.M);
-  const double ws = wave_sum(ldexp((double)r.S, (int)fmaxf(r.M - wm, -2000.f)));
-  const int wo = __ballot(r.odd) != 0;
+  const double ws = wave_sum((double)S1);
+  const int wo = __ballot(!(S1 <= 0x1p100f)) != 0;
   if (lane == 0) {
     sh.s[wave] = ws;
-    sh.m[wave] = wm;
     sh.odd[wave] = wo;
   }
   __syncthreads();
-  float M = sh.m[0];
-  int odd = sh.odd[0];
+  SegSum t{0.0, rf.ref};
+  int odd = !rf.ok;
 #pragma unroll
-  for (int w = 1; w < kSegWaves; ++w) {
-    M = fmaxf(M, sh.m[w]);
+  for (int w = 0; w < kSegWaves; ++w) {
+    t.sum += sh.s[w];
     odd |= sh.odd[w];
   }
-  SegSum t{0.0, (double)M};
   bad = 0;
-  // no term raised the reference: every value is -inf or lies below it (rows of a type's lowest value)
-  odd |= M == kNoReference;
-  if (!odd) {
-#pragma unroll
-    for (int w = 0; w < kSegWaves; ++w) t.sum += ldexp(sh.s[w], (int)fmaxf(sh.m[w] - M, -2000.f));
-    return t;
-  }
+  if (!odd) return t;
+  t.sum = 0.0;
+  float c_hi, c_lo;
+  split_scale(T, c_hi, c_lo);
   __syncthreads();
   float m = x;
 #pragma unroll 1
-  for (int j = 0; j < kSegVecs; ++j) {
+  for (int v = g.vb + (int)threadIdx.x; v < g.ve; v += kSegThreads) {
     float z[Seg::EPV];
-    Seg::unpack(again(j), z);
+    Seg::unpack(again(v), z);
 #pragma unroll
     for (int e = 0; e < Seg::EPV; ++e) m = fmaxf(m, z[e]);
   }
@@ -223,9 +238,9 @@ __device__ __forceinline__ SegSum segment_sum(SegSumShared& sh, const RunningSum
   const float mr = m > -INFINITY ? m : 0.f;
   float S = exp_term(x, mr, c_hi, c_lo);
 #pragma unroll 1
-  for (int j = 0; j < kSegVecs; ++j) {
+  for (int v = g.vb + (int)threadIdx.x; v < g.ve; v += kSegThreads) {
     float z[Seg::EPV];
-    Seg::unpack(again(j), z);
+    Seg::unpack(again(v), z);
 #pragma unroll
     for (int e = 0; e < Seg::EPV; ++e) S += exp_term(z[e], mr, c_hi, c_lo);
   }

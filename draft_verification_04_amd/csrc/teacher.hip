@@ -2,16 +2,18 @@
 // token ids (value descending, id ascending) and ln sum_v exp(z_v / T) over the whole row.
 //
 // The lists stand in for the target's rows when a drafter is trained on its distributions (DSpark
-// paper, §3.3), K * 8 bytes in place of V logits.  Two kernels:
-//   teacher_segment_kernel -- one workgroup per (row, segment of at most 64 KB), the segment held in
-//       registers (one read).  Each of the W waves takes the ceil(K / W)-th largest of its lanes' maxima; the
-//       smallest of these over the waves is a bound tau that at least K values of the segment reach,
-//       so the values >= tau hold the segment's K largest.  They go to the workspace as 64-bit keys
-//       (ordered value, complemented id); when more than `cap` reach tau (ties, mostly) the exact
-//       K-th key is found by bisection, reading the segment again (from cache), instead.  The terms
-//       exp(z / T) are summed in fp32 per thread (64 terms) and in fp64 beyond.
-//   teacher_merge_kernel -- one wave per row drops the keys below the largest tau, keeps the K largest
-//       of the rest in order, and writes them, the log normaliser and the status.
+// paper, §3.3), K * 8 bytes in place of V logits.  The work is one read of the rows:
+//   teacher_row_kernel -- one workgroup per row (or segment of one, when there are few rows).  A bound
+//       tau that at least K values reach comes from the lanes' running maxima: each of the W waves takes
+//       the ceil(K / W)-th largest of its lanes', tau is the smallest of these, and it is raised after
+//       the chunks 1, 2, 4 (so about 1.8 K values reach tau per doubling of what was read).  A vector
+//       holding a value >= tau is copied to LDS whole; in the end the candidates >= the last tau are
+//       listed (about 1.8 K), and of a whole row one wave finds the K-th largest among them bit by bit
+//       (select_topk) and the survivors are put in order by counting.  Where too many values reach tau (ties,
+//       rising rows) the K-th key is found by counting over the row again instead.  The terms
+//       exp(z / T) are summed on the way, fp32 per thread and fp64 beyond.
+//   teacher_merge_kernel -- one workgroup per row: the same selection over the lists of a row's segments;
+//       and, also for whole rows, the status of the request.
 #include "common.hpp"
 #include "rowseg.hpp"
 #include "spec_verify.h"
@@ -19,9 +21,7 @@
 namespace spec {
 namespace {
 
-constexpr int kHitCap = 3 * SPEC_MAX_TEACHER_K + 96;
-constexpr int kMergeWaves = 4;      // rows per workgroup of the merge
-constexpr int kMergeRegs = 32;      // keys of the lists a lane of it holds at most
+constexpr int kMergeKeys = 4096;   // keys of a round of the merge
 
 struct TeacherSeg {
   double sum, ref;  // sum of exp(z / T) over the segment: sum * 2^ref
@@ -31,7 +31,7 @@ struct TeacherSeg {
 };
 
 struct TeacherArgs {
-  int B, G, V, K, nseg, cap;
+  int B, G, V, K, nseg, cap, hits;
   const void* target;
   const int32_t* lengths;
   const float* temperature;
@@ -40,33 +40,155 @@ struct TeacherArgs {
   float* lse;
   int32_t* status;
   TeacherSeg* segs;   // [B * G, nseg]
-  uint64_t* keys;     // [B * G, nseg, cap]
+  uint64_t* keys;     // [B * G, nseg, cap] (several segments)
 };
 
+// Ordered value (-0 and 0 are equal) above the complemented id: larger keys come first.
 __device__ __forceinline__ uint64_t pack_key(float z, int id) {
-  return ((uint64_t)order_key(z + 0.f) << 32) | (uint32_t)~id;   // -0 and 0 are equal
+  return ((uint64_t)order_key(z + 0.f) << 32) | (uint32_t)~id;
 }
 
-struct SegShared {
+struct SelectShared {
+  int cnt[2][kSegWaves];   // of the counts over a row
+  int n;
+  uint32_t tie[SPEC_WAVE];
+  uint64_t list[SPEC_MAX_TEACHER_K];
+};
+
+// One wave: keeps the K largest of the n keys (distinct) in LDS, in any order, in sh.list, and their number in
+// sh.n.  One wave, not eight: a few hundred keys are a few per lane, and a step costs a wave the same
+// whatever it holds.  floor_key: a value key that no key lies below.
+__device__ __forceinline__ void select_topk(SelectShared& sh, const uint64_t* keys, int n, int K, uint32_t floor_key) {
+  const int lane = (int)threadIdx.x & 63;
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(keys);   // low word (id), high word (value)
+  constexpr int U = 8;   // reads in flight
+  auto count = [&](bool ids, auto pred) -> int {
+    int c = 0;
+#pragma unroll 1
+    for (int e = lane; e - lane < n; e += U * SPEC_WAVE) {
+      uint32_t h[U], l[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int at = min(e + u * SPEC_WAVE, n - 1);
+        h[u] = words[2 * at + 1];
+        l[u] = ids ? words[2 * at] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) c += (int)__popcll(__ballot(e + u * SPEC_WAVE < n && pred(h[u], l[u])));
+    }
+    return c;
+  };
+  uint32_t th = 0, tl = 0;
+  if (n > K) {
+    // the largest value key that at least K keys reach; the bits above the highest one in which the keys
+    // differ are known
+    uint32_t top = 0;
+    for (int e = lane; e < n; e += SPEC_WAVE) top = max(top, words[2 * e + 1]);
+    top = (uint32_t)wave_max_i((int)(top ^ 0x80000000u)) ^ 0x80000000u;
+    const int high = top == floor_key ? -1 : 31 - __clz((int)(top ^ floor_key));
+    th = high < 0 ? top : (top >> high >> 1) << high << 1;
+    int reach = n;
+#pragma unroll 1
+    for (int bit = high; bit >= 0 && reach != K; --bit) {
+      const uint32_t trial = th | (1u << bit);
+      const int c = count(false, [&](uint32_t h, uint32_t) { return h >= trial; });
+      if (c >= K) {
+        th = trial;
+        reach = c;
+      }
+    }
+    if (reach > K) {   // of the keys at th the largest low words (lowest ids) that fill up K
+      const int above = count(false, [&](uint32_t h, uint32_t) { return h > th; }), need = K - above;
+      if (reach - above <= SPEC_WAVE) {   // a key per lane, its place by counting
+        int m = 0;
+#pragma unroll 1
+        for (int e = lane; e - lane < n; e += SPEC_WAVE) {
+          const int at = min(e, n - 1);
+          const bool tie = e < n && words[2 * at + 1] == th;
+          const unsigned long long b = __ballot(tie);
+          if (tie) sh.tie[m + (int)__popcll(b & ((1ull << lane) - 1))] = words[2 * at];
+          m += (int)__popcll(b);
+        }
+        const uint32_t mine = lane < m ? sh.tie[lane] : 0;
+        int before = 0;
+        for (int e = 0; e < m; ++e) before += sh.tie[e] > mine ? 1 : 0;
+        const unsigned long long last = __ballot(lane < m && before == need - 1);
+        tl = read_lane(mine, (int)__ffsll((long long)last) - 1);
+      } else {
+        tl = 0xfff00000u;
+#pragma unroll 1
+        for (int bit = 19; bit >= 0; --bit) {
+          const uint32_t trial = tl | (1u << bit);
+          const int c = count(true, [&](uint32_t h, uint32_t l) { return h == th && l >= trial; });
+          if (c >= need) tl = trial;
+          if (c == need) break;
+        }
+      }
+    }
+  }
+  int kept = 0;
+#pragma unroll 1
+  for (int e = lane; e - lane < n; e += SPEC_WAVE) {
+    const uint64_t key = keys[min(e, n - 1)];
+    const uint32_t h = (uint32_t)(key >> 32);
+    const bool take = e < n && (h > th || (h == th && (uint32_t)key >= tl));
+    const unsigned long long m = __ballot(take);
+    const int at = kept + (int)__popcll(m & ((1ull << lane) - 1));
+    if (take && at < SPEC_MAX_TEACHER_K) sh.list[at] = key;
+    kept += (int)__popcll(m);
+  }
+  if (lane == 0) sh.n = min(kept, K);
+}
+
+// Writes the n selected keys of row r in order, unused entries behind them.
+__device__ __forceinline__ void write_list(const SelectShared& sh, const TeacherArgs& a, int r, int n) {
+  const int tid = threadIdx.x;
+  if (tid >= a.K) return;
+  const size_t o = (size_t)r * a.K;
+  if (tid < n) {
+    const uint64_t mine = sh.list[tid];
+    int place = 0;
+#pragma unroll 4
+    for (int e = 0; e < n; ++e) place += sh.list[e] > mine ? 1 : 0;
+    a.ids[o + place] = (int)~(uint32_t)mine;
+    a.values[o + place] = key_value((uint32_t)(mine >> 32));
+  } else {
+    a.ids[o + tid] = -1;
+    a.values[o + tid] = -INFINITY;
+  }
+}
+
+__device__ __forceinline__ void write_empty(const TeacherArgs& a, int r, float fill) {
+  const size_t o = (size_t)r * a.K;
+  for (int e = threadIdx.x; e < a.K; e += (int)blockDim.x) {
+    a.ids[o + e] = -1;
+    a.values[o + e] = fill;
+  }
+  if (a.lse && threadIdx.x == 0) a.lse[r] = fill;
+}
+
+struct RowShared {
   SegSumShared sum;
-  uint32_t t[kSegWaves];
-  int cnt[2][kSegWaves];
+  SelectShared sel;
+  uint32_t t[2][kSegWaves];
   int n, nhit;
-  uint4 hit[kHitCap];     // vectors holding a value that reaches tau, and their indices
-  int32_t hit_v[kHitCap];
 };
 
 template <bool BF16>
 __global__ __launch_bounds__(kSegThreads) __attribute__((amdgpu_waves_per_eu(8)))
-void teacher_segment_kernel(TeacherArgs a) {
+void teacher_row_kernel(TeacherArgs a) {
   using Seg = RowSeg<BF16>;
   constexpr int EPV = Seg::EPV;
-  __shared__ SegShared sh;
+  extern __shared__ __attribute__((aligned(16))) char dyn[];
+  __shared__ RowShared sh;
+  uint64_t* keys = reinterpret_cast<uint64_t*>(dyn);                          // [cap] candidates
+  uint4* hit = reinterpret_cast<uint4*>(dyn + (size_t)a.cap * 8);             // [hits] vectors reaching tau
+  int32_t* hit_v = reinterpret_cast<int32_t*>(dyn + (size_t)a.cap * 8 + (size_t)a.hits * 16);
   const int r = (int)(blockIdx.x / (unsigned)a.nseg), seg = (int)(blockIdx.x - (unsigned)r * a.nseg);
   const int i = r / a.G, k = r - i * a.G;
   const int L = a.lengths ? a.lengths[i] : a.G;
   const float T = a.temperature[i];
-  if (k >= L || L > a.G || !(T > 0.f && T < INFINITY)) return;
+  if (k >= L || L > a.G || !(T > 0.f && T < INFINITY)) return;   // the merge kernel fills these rows
   const char* row = reinterpret_cast<const char*>(a.target) + ((size_t)i * (a.G + 1) + k) * (size_t)a.V * Seg::ES;
   const Seg g(row, a.V, seg, a.nseg);
   uint4 d[kSegVecs];
@@ -74,101 +196,123 @@ void teacher_segment_kernel(TeacherArgs a) {
   const float x = g.load_scalar(row);
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   if (tid == 0) sh.n = sh.nhit = 0;
-  float c_hi, c_lo;
-  split_scale(T, c_hi, c_lo);
 
-  RunningSum sum{kNoReference, 0.f, 0};
-  float vm[kSegVecs], zm = x;   // the vectors' largest values
+  float zm = x;   // the lane's largest value so far
+  uint32_t tau = kNegInfKey;
+  float tz = -INFINITY;
+  // waves whose lanes all hold a vector of the segment
+  const int full = min((g.ve - g.vb) >> 6, kSegWaves);
+  const int need = full ? (a.K + full - 1) / full : SPEC_WAVE + 1;
+  int turn = 0;
+  auto raise_tau = [&]() {
+    // the wave's need-th largest lane maximum, bitwise from the top: bf16 keys end at bit 16, and a bound on
+    // fp32 keys need not go below bit 14
+    const uint32_t key = order_key(zm);
+    uint32_t t = need > SPEC_WAVE ? kNegInfKey : 0xffffffffu;
+    if (wave < full && need <= SPEC_WAVE) {
+      t = 0;
+#pragma unroll
+      for (int bit = 31; bit >= (BF16 ? 16 : 14); --bit) {
+        const uint32_t trial = t | (1u << bit);
+        if ((int)__popcll(__ballot(key >= trial)) >= need) t = trial;
+      }
+      if (BF16 && t < 0x80000000u) t |= 0xffffu;
+      t = max(t, kNegInfKey);
+    }
+    if (lane == 0) sh.t[turn][wave] = t;
+    lds_barrier();   // one turn's values are read before the next turn's barrier, and written anew behind it
+    tau = sh.t[turn][0];
+#pragma unroll
+    for (int w = 1; w < kSegWaves; ++w) tau = min(tau, sh.t[turn][w]);
+    tz = key_value(tau);
+    turn ^= 1;
+  };
+  auto largest = [&](const float (&z)[EPV]) {
+    float m = z[0];
+#pragma unroll
+    for (int e = 1; e < EPV; ++e) m = fmaxf(m, z[e]);
+    return m;
+  };
+  // the first bound, from the first chunk's maxima (it stays in registers)
 #pragma unroll
   for (int j = 0; j < kSegVecs; ++j) {
-    vm[j] = -INFINITY;
-    if (g.vb + j * kSegThreads < g.ve) {
-      uint4 v = d[j];
-      if (g.vb + j * kSegThreads + tid >= g.ve) v = make_uint4(Seg::kNegInf, Seg::kNegInf, Seg::kNegInf, Seg::kNegInf);
+    float z[EPV];
+    Seg::unpack(d[j], z);
+    if (g.vb + j * kSegThreads + tid < g.ve) zm = fmaxf(zm, largest(z));
+    asm volatile("" : "+v"(zm));
+  }
+  forget(d);
+  float S = 0.f;
+  const Reference rf = pick_reference(sh.sum, zm, T);
+  raise_tau();
+  int chunk = 0;
+#pragma unroll 1
+  for (int c = g.vb; c < g.ve; c += kSegChunk) {
+    g.walk_chunk(row, c, d, [&](int v, const uint4& q) {
       float z[EPV];
-      Seg::unpack(v, z);
-      add_terms<EPV>(sum, z, c_hi, c_lo);
-      vm[j] = z[0];
-#pragma unroll
-      for (int e = 1; e < EPV; ++e) vm[j] = fmaxf(vm[j], z[e]);
-      zm = fmaxf(zm, vm[j]);
-    }
-    asm volatile("" : "+v"(sum.S), "+v"(vm[j]));   // one vector's values at a time: registers
+      Seg::unpack(q, z);
+      S += exp_sum<EPV>(z, rf.c_f, rf.M);
+      const float m = largest(z);
+      zm = fmaxf(zm, m);
+      if (m >= tz && m > -INFINITY) {   // copied whole; its values are looked at one by one below
+        const int h = atomicAdd(&sh.nhit, 1);
+        if (h < a.hits) {
+          hit[h] = q;
+          hit_v[h] = v;
+        }
+      }
+      asm volatile("" : "+v"(S));   // one vector's values at a time: registers
+    });
+    ++chunk;
+    if (chunk > 1 && (chunk & (chunk - 1)) == 0 && c + kSegChunk < g.ve) raise_tau();
   }
   if (g.nx > 0) {
     const float z1[1] = {x};
-    add_terms<1>(sum, z1, c_hi, c_lo);
+    S += exp_sum<1>(z1, rf.c_f, rf.M);
   }
-  // the wave's ceil(K / W)-th largest lane maximum, over the W waves whose lanes all hold a vector
-  // (bitwise from the top; bf16 keys end at bit 16)
-  const uint32_t key = order_key(zm);
-  const int full = min((g.ve - g.vb) >> 6, kSegWaves);
-  const int need = full ? (a.K + full - 1) / full : SPEC_WAVE + 1;
-  uint32_t t = need > SPEC_WAVE ? kNegInfKey : 0xffffffffu;
-  if (wave < full && need <= SPEC_WAVE) {
-    t = 0;
-    for (int bit = 31; bit >= (BF16 ? 16 : 0); --bit) {
-      const uint32_t trial = t | (1u << bit);
-      if ((int)__popcll(__ballot(key >= trial)) >= need) t = trial;
-    }
-    if (BF16 && t < 0x80000000u) t |= 0xffffu;
-  }
-  if (lane == 0) sh.t[wave] = t;
-  __syncthreads();
-  uint32_t tau = sh.t[0];
-#pragma unroll
-  for (int w = 1; w < kSegWaves; ++w) tau = min(tau, sh.t[w]);
-  const size_t slot0 = ((size_t)r * a.nseg + seg) * a.cap;
-  const float tz = key_value(tau);
-#pragma unroll
-  for (int j = 0; j < kSegVecs; ++j) {
-    if (vm[j] >= tz && vm[j] > -INFINITY) {   // copied whole; its values are looked at one by one below
-      const int h = atomicAdd(&sh.nhit, 1);
-      if (h < kHitCap) {
-        sh.hit[h] = d[j];
-        sh.hit_v[h] = g.vb + j * kSegThreads + tid;
-      }
-    }
-  }
+  const uint4* body = reinterpret_cast<const uint4*>(row + (size_t)g.head * Seg::ES);
   int bad;
-  const SegSum total = segment_sum<BF16>(sh.sum, sum, [&](int j) { return g.reload(row, j); }, x, c_hi, c_lo, bad);
+  const SegSum total =
+      segment_sum<BF16>(sh.sum, S, rf, T, g, [&](int v) { return body[v]; }, x, bad);
+  __syncthreads();
+  // the candidates: values that reach the last tau
   const int nhit = sh.nhit;
   auto list = [&](float z, int id) {
     if (z >= tz && z > -INFINITY) {
       const int s = atomicAdd(&sh.n, 1);
-      if (s < a.cap) a.keys[slot0 + s] = pack_key(z, id);
+      if (s < a.cap) keys[s] = pack_key(z, id);
     }
   };
-  if (nhit <= kHitCap) {
+  if (nhit <= a.hits) {
     for (int h = tid; h < nhit; h += kSegThreads) {
       float z[EPV];
-      Seg::unpack(sh.hit[h], z);
+      Seg::unpack(hit[h], z);
+      const int v = hit_v[h];
 #pragma unroll
-      for (int e = 0; e < EPV; ++e) list(z[e], g.id_of(sh.hit_v[h], e));
+      for (int e = 0; e < EPV; ++e) list(z[e], g.id_of(v, e));
     }
     if (tid < g.nx) list(x, g.id_of_scalar(tid));
   }
   __syncthreads();
   int n = sh.n;
-  if (n > a.cap || nhit > kHitCap) {
+  if (n > a.cap || nhit > a.hits) {
     // more than `cap` values reach tau: the K-th key exactly, counting over the segment again
-    const uint4* vp = reinterpret_cast<const uint4*>(row + (size_t)g.head * Seg::ES);
     int step = 0;
     auto count = [&](auto pred) -> int {
       int c = tid < g.nx && pred(order_key(x + 0.f), g.id_of_scalar(tid)) ? 1 : 0;
 #pragma unroll 1
       for (int v = g.vb + tid; v < g.ve; v += kSegThreads) {
         float z[EPV];
-        Seg::unpack(vp[v], z);
+        Seg::unpack(body[v], z);
 #pragma unroll
         for (int e = 0; e < EPV; ++e) c += pred(order_key(z[e] + 0.f), g.id_of(v, e)) ? 1 : 0;
       }
       c = wave_sum_i(c);
-      if (lane == 0) sh.cnt[step & 1][wave] = c;
+      if (lane == 0) sh.sel.cnt[step & 1][wave] = c;
       __syncthreads();
       int tot = 0;
 #pragma unroll
-      for (int w = 0; w < kSegWaves; ++w) tot += sh.cnt[step & 1][w];
+      for (int w = 0; w < kSegWaves; ++w) tot += sh.sel.cnt[step & 1][w];
       ++step;
       return tot;
     };
@@ -191,13 +335,13 @@ void teacher_segment_kernel(TeacherArgs a) {
       const uint32_t u = order_key(z + 0.f);
       if (u > th || (u == th && id <= idb)) {
         const int s = atomicAdd(&sh.n, 1);
-        if (s < a.cap) a.keys[slot0 + s] = pack_key(z, id);
+        if (s < a.cap) keys[s] = pack_key(z, id);
       }
     };
 #pragma unroll 1
     for (int v = g.vb + tid; v < g.ve; v += kSegThreads) {
       float z[EPV];
-      Seg::unpack(vp[v], z);
+      Seg::unpack(body[v], z);
 #pragma unroll
       for (int e = 0; e < EPV; ++e) take(z[e], g.id_of(v, e));
     }
@@ -206,194 +350,98 @@ void teacher_segment_kernel(TeacherArgs a) {
     n = min(sh.n, a.cap);
     tau = th;
   }
+  if (a.nseg > 1) {
+    uint64_t* out = a.keys + ((size_t)r * a.nseg + seg) * a.cap;
+    for (int e = tid; e < n; e += kSegThreads) out[e] = keys[e];
+  } else {
+    if (tid < SPEC_WAVE) select_topk(sh.sel, keys, n, a.K, tau);
+    __syncthreads();
+    write_list(sh.sel, a, r, sh.sel.n);
+    if (a.lse && tid == 0) a.lse[r] = (float)(0.69314718055994530942 * (total.ref + log2(total.sum)));
+  }
   if (tid == 0) a.segs[(size_t)r * a.nseg + seg] = TeacherSeg{total.sum, total.ref, bad, tau, n, 0};
 }
 
-__device__ __forceinline__ double wave_max_d(double x) {
-  return wave_reduce(x, [](double p, double q) { return fmax(p, q); });
-}
+constexpr int kMergeThreads = 256;
 
-// One wave per row.  The keys kept so far and as many segments' lists as fit are held in registers; the K-th largest value is found bit by bit, of the values equal
-// to it the lowest ids, and the survivors go to LDS.  In the end every key's place is the number of
-// larger ones.
-__global__ __launch_bounds__(kMergeWaves * SPEC_WAVE) void teacher_merge_kernel(TeacherArgs a, int key_bits) {
-  __shared__ uint64_t kept[kMergeWaves][SPEC_MAX_TEACHER_K];
-  const int wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
-  const long long row = (long long)blockIdx.x * kMergeWaves + wave;
-  if (row >= (long long)a.B * a.G) return;
-  const int r = (int)row, i = r / a.G, k = r - i * a.G, K = a.K;
+__global__ __launch_bounds__(kMergeThreads) void teacher_merge_kernel(TeacherArgs a) {
+  __shared__ SelectShared sel;
+  __shared__ uint64_t keys[kMergeKeys];
+  __shared__ int sbad, sn;
+  const int r = (int)blockIdx.x, i = r / a.G, k = r - i * a.G, tid = threadIdx.x;
   const int L = a.lengths ? a.lengths[i] : a.G;
   const float T = a.temperature[i];
-  const size_t o = (size_t)r * K;
-  const TeacherSeg* p = a.segs + (size_t)r * a.nseg;
   int st = 0;
-  if (L < 0 || L > a.G) st = SPEC_REQ_BAD_LENGTH;
-  else if (!(T > 0.f && T < INFINITY)) st = SPEC_REQ_BAD_TEMPERATURE;
-  if (st == 0 && L > 0) {
+  if (L < 0 || L > a.G) {
+    st = SPEC_REQ_BAD_LENGTH;
+  } else if (!(T > 0.f && T < INFINITY)) {
+    st = SPEC_REQ_BAD_TEMPERATURE;
+  } else if (L > 0) {
     // every row of the request: a bad or an empty one marks the request
-    const TeacherSeg* q = a.segs + ((size_t)i * a.G + min(lane, L - 1)) * a.nseg;
-    int bad = 0, some = 0;
-    for (int s = 0; s < a.nseg; ++s) {
-      bad |= q[s].bad;
-      some |= q[s].sum > 0.0;
+    if (tid == 0) sbad = 0;
+    __syncthreads();
+    if (tid < L) {
+      const TeacherSeg* q = a.segs + ((size_t)i * a.G + tid) * a.nseg;
+      int bad = 0, some = 0;
+      for (int s = 0; s < a.nseg; ++s) {
+        bad |= q[s].bad;
+        some |= q[s].sum > 0.0;
+      }
+      if (bad || !some) sbad = 1;
     }
-    if (__ballot(bad || !some)) st = SPEC_REQ_NONFINITE;
+    __syncthreads();
+    if (sbad) st = SPEC_REQ_NONFINITE;
   }
-  if (a.status && k == 0 && lane == 0) a.status[i] = st;
+  if (a.status && k == 0 && tid == 0) a.status[i] = st;
   if (st != 0 || k >= L) {
-    const float fill = st != 0 ? NAN : -INFINITY;
-    for (int e = lane; e < K; e += SPEC_WAVE) {
-      a.ids[o + e] = -1;
-      a.values[o + e] = fill;
-    }
-    if (a.lse && lane == 0) a.lse[r] = fill;
+    write_empty(a, r, st != 0 ? NAN : -INFINITY);
     return;
   }
-  const TeacherSeg mine = p[min(lane, a.nseg - 1)];   // nseg <= 16
-  const bool on = lane < a.nseg;
-  const uint32_t tau = (uint32_t)wave_max_i(on ? (int)(mine.tau ^ 0x80000000u) : INT32_MIN) ^ 0x80000000u;
-  uint64_t* list = kept[wave];
+  if (a.nseg == 1) return;   // written by the row's own workgroup
+  const TeacherSeg* p = a.segs + (size_t)r * a.nseg;
+  uint32_t tau = kNegInfKey;
+  for (int s = 0; s < a.nseg; ++s) tau = max(tau, p[s].tau);
   int cur = 0, s0 = 0;
-  constexpr int KR = SPEC_MAX_TEACHER_K / SPEC_WAVE;   // registers of the keys kept so far
-  while (s0 < a.nseg) {
-    // a round: registers 0 .. KR - 1 hold the kept keys, each further one 64 keys of one segment's list
-    uint32_t hi[KR + kMergeRegs], lo[KR + kMergeRegs];
-#pragma unroll
-    for (int u = 0; u < KR; ++u) {
-      const uint64_t key = lane + u * SPEC_WAVE < cur ? list[lane + u * SPEC_WAVE] : 0;
-      hi[u] = (uint32_t)(key >> 32);
-      lo[u] = (uint32_t)key;
-    }
-    int used = 0, s1 = s0;
-    while (s1 < a.nseg) {
-      const int n = max(1, (read_lane(mine.n, s1) + SPEC_WAVE - 1) / SPEC_WAVE);   // an empty one takes a register too
-      if (used + n > kMergeRegs) break;
-      used += n;
-      ++s1;
-    }
-    int s = s0, off = 0;
-#pragma unroll
-    for (int g = 0; g < kMergeRegs; g += 8) {
-      if (g < used) {   // eight loads at once, clamped in bounds
-        uint64_t key[8];
-        bool in[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int sc = min(s, s1 - 1), n = read_lane(mine.n, sc), e = off + lane;
-          in[u] = s < s1 && e < n;
-          key[u] = a.keys[((size_t)r * a.nseg + sc) * a.cap + min(e, a.cap - 1)];
-          off += SPEC_WAVE;
-          if (off >= n) {
-            off = 0;
-            ++s;
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const bool take = in[u] && (uint32_t)(key[u] >> 32) >= tau;
-          hi[KR + g + u] = take ? (uint32_t)(key[u] >> 32) : 0;
-          lo[KR + g + u] = (uint32_t)key[u];
-        }
-      } else {
-#pragma unroll
-        for (int u = 0; u < 8; ++u) hi[KR + g + u] = lo[KR + g + u] = 0;
+  while (s0 < a.nseg) {   // rounds: the keys kept so far and as many segments' lists as fit
+    if (tid == 0) sn = cur;
+    for (int e = tid; e < cur; e += (int)blockDim.x) keys[e] = sel.list[e];
+    __syncthreads();
+    int total = cur, s1 = s0;
+    while (s1 < a.nseg && total + p[s1].n <= kMergeKeys) total += p[s1++].n;
+    for (int s = s0; s < s1; ++s) {
+      const uint64_t* src = a.keys + ((size_t)r * a.nseg + s) * a.cap;
+      for (int e = tid; e < p[s].n; e += kMergeThreads) {
+        const uint64_t key = src[e];
+        if ((uint32_t)(key >> 32) >= tau) keys[atomicAdd(&sn, 1)] = key;
       }
     }
-    auto count = [&](auto pred) -> int {
-      int c = 0;
-      if (cur > 0) {
-#pragma unroll
-        for (int u = 0; u < KR; ++u) c += (int)__popcll(__ballot(pred(hi[u], lo[u])));
-      }
-#pragma unroll
-      for (int g = 0; g < kMergeRegs; g += 8)
-        if (g < used) {
-#pragma unroll
-          for (int u = KR + g; u < KR + g + 8; ++u) c += (int)__popcll(__ballot(pred(hi[u], lo[u])));
-        }
-      return c;
-    };
-    uint32_t th = 0;   // the largest value key that at least K keys reach (0: fewer than K keys)
-#pragma unroll 1
-    for (int bit = 31; bit >= 32 - key_bits; --bit) {
-      const uint32_t trial = th | (1u << bit);
-      if (count([&](uint32_t h, uint32_t) { return h >= trial; }) >= K) th = trial;
-    }
-    uint32_t tl = 0;   // of the keys at th, the largest low words (lowest ids) that fill up K
-    // bf16 keys of negative values end in 16 ones: th stands for them with zeros there
-    const uint32_t top = th | (key_bits < 32 ? 0xffffu : 0u);
-    if (th > 0) {
-      const int above = count([&](uint32_t h, uint32_t) { return h > top; });
-      if (count([&](uint32_t h, uint32_t) { return h >= th; }) > K) {
-        tl = 0xfff00000u;
-#pragma unroll 1
-        for (int bit = 19; bit >= 0; --bit) {
-          const uint32_t trial = tl | (1u << bit);
-          if (count([&](uint32_t h, uint32_t l) { return h >= th && h <= top && l >= trial; }) >= K - above) tl = trial;
-        }
-      }
-    }
-    int kept_n = 0;
-#pragma unroll
-    for (int u = 0; u < KR + kMergeRegs; ++u) {
-      if (u < KR ? cur > 0 : u - KR < used) {
-        const bool take = hi[u] > 0 && (hi[u] > top || (hi[u] >= th && lo[u] >= tl));
-        const unsigned long long m = __ballot(take);
-        const int e = kept_n + (int)__popcll(m & ((1ull << lane) - 1));
-        if (take && e < SPEC_MAX_TEACHER_K) list[e] = ((uint64_t)hi[u] << 32) | lo[u];
-        kept_n += (int)__popcll(m);
-      }
-    }
-    cur = min(kept_n, K);
+    __syncthreads();
+    if (tid < SPEC_WAVE) select_topk(sel, keys, sn, a.K, tau);
+    __syncthreads();
+    cur = sel.n;
     s0 = s1;
   }
-  uint64_t key[SPEC_MAX_TEACHER_K / SPEC_WAVE];
-  int place[SPEC_MAX_TEACHER_K / SPEC_WAVE];
-#pragma unroll
-  for (int u = 0; u < SPEC_MAX_TEACHER_K / SPEC_WAVE; ++u) {
-    key[u] = lane + u * SPEC_WAVE < cur ? list[lane + u * SPEC_WAVE] : 0;
-    place[u] = 0;
-  }
-  if (cur <= SPEC_WAVE) {
-#pragma unroll 8
-    for (int e = 0; e < cur; ++e) place[0] += list[e] > key[0] ? 1 : 0;
-  } else {
-#pragma unroll 4
-    for (int e = 0; e < cur; ++e) {
-      const uint64_t x = list[e];
-#pragma unroll
-      for (int u = 0; u < SPEC_MAX_TEACHER_K / SPEC_WAVE; ++u) place[u] += x > key[u] ? 1 : 0;
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < SPEC_MAX_TEACHER_K / SPEC_WAVE; ++u) {
-    const int e = lane + u * SPEC_WAVE;
-    if (e < cur) {
-      a.ids[o + place[u]] = (int)~(uint32_t)key[u];
-      a.values[o + place[u]] = key_value((uint32_t)(key[u] >> 32));
-    } else if (e < K) {
-      a.ids[o + e] = -1;
-      a.values[o + e] = -INFINITY;
-    }
-  }
-  if (a.lse) {
-    const bool some = on && mine.sum > 0.0;
-    const double ref = wave_max_d(some ? mine.ref : -INFINITY);
-    const double S = wave_sum(some ? mine.sum * exp2(mine.ref - ref) : 0.0);
-    if (lane == 0) a.lse[r] = (float)(0.69314718055994530942 * (ref + log2(S)));
+  write_list(sel, a, r, cur);
+  if (a.lse && tid == 0) {
+    double ref = -INFINITY, S = 0.0;
+    for (int s = 0; s < a.nseg; ++s)
+      if (p[s].sum > 0.0) ref = fmax(ref, p[s].ref);
+    for (int s = 0; s < a.nseg; ++s)
+      if (p[s].sum > 0.0) S += p[s].sum * exp2(p[s].ref - ref);
+    a.lse[r] = (float)(0.69314718055994530942 * (ref + log2(S)));
   }
 }
 
-// Keys a segment may list: 22 (K = 1) to 460 (K = 256) reach tau on Gaussian rows, 700 at most seen of
-// 160 segments; rows of one segment may have no full wave to take tau from (at most 64 vectors and 14
-// scalars, all listed then).
-int list_cap(int K, int nseg) { return 3 * K + 96 + (nseg == 1 ? 512 : 0); }
-static_assert(3 * SPEC_MAX_TEACHER_K + 96 + 512 <= SPEC_WAVE * kMergeRegs, "a segment's list fits a round");
+// Candidates a segment may list: on Gaussian rows 22 (K = 1) to 460 (K = 256) reach tau on average, 700 at
+// most seen of 160 segments; a short row may have no full wave to take tau from (at most 64 vectors and
+// 14 scalars, all listed then).  Vectors reaching one of the earlier bounds: one such lot per doubling.
+int list_cap(int K) { return 3 * K + 640 + (K & 1); }   // even: the vectors behind the keys lie on 16 bytes
+int hit_cap(int K) { return 6 * K + 288; }
+static_assert(3 * SPEC_MAX_TEACHER_K + 641 + SPEC_MAX_TEACHER_K <= kMergeKeys, "a list fits a round of the merge");
 
-size_t workspace_of(size_t rows, int V, int K, int dtype) {
-  const int nseg = row_segments(V, dtype);
-  return round256(rows * nseg * sizeof(TeacherSeg)) +
-         round256(rows * nseg * (size_t)list_cap(K, nseg) * sizeof(uint64_t));
+size_t segs_bytes(size_t rows, int nseg) { return round256(rows * nseg * sizeof(TeacherSeg)); }
+size_t keys_bytes(size_t rows, int nseg, int K) {
+  return nseg > 1 ? round256(rows * nseg * (size_t)list_cap(K) * sizeof(uint64_t)) : 0;
 }
 
 }  // namespace
@@ -403,9 +451,14 @@ using namespace spec;
 
 extern "C" size_t spec_teacher_workspace_size(int32_t B, int32_t gamma, int32_t V, int32_t K) {
   if (!shape_ok(B, gamma, V, SPEC_BF16) || K < 1 || K > SPEC_MAX_TEACHER_K) return 0;
-  const size_t rows = (size_t)B * gamma, b = workspace_of(rows, V, K, SPEC_BF16);
-  const size_t f = V <= SPEC_MAX_V / 2 ? workspace_of(rows, V, K, SPEC_F32) : 0;
-  return b > f ? b : f;
+  const size_t rows = (size_t)B * gamma;
+  size_t most = 0;
+  for (int dtype : {SPEC_F32, SPEC_BF16}) {   // the larger of the two storage types'
+    const int nseg = row_segments((int64_t)rows, V, dtype);
+    const size_t n = segs_bytes(rows, nseg) + keys_bytes(rows, nseg, K);
+    if (n > most) most = n;
+  }
+  return most;
 }
 
 extern "C" int32_t spec_teacher_topk(int32_t B, int32_t gamma, int32_t V, int32_t dtype, const void* target_logits,
@@ -419,22 +472,22 @@ extern "C" int32_t spec_teacher_topk(int32_t B, int32_t gamma, int32_t V, int32_
     return SPEC_ERR_WORKSPACE;
   TeacherArgs a{};
   a.B = B; a.G = gamma; a.V = V; a.K = K;
-  a.nseg = row_segments(V, dtype);
-  a.cap = list_cap(K, a.nseg);
   const uint64_t rows = (uint64_t)B * gamma;
+  a.nseg = row_segments((int64_t)rows, V, dtype);
+  a.cap = list_cap(K);
+  a.hits = hit_cap(K);
   if (rows * a.nseg * kSegThreads > 0xffffffffull) return SPEC_ERR_UNSUPPORTED;
   a.target = target_logits; a.lengths = lengths; a.temperature = temperature;
   a.ids = ids_out; a.values = values_out; a.lse = lse_out; a.status = status;
   a.segs = reinterpret_cast<TeacherSeg*>(workspace);
-  a.keys = reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(workspace) +
-                                       round256(rows * a.nseg * sizeof(TeacherSeg)));
+  a.keys = reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(workspace) + segs_bytes(rows, a.nseg));
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const dim3 grid((unsigned)(rows * a.nseg));
+  const unsigned lds = (unsigned)(a.cap * 8 + a.hits * 20);
   if (dtype == SPEC_BF16)
-    hipLaunchKernelGGL(teacher_segment_kernel<true>, grid, dim3(kSegThreads), 0, s, a);
+    hipLaunchKernelGGL(teacher_row_kernel<true>, grid, dim3(kSegThreads), lds, s, a);
   else
-    hipLaunchKernelGGL(teacher_segment_kernel<false>, grid, dim3(kSegThreads), 0, s, a);
-  hipLaunchKernelGGL(teacher_merge_kernel, dim3((unsigned)((rows + kMergeWaves - 1) / kMergeWaves)),
-                     dim3(kMergeWaves * SPEC_WAVE), 0, s, a, dtype == SPEC_BF16 ? 16 : 32);
+    hipLaunchKernelGGL(teacher_row_kernel<false>, grid, dim3(kSegThreads), lds, s, a);
+  hipLaunchKernelGGL(teacher_merge_kernel, dim3((unsigned)rows), dim3(kMergeThreads), 0, s, a);
   return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
 }

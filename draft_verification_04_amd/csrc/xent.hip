@@ -11,6 +11,7 @@
 //           both ways round, [N, piece] and [piece, N].
 //   kAcc    dH += G W over the piece: A = W^T (the piece transposed once), B = G; fp32 in memory.
 //   kStore  dW of the piece: A = H^T, B = G^T; rounded to the storage type.
+// G is rounded to bf16 for its products; its one large entry per row, the label's, is corrected in fp32.
 // The pieces bound the memory: G, G^T and W^T of one piece at a time instead of N V logits.
 //
 // Operands in LDS: a step of 128 bytes of k (64 bf16 or 32 fp32) per row, rows 128 bytes apart, the
@@ -40,6 +41,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2eF = 1.44269504f;
 constexpr int kStepBytes = 128;   // of k per row and pipeline step
+constexpr int kNoRow = INT32_MAX;
 
 enum { kStats = 0, kGradZ = 1, kAcc = 2, kStore = 3 };
 
@@ -63,6 +65,11 @@ struct GemmArgs {
   char* gt;          // [rowsA, ldgt bytes]
   size_t ldgn, ldgt;
   int vpad, npad;    // columns of gn and gt that are written (zeros past the valid ones)
+  // bf16: the labels' entries of G (see xent_label_rows_kernel)
+  float* glab;       // [N] what the rounding of row n's left out
+  int32_t* first;    // [V] the first row with the token as its label (kNoRow: none)
+  float* side;       // [N, side_ld] dW of a label's token, unrounded, at its first row
+  int side_ld;
   // kAcc, kStore
   float* acc;        // [rowsB, rowsA]: whole tiles and the first part of the others
   float* acc_parts;  // [rest tiles, parts - 1, tile]: their further parts
@@ -301,7 +308,13 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
         if constexpr (ES == 2) {
           bf16x4 h;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) h[x] = (__bf16)o[x];
+          for (int x = 0; x < 4; ++x) {
+            h[x] = (__bf16)o[x];
+            if (live && i + x == lab && i + x < g.rowsA) {
+              g.glab[j] = o[x] - (float)h[x];
+              if (g.first) atomicMin(&g.first[label], j);
+            }
+          }
           if (j < g.rowsB && i < g.vpad) *reinterpret_cast<bf16x4*>(g.gn + (size_t)j * g.ldgn + (size_t)i * 2) = h;
           if (j < g.npad)
 #pragma unroll
@@ -321,6 +334,8 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
     for (int n = 0; n < NT; ++n) {
       const int j = jw + n * 16;
       if (j >= g.rowsB) continue;
+      int first = kNoRow;
+      if constexpr (KIND == kStore && ES == 2) first = g.first[g.v0 + j];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const int i = iw + m * 16;
@@ -337,7 +352,8 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
           bf16x4 h;
 #pragma unroll
           for (int x = 0; x < 4; ++x) h[x] = (__bf16)o[x];
-          *reinterpret_cast<bf16x4*>(g.out + (size_t)j * g.ldo + (size_t)i * 2) = h;
+          if (first != kNoRow) *reinterpret_cast<f32x4*>(g.side + (size_t)first * g.side_ld + i) = o;
+          else *reinterpret_cast<bf16x4*>(g.out + (size_t)j * g.ldo + (size_t)i * 2) = h;
         } else {
           *reinterpret_cast<f32x4*>(g.out + (size_t)j * g.ldo + (size_t)i * 4) = o;
         }
@@ -436,14 +452,14 @@ __global__ __launch_bounds__(256) void xent_transpose_kernel(const char* in, siz
 // grad_hidden = the sums, the parts of a shared tile added in order, rounded once; zeros for the rows
 // left out.
 template <int ES>
-__global__ __launch_bounds__(256) void xent_finish_kernel(GemmArgs g, int bm, int bn, char* out,
-                                                          const int32_t* labels, const float* lse, int V) {
+__global__ __launch_bounds__(256) void xent_finish_kernel(GemmArgs g, int bm, int bn, char* out, const char* weight) {
   const int d = g.rowsA, N = g.rowsB, d4 = d / 4;
   const size_t t = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (t >= (size_t)N * d4) return;
   const int n = (int)(t / d4), i = (int)(t - (size_t)n * d4) * 4;
   f32x4 s = {};
-  if (live_row(labels[n], lse[n], V)) {
+  const int label = g.labels[n];
+  if (live_row(label, g.lse[n], g.V)) {
     s = reinterpret_cast<const f32x4*>(g.acc)[t];
     const int ti = i / bm, tj = n / bn, band = tj / 8;
     const int rest = band * 8 * g.ti + ti * min(8, g.tj - band * 8) + tj % 8 - g.whole;
@@ -451,6 +467,12 @@ __global__ __launch_bounds__(256) void xent_finish_kernel(GemmArgs g, int bm, in
       for (int p = 0; p < g.parts - 1; ++p)
         s += *reinterpret_cast<const f32x4*>(g.acc_parts + ((size_t)(rest * (g.parts - 1) + p) * bn + (n - tj * bn)) * bm +
                                              (i - ti * bm));
+    if constexpr (ES == 2) {   // what the rounding of the label's G left out
+      const bf16x4 w = *reinterpret_cast<const bf16x4*>(weight + ((size_t)label * d + i) * 2);
+      const float r = g.glab[n];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[x] += r * (float)w[x];
+    }
   }
   if constexpr (ES == 2) {
     bf16x4 h;
@@ -459,6 +481,85 @@ __global__ __launch_bounds__(256) void xent_finish_kernel(GemmArgs g, int bm, in
     reinterpret_cast<bf16x4*>(out)[t] = h;
   } else {
     reinterpret_cast<f32x4*>(out)[t] = s;
+  }
+}
+
+// dW of the tokens that are labels (bf16): the label's entry of G, (p - 1) grad_loss, outweighs the rest of
+// its row together, and its rounding alone would add as much again to the gradient's error.  The product
+// leaves these tokens' sums unrounded at their first row; the workgroup of that row adds, in row order,
+// what the rounding left out times the hidden state of every row with the label, and rounds once.
+constexpr int kLabelThreads = 256;
+
+__global__ __launch_bounds__(kLabelThreads) void xent_fill_kernel(int32_t* p, int n) {
+  const int t = (int)blockIdx.x * kLabelThreads + (int)threadIdx.x;
+  if (t < n) p[t] = kNoRow;
+}
+
+__global__ __launch_bounds__(kLabelThreads) void xent_label_rows_kernel(const int32_t* labels, const float* lse, int N,
+                                                                        int V, int d, const float* glab,
+                                                                        const int32_t* first, const float* side,
+                                                                        const char* hidden, char* out) {
+  constexpr int NW = kLabelThreads / SPEC_WAVE, CHUNK = 4 * kLabelThreads, PER = 4;
+  __shared__ int32_t rows[CHUNK];
+  __shared__ int cnt[NW];
+  const int n = (int)blockIdx.x, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int label = labels[n];
+  if (!live_row(label, lse[n], V) || first[label] != n) return;
+  const bf16x4* h4 = reinterpret_cast<const bf16x4*>(hidden);
+  const int d4 = d / 4;
+  for (int c0 = 0; c0 < d4; c0 += PER * kLabelThreads) {   // PER groups of four columns per thread
+    f32x4 s[PER];
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int c = min(c0 + u * kLabelThreads + tid, d4 - 1);
+      s[u] = reinterpret_cast<const f32x4*>(side + (size_t)n * d)[c];
+    }
+    for (int m0 = n; m0 < N; m0 += CHUNK) {
+      // the rows of the chunk with this label, in order: a wave takes 4 * 64 rows in a row
+      unsigned long long hit[4];
+      int mine = 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int m = m0 + (wave * 4 + u) * SPEC_WAVE + lane, mc = min(m, N - 1);
+        hit[u] = __ballot(m < N && labels[mc] == label && fabsf(lse[mc]) < INFINITY);
+        mine += (int)__popcll(hit[u]);
+      }
+      __syncthreads();   // the last chunk's rows are read
+      if (lane == 0) cnt[wave] = mine;
+      __syncthreads();
+      int base = 0, total = 0;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        base += w < wave ? cnt[w] : 0;
+        total += cnt[w];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if ((hit[u] >> lane) & 1ull)
+          rows[base + (int)__popcll(hit[u] & ((1ull << lane) - 1))] = m0 + (wave * 4 + u) * SPEC_WAVE + lane;
+        base += (int)__popcll(hit[u]);
+      }
+      __syncthreads();
+#pragma unroll 2
+      for (int e = 0; e < total; ++e) {
+        const int m = rows[e];
+        const float r = glab[m];
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+          const bf16x4 x = h4[(size_t)m * d4 + min(c0 + u * kLabelThreads + tid, d4 - 1)];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) s[u][q] += r * (float)x[q];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int c = c0 + u * kLabelThreads + tid;
+      bf16x4 o;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) o[q] = (__bf16)s[u][q];
+      if (c < d4) reinterpret_cast<bf16x4*>(out + (size_t)label * d * 2)[c] = o;
+    }
   }
 }
 
@@ -562,11 +663,15 @@ void launch_gemm(const GemmArgs& g, hipStream_t s) {
         h.gt += (size_t)sh.head * g.ldgt;
         h.vpad -= (int)sh.head;
       }
-      if (KIND == kStore) h.out += (size_t)sh.head * ES;
+      if (KIND == kStore) {
+        h.out += (size_t)sh.head * ES;
+        h.side += sh.head;
+      }
     } else {
       h.B += (size_t)sh.head * g.ldb;
       h.rowsB -= (int)sh.head;
       h.out += (size_t)sh.head * g.ldo;
+      h.v0 += (int)sh.head;
     }
   }
   launch_tiles<ES, KIND>(h, split || sh.head == 0 ? sh.tail : kBig, INT32_MAX, 1, s);
@@ -600,8 +705,8 @@ struct BackPlan {
   int pieces, vc;        // vocabulary pieces of vc tokens (a multiple of 256; the last may be shorter)
   long long npad;
   int tile, whole, parts;   // of dH: tiles taken whole, and the workgroups that share each of the others
-  size_t gn, gt, wt, ht, acc, acc_parts;   // bytes
-  size_t total() const { return gn + gt + wt + ht + acc + acc_parts; }
+  size_t gn, gt, wt, ht, acc, acc_parts, glab, first, side;   // bytes
+  size_t total() const { return gn + gt + wt + ht + acc + acc_parts + glab + first + side; }
 };
 
 constexpr long long kPieceBytes = 128ll << 20;   // of G (and of W^T) per piece
@@ -643,6 +748,11 @@ BackPlan back_plan(int N, int V, int d, int dtype) {
   p.wt = round256((size_t)d * p.vc * p.es);
   p.ht = round256((size_t)d * p.npad * p.es);
   p.acc = round256((size_t)N * d * sizeof(float));
+  if (p.es == 2) {
+    p.glab = round256((size_t)N * sizeof(float));
+    p.first = round256((size_t)V * sizeof(int32_t));
+    p.side = round256((size_t)N * d * sizeof(float));
+  }
   return p;
 }
 
@@ -684,6 +794,13 @@ int32_t run_backward(int N, int V, int d, int dtype, const void* hidden, const v
   h.A = wt; h.lda = (size_t)p.vc * ES; h.rowsA = d;
   h.B = gn; h.ldb = (size_t)p.vc * ES; h.rowsB = N;
   h.acc = acc; h.acc_parts = reinterpret_cast<float*>(ht + p.ht + p.acc);
+  h.labels = labels; h.lse = lse; h.V = V;
+  char* lab = ht + p.ht + p.acc + p.acc_parts;
+  h.glab = reinterpret_cast<float*>(lab);
+  int32_t* first = ES == 2 && grad_weight ? reinterpret_cast<int32_t*>(lab + p.glab) : nullptr;
+  float* side = reinterpret_cast<float*>(lab + p.glab + p.first);
+  if (first)
+    hipLaunchKernelGGL(xent_fill_kernel, dim3(ceil_div(V, kLabelThreads)), dim3(kLabelThreads), 0, s, first, V);
   const size_t ld = (size_t)d * ES;
   if (grad_weight)
     hipLaunchKernelGGL(xent_transpose_kernel<ES>, dim3(ceil_div(p.npad, 64), ceil_div(d, 64)), dim3(256), 0, s,
@@ -700,6 +817,7 @@ int32_t run_backward(int N, int V, int d, int dtype, const void* hidden, const v
     g.labels = labels; g.V = V; g.v0 = v0; g.lse = lse; g.grad_loss = grad_loss;
     g.gn = gn; g.ldgn = (size_t)p.vc * ES; g.vpad = vpad;
     g.gt = gt; g.ldgt = (size_t)p.npad * ES; g.npad = (int)p.npad;
+    g.glab = h.glab; g.first = first;
     launch_gemm<ES, kGradZ>(g, s);
     if (grad_hidden) {
       hipLaunchKernelGGL(xent_transpose_kernel<ES>, dim3(ceil_div(vpad, 64), ceil_div(d, 64)), dim3(256), 0, s, w, ld,
@@ -714,12 +832,17 @@ int32_t run_backward(int N, int V, int d, int dtype, const void* hidden, const v
       w.B = gt; w.ldb = (size_t)p.npad * ES; w.rowsB = nv;
       w.kbytes = (int)p.npad * ES;
       w.out = reinterpret_cast<char*>(grad_weight) + (size_t)v0 * ld; w.ldo = ld;
+      w.v0 = v0; w.first = first; w.side = side; w.side_ld = d;
       launch_gemm<ES, kStore>(w, s);
     }
   }
+  if (first)
+    hipLaunchKernelGGL(xent_label_rows_kernel, dim3(N), dim3(kLabelThreads), 0, s, labels, lse, N, V, d, h.glab, first,
+                       side, reinterpret_cast<const char*>(hidden), reinterpret_cast<char*>(grad_weight));
   if (grad_hidden)
     hipLaunchKernelGGL(xent_finish_kernel<ES>, dim3(ceil_div((long long)N * d / 4, 256)), dim3(256), 0, s, h,
-                       tile_m(p.tile), tile_n(p.tile), reinterpret_cast<char*>(grad_hidden), labels, lse, V);
+                       tile_m(p.tile), tile_n(p.tile), reinterpret_cast<char*>(grad_hidden),
+                       reinterpret_cast<const char*>(weight));
   return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
 }
 

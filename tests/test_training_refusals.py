@@ -50,11 +50,12 @@ def test_teacher_topk(sv, p):
 
 
 def test_teacher_workspace_holds_either_type(sv):
-    """The size does not name the storage type: it covers the segments of both."""
+    """The size does not name the storage type: it covers the segments of both (and their lists, where
+    a row is cut into several)."""
     lib = sv.load_library()
     for V in (1, 7, 8191, 16384, 16385, 32768, 32769, 262144, 262145, 524288):
         a, b = (lib.spec_teacher_workspace_size(3, 2, V, K) for K in (1, 256))
-        assert 0 < a < b
+        assert 0 < a <= b
 
 
 def test_distill(sv, p):

@@ -207,19 +207,13 @@ void distill_stream_kernel(DistillArgs a) {
   __shared__ SegSumShared ss;
   __shared__ ListShared ls;
   __shared__ int sflags;
-  const int r = (int)(blockIdx.x / (unsigned)a.nseg), seg = (int)(blockIdx.x - (unsigned)r * a.nseg);
-  const int i = r / a.G, k = r - i * a.G;
-  const int L = a.lengths ? a.lengths[i] : a.G;
+  __shared__ LiveShared live;
+  const int o = (int)(blockIdx.x / (unsigned)a.nseg), seg = (int)(blockIdx.x - (unsigned)o * a.nseg);
+  int i, k;
+  if (!live_row(live, o, a.B, a.G, a.lengths, a.temperature, i, k)) return;   // the status kernel fills the other rows
+  const int r = i * a.G + k;
   const float T = a.temperature[i];
   const int tid = threadIdx.x;
-  if (k >= L || L > a.G || !(T > 0.f && T < INFINITY)) {
-    if (a.nseg == 1 && tid == 0) {
-      a.loss[r] = 0.f;
-      a.saved[(size_t)r * SPEC_DISTILL_SAVED] = NAN;
-      a.row_status[r] = 0;
-    }
-    return;
-  }
   const int e0 = min(tid, a.K - 1);
   const int id = a.ids[(size_t)r * a.K + e0];
   const float val = a.values[(size_t)r * a.K + e0];
@@ -324,14 +318,7 @@ __global__ __launch_bounds__(kFinishWaves * SPEC_WAVE) void distill_finish_kerne
   const int i = (int)(r / a.G), k = (int)(r - (int64_t)i * a.G);
   const int L = a.lengths ? a.lengths[i] : a.G;
   const float T = a.temperature[i];
-  if (k >= L || L > a.G || !(T > 0.f && T < INFINITY)) {
-    if (lane == 0) {
-      a.loss[r] = 0.f;
-      a.saved[(size_t)r * SPEC_DISTILL_SAVED] = NAN;
-      a.row_status[r] = 0;
-    }
-    return;
-  }
+  if (k >= L || L > a.G || !(T > 0.f && T < INFINITY)) return;
   const DistillSeg mine = a.segs[(size_t)r * a.nseg + min(lane, a.nseg - 1)];
   const bool on = lane < a.nseg;
   const char* row = reinterpret_cast<const char*>(a.draft) + (size_t)r * (size_t)a.V * RowSeg<BF16>::ES;
@@ -362,12 +349,13 @@ __global__ __launch_bounds__(256) void distill_status_kernel(DistillArgs a) {
   const int L = a.lengths ? a.lengths[i] : a.G;
   const float T = a.temperature[i];
   const size_t r = (size_t)i * a.G + min(k, a.G - 1);
-  int st = wave_or_i(a.row_status[r]);
+  int st = 0;
   if (L < 0 || L > a.G) st = SPEC_REQ_BAD_LENGTH;
   else if (!(T > 0.f && T < INFINITY)) st = SPEC_REQ_BAD_TEMPERATURE;
+  else st = wave_or_i(k < L ? a.row_status[r] : 0);
   if (k == 0 && a.status) a.status[i] = st;
-  if (st != 0 && k < a.G) {
-    a.loss[r] = NAN;
+  if (k < a.G && (st != 0 || k >= L)) {   // a failed request, or a row that is not read
+    a.loss[r] = st != 0 ? NAN : 0.f;
     a.saved[r * SPEC_DISTILL_SAVED] = NAN;
   }
 }

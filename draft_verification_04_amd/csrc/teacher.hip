@@ -53,28 +53,39 @@ struct SelectShared {
   int n;
   uint32_t tie[SPEC_WAVE];
   uint64_t list[SPEC_MAX_TEACHER_K];
+  int place[SPEC_MAX_TEACHER_K];
 };
 
 // One wave: keeps the K largest of the n keys (distinct) in LDS, in any order, in sh.list, and their number in
 // sh.n.  One wave, not eight: a few hundred keys are a few per lane, and a step costs a wave the same
-// whatever it holds.  floor_key: a value key that no key lies below.
+// whatever it holds.  Value keys are compared without their low SH bits (16 for bf16, whose keys end
+// there).  floor_key: a value key that no key lies below.
+template <int SH>
 __device__ __forceinline__ void select_topk(SelectShared& sh, const uint64_t* keys, int n, int K, uint32_t floor_key) {
   const int lane = (int)threadIdx.x & 63;
   const uint32_t* words = reinterpret_cast<const uint32_t*>(keys);   // low word (id), high word (value)
-  constexpr int U = 8;   // reads in flight
-  auto count = [&](bool ids, auto pred) -> int {
+  constexpr int U = 8, R = U * SPEC_WAVE;   // keys in registers; the others are read from LDS again and again
+  // value words (0: no key; every key's is larger) and id words of keys e, e + 64, ..
+  auto fetch = [&](int e, uint32_t (&h)[U], uint32_t (&l)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = min(e + u * SPEC_WAVE, n - 1);
+      h[u] = e + u * SPEC_WAVE < n ? words[2 * at + 1] >> SH : 0;
+      l[u] = words[2 * at];
+    }
+  };
+  uint32_t h0[U], l0[U];
+  if (n > 0) fetch(lane, h0, l0);
+  auto count = [&](auto pred) -> int {
     int c = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) c += (int)__popcll(__ballot(pred(h0[u], l0[u])));
 #pragma unroll 1
-    for (int e = lane; e - lane < n; e += U * SPEC_WAVE) {
+    for (int e = R + lane; e - lane < n; e += R) {
       uint32_t h[U], l[U];
+      fetch(e, h, l);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int at = min(e + u * SPEC_WAVE, n - 1);
-        h[u] = words[2 * at + 1];
-        l[u] = ids ? words[2 * at] : 0;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) c += (int)__popcll(__ballot(e + u * SPEC_WAVE < n && pred(h[u], l[u])));
+      for (int u = 0; u < U; ++u) c += (int)__popcll(__ballot(pred(h[u], l[u])));
     }
     return c;
   };
@@ -83,34 +94,36 @@ __device__ __forceinline__ void select_topk(SelectShared& sh, const uint64_t* ke
     // the largest value key that at least K keys reach; the bits above the highest one in which the keys
     // differ are known
     uint32_t top = 0;
-    for (int e = lane; e < n; e += SPEC_WAVE) top = max(top, words[2 * e + 1]);
+    for (int e = lane; e < n; e += SPEC_WAVE) top = max(top, words[2 * e + 1] >> SH);
     top = (uint32_t)wave_max_i((int)(top ^ 0x80000000u)) ^ 0x80000000u;
-    const int high = top == floor_key ? -1 : 31 - __clz((int)(top ^ floor_key));
+    const uint32_t low = floor_key >> SH;
+    const int high = top == low ? -1 : 31 - __clz((int)(top ^ low));
     th = high < 0 ? top : (top >> high >> 1) << high << 1;
     int reach = n;
 #pragma unroll 1
     for (int bit = high; bit >= 0 && reach != K; --bit) {
       const uint32_t trial = th | (1u << bit);
-      const int c = count(false, [&](uint32_t h, uint32_t) { return h >= trial; });
+      const int c = count([&](uint32_t h, uint32_t) { return h >= trial; });
       if (c >= K) {
         th = trial;
         reach = c;
       }
     }
     if (reach > K) {   // of the keys at th the largest low words (lowest ids) that fill up K
-      const int above = count(false, [&](uint32_t h, uint32_t) { return h > th; }), need = K - above;
+      const int above = count([&](uint32_t h, uint32_t) { return h > th; }), need = K - above;
       if (reach - above <= SPEC_WAVE) {   // a key per lane, its place by counting
         int m = 0;
 #pragma unroll 1
         for (int e = lane; e - lane < n; e += SPEC_WAVE) {
           const int at = min(e, n - 1);
-          const bool tie = e < n && words[2 * at + 1] == th;
+          const bool tie = e < n && words[2 * at + 1] >> SH == th;
           const unsigned long long b = __ballot(tie);
           if (tie) sh.tie[m + (int)__popcll(b & ((1ull << lane) - 1))] = words[2 * at];
           m += (int)__popcll(b);
         }
         const uint32_t mine = lane < m ? sh.tie[lane] : 0;
         int before = 0;
+#pragma unroll 4
         for (int e = 0; e < m; ++e) before += sh.tie[e] > mine ? 1 : 0;
         const unsigned long long last = __ballot(lane < m && before == need - 1);
         tl = read_lane(mine, (int)__ffsll((long long)last) - 1);
@@ -119,7 +132,7 @@ __device__ __forceinline__ void select_topk(SelectShared& sh, const uint64_t* ke
 #pragma unroll 1
         for (int bit = 19; bit >= 0; --bit) {
           const uint32_t trial = tl | (1u << bit);
-          const int c = count(true, [&](uint32_t h, uint32_t l) { return h == th && l >= trial; });
+          const int c = count([&](uint32_t h, uint32_t l) { return h == th && l >= trial; });
           if (c >= need) tl = trial;
           if (c == need) break;
         }
@@ -130,7 +143,7 @@ __device__ __forceinline__ void select_topk(SelectShared& sh, const uint64_t* ke
 #pragma unroll 1
   for (int e = lane; e - lane < n; e += SPEC_WAVE) {
     const uint64_t key = keys[min(e, n - 1)];
-    const uint32_t h = (uint32_t)(key >> 32);
+    const uint32_t h = (uint32_t)(key >> 32) >> SH;
     const bool take = e < n && (h > th || (h == th && (uint32_t)key >= tl));
     const unsigned long long m = __ballot(take);
     const int at = kept + (int)__popcll(m & ((1ull << lane) - 1));
@@ -140,19 +153,30 @@ __device__ __forceinline__ void select_topk(SelectShared& sh, const uint64_t* ke
   if (lane == 0) sh.n = min(kept, K);
 }
 
-// Writes the n selected keys of row r in order, unused entries behind them.
-__device__ __forceinline__ void write_list(const SelectShared& sh, const TeacherArgs& a, int r, int n) {
-  const int tid = threadIdx.x;
-  if (tid >= a.K) return;
+// Writes the sh.n selected keys of row r in order, unused entries behind them: a key's place is the number
+// of larger ones, counted by the workgroup's waves (NW) in slices of the list, 64 keys at a time.
+template <int NW>
+__device__ __forceinline__ void write_list(SelectShared& sh, const TeacherArgs& a, int r) {
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = sh.n;
+  const int groups = max(1, (n + SPEC_WAVE - 1) / SPEC_WAVE), slices = NW / groups;   // n <= 256: 4 groups
+  static_assert(NW >= SPEC_MAX_TEACHER_K / SPEC_WAVE, "a wave per 64 keys");
+  for (int e = tid; e < n; e += NW * SPEC_WAVE) sh.place[e] = 0;
+  __syncthreads();
+  const int grp = wave % groups, slice = wave / groups, e = grp * SPEC_WAVE + lane;
+  if (slice < slices && e < n) {
+    const uint64_t mine = sh.list[e];
+    int before = 0;
+#pragma unroll 4
+    for (int f = n * slice / slices; f < n * (slice + 1) / slices; ++f) before += sh.list[f] > mine ? 1 : 0;
+    atomicAdd(&sh.place[e], before);
+  }
+  __syncthreads();
   const size_t o = (size_t)r * a.K;
   if (tid < n) {
-    const uint64_t mine = sh.list[tid];
-    int place = 0;
-#pragma unroll 4
-    for (int e = 0; e < n; ++e) place += sh.list[e] > mine ? 1 : 0;
-    a.ids[o + place] = (int)~(uint32_t)mine;
-    a.values[o + place] = key_value((uint32_t)(mine >> 32));
-  } else {
+    const uint64_t key = sh.list[tid];
+    a.ids[o + sh.place[tid]] = (int)~(uint32_t)key;
+    a.values[o + sh.place[tid]] = key_value((uint32_t)(key >> 32));
+  } else if (tid < a.K) {
     a.ids[o + tid] = -1;
     a.values[o + tid] = -INFINITY;
   }
@@ -168,6 +192,7 @@ __device__ __forceinline__ void write_empty(const TeacherArgs& a, int r, float f
 }
 
 struct RowShared {
+  LiveShared live;
   SegSumShared sum;
   SelectShared sel;
   uint32_t t[2][kSegWaves];
@@ -184,11 +209,11 @@ void teacher_row_kernel(TeacherArgs a) {
   uint64_t* keys = reinterpret_cast<uint64_t*>(dyn);                          // [cap] candidates
   uint4* hit = reinterpret_cast<uint4*>(dyn + (size_t)a.cap * 8);             // [hits] vectors reaching tau
   int32_t* hit_v = reinterpret_cast<int32_t*>(dyn + (size_t)a.cap * 8 + (size_t)a.hits * 16);
-  const int r = (int)(blockIdx.x / (unsigned)a.nseg), seg = (int)(blockIdx.x - (unsigned)r * a.nseg);
-  const int i = r / a.G, k = r - i * a.G;
-  const int L = a.lengths ? a.lengths[i] : a.G;
+  const int o = (int)(blockIdx.x / (unsigned)a.nseg), seg = (int)(blockIdx.x - (unsigned)o * a.nseg);
+  int i, k;
+  if (!live_row(sh.live, o, a.B, a.G, a.lengths, a.temperature, i, k)) return;   // the merge kernel fills the other rows
+  const int r = i * a.G + k;
   const float T = a.temperature[i];
-  if (k >= L || L > a.G || !(T > 0.f && T < INFINITY)) return;   // the merge kernel fills these rows
   const char* row = reinterpret_cast<const char*>(a.target) + ((size_t)i * (a.G + 1) + k) * (size_t)a.V * Seg::ES;
   const Seg g(row, a.V, seg, a.nseg);
   uint4 d[kSegVecs];
@@ -264,7 +289,8 @@ void teacher_row_kernel(TeacherArgs a) {
       asm volatile("" : "+v"(S));   // one vector's values at a time: registers
     });
     ++chunk;
-    if (chunk > 1 && (chunk & (chunk - 1)) == 0 && c + kSegChunk < g.ve) raise_tau();
+    // (at the end only for long lists: it halves the candidates)
+    if (chunk > 1 && (c + kSegChunk < g.ve ? (chunk & (chunk - 1)) == 0 : a.K > SPEC_WAVE)) raise_tau();
   }
   if (g.nx > 0) {
     const float z1[1] = {x};
@@ -354,9 +380,9 @@ void teacher_row_kernel(TeacherArgs a) {
     uint64_t* out = a.keys + ((size_t)r * a.nseg + seg) * a.cap;
     for (int e = tid; e < n; e += kSegThreads) out[e] = keys[e];
   } else {
-    if (tid < SPEC_WAVE) select_topk(sh.sel, keys, n, a.K, tau);
+    if (tid < SPEC_WAVE) select_topk<BF16 ? 16 : 0>(sh.sel, keys, n, a.K, tau);
     __syncthreads();
-    write_list(sh.sel, a, r, sh.sel.n);
+    write_list<kSegWaves>(sh.sel, a, r);
     if (a.lse && tid == 0) a.lse[r] = (float)(0.69314718055994530942 * (total.ref + log2(total.sum)));
   }
   if (tid == 0) a.segs[(size_t)r * a.nseg + seg] = TeacherSeg{total.sum, total.ref, bad, tau, n, 0};
@@ -364,6 +390,7 @@ void teacher_row_kernel(TeacherArgs a) {
 
 constexpr int kMergeThreads = 256;
 
+template <int SH>
 __global__ __launch_bounds__(kMergeThreads) void teacher_merge_kernel(TeacherArgs a) {
   __shared__ SelectShared sel;
   __shared__ uint64_t keys[kMergeKeys];
@@ -416,12 +443,12 @@ __global__ __launch_bounds__(kMergeThreads) void teacher_merge_kernel(TeacherArg
       }
     }
     __syncthreads();
-    if (tid < SPEC_WAVE) select_topk(sel, keys, sn, a.K, tau);
+    if (tid < SPEC_WAVE) select_topk<SH>(sel, keys, sn, a.K, tau);
     __syncthreads();
     cur = sel.n;
     s0 = s1;
   }
-  write_list(sel, a, r, cur);
+  write_list<kMergeThreads / SPEC_WAVE>(sel, a, r);
   if (a.lse && tid == 0) {
     double ref = -INFINITY, S = 0.0;
     for (int s = 0; s < a.nseg; ++s)
@@ -484,10 +511,12 @@ extern "C" int32_t spec_teacher_topk(int32_t B, int32_t gamma, int32_t V, int32_
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const dim3 grid((unsigned)(rows * a.nseg));
   const unsigned lds = (unsigned)(a.cap * 8 + a.hits * 20);
-  if (dtype == SPEC_BF16)
+  if (dtype == SPEC_BF16) {
     hipLaunchKernelGGL(teacher_row_kernel<true>, grid, dim3(kSegThreads), lds, s, a);
-  else
+    hipLaunchKernelGGL(teacher_merge_kernel<16>, dim3((unsigned)rows), dim3(kMergeThreads), 0, s, a);
+  } else {
     hipLaunchKernelGGL(teacher_row_kernel<false>, grid, dim3(kSegThreads), lds, s, a);
-  hipLaunchKernelGGL(teacher_merge_kernel, dim3((unsigned)rows), dim3(kMergeThreads), 0, s, a);
+    hipLaunchKernelGGL(teacher_merge_kernel<0>, dim3((unsigned)rows), dim3(kMergeThreads), 0, s, a);
+  }
   return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
 }

@@ -32,7 +32,7 @@ SPEC_SCHED_GLOBAL = 1
 SPEC_VERIFY_LEFT_TO_RIGHT = 0x100
 SPEC_DISTILL_KL = 0
 SPEC_DISTILL_TV = 1
-SPEC_DISTILL_SAVED = 6
+SPEC_DISTILL_SAVED = 8
 
 REQ_BAD_TOKEN = 1
 REQ_BAD_TEMPERATURE = 2

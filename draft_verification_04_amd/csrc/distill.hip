@@ -6,7 +6,8 @@
 //   KL: sum_e p_e ln(p_e / q_e) + r_t ln(r_t / r_s)
 //   TV: sum_e max(p_e - q_e, 0) + max(r_t - r_s, 0)   (DSpark paper, §3.3 and Eq. 8)
 // Their derivatives are multiples of q outside the list and q b - c_e in it:
-//   KL: a = 1 - r_t / r_s, b = 1, c_e = p_e
+//   KL: b = sum of p_e + r_t (1, unless the teacher's normaliser is rounded or lies below its list's),
+//       a = b - r_t / r_s, c_e = p_e
 //   TV: b = sum of q_e over p_e > q_e, + r_s if r_t > r_s;  a = b - [r_t > r_s];  c_e = [p_e > q_e] q_e
 //   dz_v = grad_loss / T * (q_v a, or q_e b - c_e)
 //
@@ -118,7 +119,6 @@ __device__ __forceinline__ void finish_row(ListShared& sh, const DistillArgs& a,
     }
     return;
   }
-  double t = (double)tl * kLog2eSeg;   // log2 of p's normaliser (with a tail)
   double lsum = 0.0, tsum = 0.0;
 #pragma unroll 1
   for (int e0 = 0; e0 < K; e0 += SPEC_WAVE) {
@@ -141,6 +141,7 @@ __device__ __forceinline__ void finish_row(ListShared& sh, const DistillArgs& a,
   tsum = wave_sum(tsum);
   // lanes s the segments' shares exp2(ref - mo), lane 62 exp2(tmax - t), lane 63 exp2(mo - zmax)
   static_assert(kMaxSegs <= 62, "lanes of the segments");
+  const double t = tail ? (double)tl * kLog2eSeg : tmax;   // p = exp2((v c - t) - tl2)
   const double sc = exp2(lane == 62 ? tmax - t : lane == 63 ? mo - zmax : ref - mo);
   const double out = wave_sum(seg_on ? seg * sc : 0.0);
   const double rest = outside ? out * read_lane(sc, 63) : 0.0;   // outside the list, against zmax
@@ -151,13 +152,14 @@ __device__ __forceinline__ void finish_row(ListShared& sh, const DistillArgs& a,
   const int which = lane & 3;
   const double lg = log2(which == 0 ? out : which == 1 ? tot : which == 2 ? tsum : rt);
   const double lout = read_lane(lg, 0), lt = read_lane(lg, 1), lrt = read_lane(lg, 3);
-  if (!tail) t = tmax + read_lane(lg, 2);
+  // (the normalisers stay in two parts: beside logits of 1e17 T and more their logarithm would be lost)
+  const double tl2 = tail ? 0.0 : read_lane(lg, 2);
   double loss = 0.0, bv = 0.0;
 #pragma unroll 1
   for (int e = lane; e < K; e += SPEC_WAVE) {
     const double pe = sh.te[e] * ps, qe = sh.el[e] * itot;
     if (a.mode == SPEC_DISTILL_KL) {
-      if (pe > 0.0) loss += pe * (((double)sh.val[e] * c - t) - ((double)sh.z[e] * c - zmax - lt));
+      if (pe > 0.0) loss += pe * (((double)sh.val[e] * c - t - tl2) - ((double)sh.z[e] * c - zmax - lt));
     } else if (pe > qe) {
       loss += pe - qe;
       bv += qe;
@@ -166,8 +168,8 @@ __device__ __forceinline__ void finish_row(ListShared& sh, const DistillArgs& a,
   loss = wave_sum(loss);
   double ars;   // a r_s: q a = (q / r_s) (a r_s) outside the list, finite however small r_s
   if (a.mode == SPEC_DISTILL_KL) {
-    bv = 1.0;
-    ars = rs - rt;
+    bv = tail ? tsum * ps + rt : 1.0;
+    ars = bv * rs - rt;
     // in logs (the tail may lie hundreds of nats below the list); +inf when the draft leaves no mass there
     if (rt > 0.0) loss += rt * (lrt - (outside ? mo - zmax + lout - lt : -INFINITY));
     loss *= kLn2Seg;
@@ -188,7 +190,9 @@ __device__ __forceinline__ void finish_row(ListShared& sh, const DistillArgs& a,
   sv[2] = outside ? ars : 0.0;
   sv[3] = bv;
   sv[4] = t;
-  sv[5] = zmax + lt;
+  sv[5] = tl2;
+  sv[6] = zmax;
+  sv[7] = lt;
   a.loss[r] = (float)loss;
   a.row_status[r] = 0;
 }
@@ -447,7 +451,7 @@ __global__ __launch_bounds__(kSegThreads) void distill_grad_kernel(DistillArgs a
   memory_barrier();   // the segment's stores are done: the listed tokens' go over them
   if (id >= 0) {
     const double c2 = scale_of(T);
-    const double q = exp2((double)ze * c2 - sv[5]), p = exp2((double)val * c2 - sv[4]);
+    const double q = exp2((double)ze * c2 - sv[6] - sv[7]), p = exp2((double)val * c2 - sv[4] - sv[5]);
     const double c = a.mode == SPEC_DISTILL_KL ? p : (p > q ? q : 0.0);
     store_elem<BF16>(out, id, (float)(s * (q * sv[3] - c)));
   }

@@ -312,7 +312,7 @@ __device__ __forceinline__ SegSum segment_sum(SegSumShared& sh, float S1, const 
     t.sum += sh.s[w];
     bad |= sh.odd[w];
   }
-  t.ref = (double)mr * ((double)c_hi + (double)c_lo);
+  t.ref = (double)mr * rf.c;   // exactly the exponent of a logit mr, also where mr c is so large that its neighbours differ by more
   return t;
 }
 

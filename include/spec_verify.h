@@ -113,7 +113,7 @@ enum {
     SPEC_DISTILL_KL = 0, /* KL(teacher || draft) */
     SPEC_DISTILL_TV = 1  /* total variation distance, 1 - the overlap mass */
 };
-#define SPEC_DISTILL_SAVED 6 /* float64 words per position that the forward call leaves for the backward */
+#define SPEC_DISTILL_SAVED 8 /* float64 words per position that the forward call leaves for the backward */
 
 int32_t spec_abi_version(void);
 const char* spec_status_string(int32_t status);
@@ -593,7 +593,7 @@ int32_t spec_sts_apply(int32_t B, int32_t gamma, const float* conf_logits, const
  *                kernels finish on `stream`.
  * Errors: as for spec_overlap_mass; SPEC_ERR_INVALID_ARG for K; and
  * SPEC_ERR_UNSUPPORTED when a launch would pass 2^32 work-items (512 per row
- * and per 64 KB of a row).
+ * and segment of a row, 1 to 16 of them; a segment holds at most 320 KB).
  */
 size_t spec_teacher_workspace_size(int32_t B, int32_t gamma, int32_t V, int32_t K);
 
@@ -646,7 +646,8 @@ int32_t spec_teacher_topk(int32_t B, int32_t gamma, int32_t V, int32_t dtype, co
  *   grad_loss    [B, gamma] float32
  *   grad_out     [B, gamma, V] dtype, 16-byte aligned; may be draft_logits
  *                itself (each logit is read before its gradient is written)
- * No workspace; one kernel.  Errors: as above.
+ * No workspace; one kernel (512 work-items per row and 64 KB of a row).  Errors:
+ * as above.
  */
 size_t spec_distill_workspace_size(int32_t B, int32_t gamma, int32_t V, int32_t K);
 
@@ -693,7 +694,8 @@ int32_t spec_distill_loss_backward(int32_t B, int32_t gamma, int32_t V, int32_t 
  *   `dtype`; either may be NULL.  The logits are formed again, a piece of the
  *   vocabulary at a time.  A row left out, with a bad label or with an lse that
  *   is not finite adds nothing to grad_weight and gets a zero row of grad_hidden.
- *   Results do not depend on scheduling (no atomics).
+ *   Results do not depend on scheduling.  The softmax is taken against lse, whose
+ *   rounding is a relative error of 2^-24 |lse_n| of row n's.
  *   grad_loss    [N] float32
  *   grad_hidden, grad_weight: 16-byte aligned, distinct from the inputs
  *   workspace    at least spec_head_xent_backward_workspace_size(N, V, d, dtype)

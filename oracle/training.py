@@ -45,6 +45,15 @@ def _lse(x):
         return np.log(np.exp(x - m).sum(axis=-1)) + m[..., 0]
 
 
+def _log_softmax(x, total=None):
+    """x - ln sum exp(total), total = x by default, for sums whose logarithm is lost beside the values:
+    the largest value is taken off first."""
+    total = x if total is None else total
+    m = np.max(total)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        return (x - m) - np.log(np.exp(total - m).sum())
+
+
 def _request_status(L, G, T):
     if L < 0 or L > G:
         return STATUS_BAD_LENGTH
@@ -115,11 +124,14 @@ def distill_loss(draft, ids, values, teacher_lse=None, mode="kl", lengths=None, 
                 st |= STATUS_NONFINITE
             if st:
                 continue
-            lq = z / T - _lse(z / T)
+            lq = _log_softmax(z / T)
             outside = np.ones(V, dtype=bool)
             outside[at] = False
-            lo = _lse(np.where(outside, z / T, -np.inf)) - _lse(z / T) if outside.any() else -np.inf
-            lp = v / T - (_lse(v / T) if tl is None else tl[i, k])
+            zo = z[outside] / T
+            lo = -np.inf
+            if (zo > -np.inf).any():   # both sums against the outside's largest value, then that value's own share
+                lo = _log_softmax(zo.max(), z / T) - _log_softmax(zo.max(), zo)
+            lp = _log_softmax(v / T) if tl is None else v / T - tl[i, k]
             p, q, rs = np.exp(lp), np.exp(lq), np.exp(lo)
             rt = max(0.0, 1.0 - p.sum()) if tl is not None and outside.any() else 0.0
             qs[i, k] = q

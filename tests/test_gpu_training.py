@@ -2,9 +2,11 @@
 
 Tolerances (u = 2^-24, half a step of fp32):
   exponentials and sums: a term exp((z - m) / T) carries at most 1 ulp (2 u) of exp2 and 3 u x of its
-    exponent, x = |z - m| / T; a thread adds at most 64 + 1 terms in fp32 and the rest is fp64.  The sum is
-    off by at most u (65 + 2 + 3 E[x]) relative, and E[x] <= ln V + 1 over a softmax of V terms:
-    u (67 + 3 * 14.2) < 110 u for every V <= 2^19 + 1.
+    exponent, x = |z - m| / T (a rounded difference or scale, and one multiply-add); a thread adds its
+    vectors in pairs (3 levels) and at most 40 of them and a scalar one after the other in fp32, a term's
+    sum is rounded at most 44 < 65 times, and the rest is fp64.  The sum is off by at most
+    u (65 + 2 + 3 E[x]) relative, and E[x] <= ln V + 1 over a softmax of V terms: u (67 + 3 * 14.2) < 110 u
+    for every V <= 2^19 + 1.
   lse: 110 u + u |lse| for the final rounding.
   distillation losses: they depend on sums over the row through one normaliser and the tail's
     logarithm, each weighed by at most 1: 220 u + u |loss|; 400 u covers both and the margins of the
@@ -138,7 +140,7 @@ def test_teacher_topk_status(sv):
     _check_teacher(got, ref)
 
 
-def _check_distill(sv, draft, ids, vals, tlse, mode, L, T, w, in_place=False):
+def _check_distill(sv, draft, ids, vals, tlse, mode, L, T, w, in_place=False, far_tail=False):
     name = "kl" if mode == sv.SPEC_DISTILL_KL else "tv"
     ref = oracle.distill_loss(draft, ids, vals, tlse, name, L, T, w)
     # no pair so near p = q that rounding could pick the other side: q is off by 110 u, r_s (one sum
@@ -161,6 +163,13 @@ def _check_distill(sv, draft, ids, vals, tlse, mode, L, T, w, in_place=False):
         scale = np.where(np.isfinite(Td) & (Td > 0), np.abs(_np(w)).T / Td, 0.0).T[..., None]
     eps = torch.finfo(draft.dtype).eps
     tol = 700 * U * ref["q"] * scale + eps / 2 * (1 + 2 ** -10) * np.abs(ref["grad"]) + 1e-37
+    if far_tail:
+        # r_t large beside r_s: outside the list the gradient is (q / r_s) (b r_s - r_t), its second factor
+        # fp64 and no longer about r_s.  q / r_s is off by 110 u (its sum) and 3 u x, x <= 104 before it is
+        # 0 in fp32: 422 u < 700 u of the gradient.
+        outside = torch.ones(draft.shape, dtype=torch.bool)
+        outside.scatter_(2, ids.cpu().long(), False)
+        tol += 700 * U * np.abs(ref["grad"]) * outside.numpy()
     err = np.abs(_np(grad) - ref["grad"])
     assert (err <= tol).all(), (np.argwhere(err > tol)[:5], err.max())
     return got, grad, ref
@@ -240,6 +249,98 @@ def test_distill_status_and_empty_rows(sv):
     lse[6, 1] = float("inf")
     _, _, ref = _check_distill(sv, d, ids, vals, lse, 0, L, T, w)
     assert ref["status"].tolist() == [0, 0, 1, 1, 256, 4, 4, 4, 8, 2, 4, 0]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_walked_whole(sv, dtype):
+    """Rows of several chunks, one workgroup each (512 rows or more): values that rise with the token id
+    (each chunk's bound is passed by the next one's), ties, and ordinary rows."""
+    B, G, V = 64, 8, 50021
+    t, d, L, T, w = _dist_inputs(71, B, G, V, dtype)
+    t[0] = (torch.arange(V, device=DEV) / 64.0).to(t.dtype)
+    t[1] = 1.5
+    t[2] = torch.where(torch.arange(V, device=DEV) % 7 == 0, 2.0, -1.0).to(t.dtype)
+    t[3] = -float("inf")
+    t[3, :, V - 1] = 0.25
+    t[4, :, V // 2:] += 200.0        # past the first chunk's reference by more than fp32 holds
+    d[4, :, V // 2:] += 200.0
+    L[:5] = torch.tensor([8, 3, 5, 8, 8], dtype=torch.int32)
+    for K, tail in ((16, True), (256, False)):
+        print(f"whole rows {dtype} K={K}", flush=True)
+        o = sv.teacher_topk(t, K, L, T)
+        torch.cuda.synchronize()
+        _check_teacher(o, oracle.teacher_topk(t, K, L, T))
+        _check_distill(sv, d, o["ids"], o["values"], o["lse"] if tail else None, 0, L, T, w)
+
+
+def test_many_requests_with_lengths(sv):
+    """Up to 4096 requests the live rows are found by a prefix sum, beyond that rows keep their places."""
+    for B in (513, 4096, 4097):
+        t, d, L, T, w = _dist_inputs(B, B, 2, 130, "bf16")
+        L[5], T[7] = 3, 0.0
+        print(f"requests {B}", flush=True)
+        o = sv.teacher_topk(t, 9, L, T)
+        torch.cuda.synchronize()
+        _check_teacher(o, oracle.teacher_topk(t, 9, L, T))
+        _check_distill(sv, d, o["ids"], o["values"], None, 0, L, T, w)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_masks_of_the_lowest_value(sv, dtype):
+    """Masked tokens at the type's lowest finite value have no mass; a row of nothing else is uniform."""
+    low = torch.finfo(DT[dtype]).min
+    t, d, L, T, w = _dist_inputs(81, 4, 3, 9001, dtype, ragged=False)
+    m = torch.arange(9001, device=DEV) % 3 != 0
+    t[:, :, m] = low
+    d[:, :, m] = low
+    t[2, 1], d[2, 1] = low, low
+    T[2] = 1.25                      # low / T is finite
+    for K in (20, 256):
+        print(f"lowest {dtype} K={K}", flush=True)
+        o = sv.teacher_topk(t, K, L, T)
+        torch.cuda.synchronize()
+        _check_teacher(o, oracle.teacher_topk(t, K, L, T))
+        _check_distill(sv, d, o["ids"], o["values"], None, 0, L, T, w)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_extreme_temperatures(sv, dtype):
+    """Temperatures towards 0 (the argmax) and towards infinity (uniform).  (KL: at both ends p = q.)"""
+    t, d, _, T, w = _dist_inputs(83, 5, 2, 4099, dtype, ragged=False)
+    T = torch.tensor([1e-30, 1e-4, 1e-2, 1e4, 1e30], device=DEV)
+    o = sv.teacher_topk(t, 33, None, T)
+    torch.cuda.synchronize()
+    _check_teacher(o, oracle.teacher_topk(t, 33, None, T))
+    _check_distill(sv, d, o["ids"], o["values"], None, 0, None, T, w)
+    c = slice(1, 4)
+    _check_distill(sv, d[c].clone(), o["ids"][c].clone(), o["values"][c].clone(),
+                   o["lse"][c].clone(), 0, None, T[c].clone(), w[c].clone(), far_tail=True)
+
+
+def test_offsets_past_32_bits(sv):
+    """Logits of more than 4 GiB: the last request's rows, behind requests without work."""
+    B, G, V = 130, 64, 262143
+    lt, ld, _, _, lw = _dist_inputs(91, 1, G, V, "bf16", ragged=False)
+    t = torch.zeros((B, G + 1, V), dtype=torch.bfloat16, device=DEV)
+    d = torch.zeros((B, G, V), dtype=torch.bfloat16, device=DEV)
+    t[-1], d[-1] = lt[0], ld[0]
+    assert t.numel() * 2 > 2 ** 32 and d.numel() * 2 > 2 ** 32
+    L = torch.zeros(B, dtype=torch.int32, device=DEV)
+    L[-1] = 5
+    w = lw.expand(B, G).contiguous()
+    print("past 32 bits", flush=True)
+    o = sv.teacher_topk(t, 12, L)
+    f = sv.distill_loss(d, o["ids"], o["values"], o["lse"], 0, L)
+    g = sv.distill_loss_backward(d, o["ids"], o["values"], f["saved"], w)
+    torch.cuda.synchronize()
+    one = {k: v[-1:] for k, v in o.items()}
+    _check_teacher(one, oracle.teacher_topk(lt, 12, L[-1:], None))
+    assert (o["ids"][:-1] == -1).all() and (f["loss"][:-1] == 0).all()
+    ref = oracle.distill_loss(ld, one["ids"], one["values"], one["lse"], "kl", L[-1:], None, lw)
+    assert (np.abs(_np(f["loss"][-1:]) - ref["loss"]) <= U * (400 + np.abs(ref["loss"]))).all()
+    tol = 700 * U * ref["q"] * np.abs(_np(lw))[..., None] + 2.0 ** -8 * (1 + 2 ** -10) * np.abs(ref["grad"]) + 1e-37
+    assert (np.abs(_np(g[-1:]) - ref["grad"]) <= tol).all()
+    assert not g[:-1].any()
 
 
 def test_distill_list_in_any_order_and_unused_entries(sv):
@@ -350,6 +451,74 @@ def test_head_xent_one_gradient_only(sv):
     torch.cuda.synchronize()
     assert set(a) == {"grad_hidden"} and set(b) == {"grad_weight"}
     assert torch.equal(a["grad_hidden"], both["grad_hidden"]) and torch.equal(b["grad_weight"], both["grad_weight"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_head_xent_one_label_for_many_rows(sv, dtype):
+    """Every row names one of two tokens: the sums of a token's row of grad_weight run over all rows."""
+    h, w, y, gl = _head_inputs(23, 2100, 300, 1032, dtype)
+    y[:] = 7
+    y[1030:1040] = 299
+    y[2050] = -1
+    h[3, 5] = float("inf")
+    _check_head(sv, h, w, y, gl)
+
+
+@pytest.mark.parametrize("dtype,V,d", [("bf16", 300001, 16), ("f32", 5001, 8200)])
+def test_head_xent_pieces_for_one_gradient(sv, dtype, V, d):
+    """A vocabulary in pieces for few rows, and each gradient alone."""
+    print(f"head pieces {V} {d} {dtype}", flush=True)
+    h, w, y, gl = _head_inputs(24, 5, V, d, dtype)
+    y[:3] = torch.tensor([V - 1, 0, V // 2])
+    _, both, _ = _check_head(sv, h, w, y, gl)
+    lse = sv.head_xent(h, w, y)["lse"]
+    a = sv.head_xent_backward(h, w, y, lse, gl, need_weight=False)
+    b = sv.head_xent_backward(h, w, y, lse, gl, need_hidden=False)
+    torch.cuda.synchronize()
+    assert torch.equal(a["grad_hidden"], both["grad_hidden"]) and torch.equal(b["grad_weight"], both["grad_weight"])
+
+
+def test_head_xent_offsets_past_32_bits(sv):
+    """A head of more than 4 GiB, zero but for a few rows: with z = 0 for V - 3 tokens the loss, lse and
+    gradients follow in closed form.  The rows hold small integers times powers of two, so the logits are
+    exact (no rounding in fp32) and only the softmax rounds."""
+    N, V, d = 3, 262143, 16384
+    W = torch.zeros((V, d), dtype=torch.bfloat16, device=DEV)
+    h = torch.zeros((N, d), dtype=torch.bfloat16, device=DEV)
+    assert W.numel() * 2 > 2 ** 32
+    toks = [0, V - 2, V - 1]
+    for n, v in enumerate(toks):
+        W[v, n::4] = 0.5
+        h[n, n::4] = 2.0 ** -8
+        h[n, (n + 1) % 3::4] = 2.0 ** -9
+    y = torch.tensor([V - 1, V - 2, V - 1], dtype=torch.int32, device=DEV)
+    gl = torch.tensor([1.0, -0.5, 2.0], device=DEV)
+    print("head past 32 bits", flush=True)
+    got = sv.head_xent(h, W, y)
+    b = sv.head_xent_backward(h, W, y, got["lse"], gl)
+    torch.cuda.synchronize()
+    H, Z = _np(h), np.zeros((N, 3))
+    Ws = _np(W[toks])
+    Z = H @ Ws.T
+    lse = np.log(np.exp(Z).sum(1) + (V - 3))
+    p = np.exp(Z - lse[:, None])
+    hot = np.array([[int(y[n]) == v for v in toks] for n in range(N)], dtype=float)
+    assert (np.abs(_np(got["lse"]) - lse) <= U * (310 + lse)).all()
+    assert (np.abs(_np(got["loss"]) - (lse - (Z * hot).sum(1))) <= U * (310 + 2 * lse + np.abs(Z).max())).all()
+    Gm = (p - hot) * _np(gl)[:, None]
+    # G: p off by (dlse + 310 u) of itself, half a step of bf16 in the product; half a step for the result
+    eG = (620 + lse.max()) * U * p * np.abs(_np(gl))[:, None] * 1.01 + (2.0 ** -8 * 1.01 + 4 * U) * np.abs(Gm)
+    gh, gw = Gm @ Ws, Gm.T @ H
+    th = eG @ np.abs(Ws) + 2.0 ** -8 * 1.01 * np.abs(gh) + 16 * U * (np.abs(Gm) @ np.abs(Ws))
+    tw = eG.T @ np.abs(H) + 2.0 ** -8 * 1.01 * np.abs(gw) + 16 * U * (np.abs(Gm).T @ np.abs(H))
+    assert (np.abs(_np(b["grad_hidden"]) - gh) <= th).all()
+    assert (np.abs(_np(b["grad_weight"][toks]) - gw) <= tw).all()
+    # every other token: p0 = 1 / sum of the row, the same row for all of them
+    g0 = (np.exp(-lse) * _np(gl)) @ H
+    rest = b["grad_weight"][1:V - 2]
+    assert torch.equal(rest.min(0).values, rest.max(0).values)
+    t0 = (np.exp(-lse) * np.abs(_np(gl))) @ np.abs(H) * (2.0 ** -8 * 1.01 + 700 * U) + 2.0 ** -8 * 1.01 * np.abs(g0)
+    assert (np.abs(_np(rest[0]) - g0) <= t0).all()
 
 
 def test_gradients_against_differences(sv):

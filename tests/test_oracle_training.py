@@ -61,6 +61,20 @@ def test_tv_is_one_minus_the_overlap_mass():
     assert np.allclose(o["loss"], 1.0 - oracle.overlap_mass(t, d, None, T)["overlap"], rtol=0, atol=1e-12)
 
 
+def test_rows_of_one_huge_value_are_uniform():
+    """Every logit at the lowest fp32 value (a row that a mask leaves empty): q = 1/V, p = 1/K."""
+    V, K = 50, 8
+    d = np.full((1, 1, V), np.finfo(np.float32).min)
+    ids, vals = np.arange(K).reshape(1, 1, K), np.full((1, 1, K), np.finfo(np.float32).min)
+    kl = oracle.distill_loss(d, ids, vals, grad_loss=np.ones((1, 1)))
+    assert abs(kl["loss"][0, 0] - np.log(V / K)) < 1e-14
+    want = np.full(V, 1 / V)
+    want[:K] -= 1 / K
+    assert np.abs(kl["grad"][0, 0] - want).max() < 1e-15
+    tv = oracle.distill_loss(d, ids, vals, mode="tv")
+    assert abs(tv["loss"][0, 0] - (1 - K / V)) < 1e-14
+
+
 def test_the_tail_is_one_bucket():
     """With the tail kept the loss is that of the distributions over K + 1 outcomes."""
     rng, t, d = _rows(4, B=1, G=1)

@@ -7,12 +7,16 @@
 // (out[j][i] = sum_k A[i][k] B[j][k], both row-major with k contiguous), with an epilogue per use:
 //   kStats  A = W, B = H: per row and per strip of the vocabulary, the largest logit and the sum of
 //           exp against it, and the label's logit; xent_combine_kernel adds the strips in fp64.
-//   kGradZ  the same product again for a piece of the vocabulary; the epilogue forms G and stores it
-//           both ways round, [N, piece] and [piece, N].
-//   kAcc    dH += G W over the piece: A = W^T (the piece transposed once), B = G; fp32 in memory.
+//   kGradZ  the same product again for a piece of the vocabulary; the epilogue forms G.
+//   kAcc    dH += G W over the piece: A = W^T, B = G; fp32 in memory.
 //   kStore  dW of the piece: A = H^T, B = G^T; rounded to the storage type.
+// W^T, H^T and G^T are read as they lie, turned by the transposing LDS read, in bf16; fp32 has no such read
+// and takes transposed copies (bf16 by copies: 18.1 ms in place of 17.4 on the case below).
 // G is rounded to bf16 for its products; its one large entry per row, the label's, is corrected in fp32.
-// The pieces bound the memory: G, G^T and W^T of one piece at a time instead of N V logits.
+// The pieces bound the memory: G of one piece at a time instead of N V logits.
+//
+// Bound by the matrix units.  MI355X, N = 4096, V = 151936, d = 4352, bf16 (a product is 5.42 TFLOP): kStats
+// 3.98 ms (1360 TFLOP/s), kGradZ in 10 pieces 4.67 ms (1160), kAcc 4.19 ms (1290), kStore 4.28 ms (1270).
 //
 // Operands in LDS: a step of 128 bytes of k (64 bf16 or 32 fp32) per row, rows 128 bytes apart, the
 // 16-byte chunk c of row r stored at c ^ (r & 7), so that the 16 rows an MFMA operand read touches
@@ -22,8 +26,6 @@
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
-
-#include <type_traits>
 
 #include "common.hpp"
 #include "rowseg.hpp"
@@ -35,6 +37,7 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int v2u32 __attribute__((ext_vector_type(2)));
 
 #define SPEC_GLOBAL __attribute__((address_space(1)))
 #define SPEC_LDS __attribute__((address_space(3)))
@@ -50,7 +53,8 @@ struct GemmArgs {
   const char* B;     // [rowsB] rows ldb bytes apart
   size_t lda, ldb;
   int rowsA, rowsB;
-  int kbytes;        // of a row (a multiple of 16)
+  int kbytes;        // of a row (a multiple of 16); the contraction's length times the element size
+  int arows;         // rows of a k-major A that exist (past them the last one is read: B is zero there)
   int ti, tj;        // tiles
   int whole, parts;  // tiles taken by one workgroup each; the rest by `parts` workgroups each (kAcc)
   // kStats, kGradZ
@@ -109,6 +113,18 @@ __device__ __forceinline__ void interleave() {
   __builtin_amdgcn_sched_group_barrier(0x008, M % R, 0);
 }
 
+// bf16 operands that lie the other way round in memory, k along the rows ("k-major": dH = G W takes W, dW =
+// G^T H takes both): the tile keeps the memory's layout, 64 rows of k and W columns, and the transposing
+// LDS read (ds_read_b64_tr_b16: 16 lanes bring 4 rows of 16 values, lane i takes column i) turns it.  Its
+// 16 lanes touch 4 rows of k, 32 bytes each, and a wave rows 8 apart as well: the 32-byte segment s of row
+// r is stored at s ^ kswz(r), so that they fall into different banks.
+__device__ __forceinline__ int kswz(int row) { return (row & 3) | ((row >> 1) & 4); }
+
+__device__ __forceinline__ v2u32 read_tr(const SPEC_LDS char* p) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(v2u32, __builtin_amdgcn_ds_read_tr16_b64_v4i16((SPEC_LDS s16x4*)p));
+}
+
 // A row takes part in the gradient: a label in range and a finite normaliser.
 __device__ __forceinline__ bool live_row(int label, float lse, int V) {
   return label >= 0 && label < V && fabsf(lse) < INFINITY;
@@ -127,7 +143,8 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
   constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
   constexpr int CA = BM * 8 / NTHR, CB = BN * 8 / NTHR;   // 16-byte chunks per thread and step
   constexpr int STAGE = (BM + BN) * kStepBytes;
-  __shared__ __attribute__((aligned(128))) char lds[ST * STAGE];
+  __shared__ __attribute__((aligned(128))) char lds_[ST * STAGE];
+  SPEC_LDS char* const lds = (SPEC_LDS char*)lds_;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wi = wave % WM, wj = wave / WM;
   const int l16 = lane & 15, q = lane >> 4;
@@ -146,104 +163,172 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
   const int bw = min(8, g.tj - band * 8);
   const int i0 = in / bw * BM, j0 = (band * 8 + in % bw) * BN;
 
+  constexpr bool AK = ES == 2 && (KIND == kAcc || KIND == kStore), BK = ES == 2 && KIND == kStore;   // k-major
+  constexpr int KROWS = kStepBytes / ES;   // of k per step
   const int kb = step0 * kStepBytes, kbytes = min(steps * kStepBytes, g.kbytes) - kb;
-  const int full = kbytes / kStepBytes, rem = kbytes - full * kStepBytes;
-  const int nk = full + (rem > 0);
-  const char* A = g.A + (size_t)i0 * g.lda + kb;
-  const char* B = g.B + (size_t)j0 * g.ldb + kb;
+  const int krows = AK ? min(kbytes / ES, g.arows - step0 * KROWS) : 0;
+  const int full = AK ? krows / KROWS : kbytes / kStepBytes, rem = kbytes % kStepBytes;
+  const int nk = (kbytes + kStepBytes - 1) / kStepBytes;
+  const char* A = g.A + (AK ? (size_t)step0 * KROWS * g.lda + (size_t)i0 * ES : (size_t)i0 * g.lda + kb);
+  const char* B = g.B + (BK ? (size_t)step0 * KROWS * g.ldb + (size_t)j0 * ES : (size_t)j0 * g.ldb + kb);
+  const size_t stepA = AK ? (size_t)KROWS * g.lda : kStepBytes, stepB = BK ? (size_t)KROWS * g.ldb : kStepBytes;
 
-  // chunk u of this thread: row (u NW + wave) 8 + lane / 8 of the operand (clamped to the last one),
-  // stored at chunk lane % 8 and so read from chunk (lane % 8) ^ (row % 8)
+  // Chunk u of this thread.  Rows along k: row (u NW + wave) 8 + lane / 8 of the operand (clamped to the last
+  // one), stored at chunk lane % 8 and so read from chunk (lane % 8) ^ (row % 8).  k-major: row (u NW + wave)
+  // 64 / L + lane / L of the step, L = lanes per row, 32-byte segment swizzled by the row (columns clamped
+  // to the last chunk of the row).
   const int lr = lane >> 3, lc = ((lane & 7) ^ lr) * 16;
-  uint32_t va[CA], vb[CB];
+  // (k-major: the chunks of a thread lie 16 rows apart, which the swizzle does not see: one lane offset)
+  constexpr int LA = BM * ES / 16, LB = BN * ES / 16;
+  static_assert(!AK || (NW * (64 / LA) == 16 && LA >= 16), "k-major chunks 16 rows apart");
+  static_assert(!BK || (NW * (64 / LB) == 16 && LB >= 16), "k-major chunks 16 rows apart");
+  constexpr bool B1 = BK || (AK && KIND == kAcc);   // one lane offset for B, too: dH's B has rows for whole tiles
+  uint32_t va[AK ? 1 : CA], vb[B1 ? 1 : CB];
+  if constexpr (AK) {
+    const int r = wave * (64 / LA) + lane / LA;
+    va[0] = (uint32_t)r * (uint32_t)g.lda + min(((lane % LA) ^ (kswz(r) << 1)) * 16, (g.rowsA - i0) * ES - 16);
+  } else {
 #pragma unroll
-  for (int u = 0; u < CA; ++u) va[u] = (uint32_t)min((u * NW + wave) * 8 + lr, g.rowsA - 1 - i0) * (uint32_t)g.lda + lc;
+    for (int u = 0; u < CA; ++u) va[u] = (uint32_t)min((u * NW + wave) * 8 + lr, g.rowsA - 1 - i0) * (uint32_t)g.lda + lc;
+  }
+  if constexpr (BK) {   // whole tiles of columns are allocated
+    const int r = wave * (64 / LB) + lane / LB;
+    vb[0] = (uint32_t)r * (uint32_t)g.ldb + ((lane % LB) ^ (kswz(r) << 1)) * 16;
+  } else if constexpr (B1) {
+    vb[0] = (uint32_t)(wave * 8 + lr) * (uint32_t)g.ldb + lc;
+  } else {
 #pragma unroll
-  for (int u = 0; u < CB; ++u) vb[u] = (uint32_t)min((u * NW + wave) * 8 + lr, g.rowsB - 1 - j0) * (uint32_t)g.ldb + lc;
+    for (int u = 0; u < CB; ++u) vb[u] = (uint32_t)min((u * NW + wave) * 8 + lr, g.rowsB - 1 - j0) * (uint32_t)g.ldb + lc;
+  }
 
-  auto issue_whole = [&](int t) {   // a step of 128 bytes
-    char* dst = lds + (t % ST) * STAGE + wave * 1024;
-    // scalar base + 32-bit lane offset (the compiler would otherwise keep 64-bit lane pointers in registers)
-    size_t off = (size_t)t * kStepBytes;
-    asm("" : "+s"(off));
-    const char* a = A + off;
-    const char* b = B + off;
-#pragma unroll
-    for (int u = 0; u < CA; ++u)
-      __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(a + va[u]), (SPEC_LDS void*)(dst + u * NW * 1024), 16,
-                                       0, 0);
-#pragma unroll
-    for (int u = 0; u < CB; ++u)
-      __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(b + vb[u]),
-                                       (SPEC_LDS void*)(dst + BM * kStepBytes + u * NW * 1024), 16, 0, 0);
+  auto dma = [&](const char* src, uint32_t off, SPEC_LDS char* dst) {
+    __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(src + off), (SPEC_LDS void*)dst, 16, 0, 0);
   };
-  auto issue_rest = [&](int t) {   // the last step of a row that is no multiple of 128 bytes: zeros behind its end
-    char* dst = lds + (t % ST) * STAGE + wave * 1024 + lane * 16;
-    const char* a = A + (size_t)t * kStepBytes;
-    const char* b = B + (size_t)t * kStepBytes;
-    const v4u32 zero = {};
+  auto issue_whole = [&](SPEC_LDS char* dst, int t) {   // a step of 128 bytes
+    dst += wave * 1024;
+    // scalar base + 32-bit lane offset (the compiler would otherwise keep 64-bit lane pointers in registers)
+    size_t oa = t * stepA, ob = t * stepB;
+    asm("" : "+s"(oa), "+s"(ob));
+    const char* a = A + oa;
+    const char* b = B + ob;
 #pragma unroll
-    for (int u = 0; u < CA; ++u)
-      *reinterpret_cast<v4u32*>(dst + u * NW * 1024) = lc < rem ? *reinterpret_cast<const v4u32*>(a + va[u]) : zero;
+    for (int u = 0; u < CA; ++u) dma(AK ? a + u * 16 * g.lda : a, va[AK ? 0 : u], dst + u * NW * 1024);
 #pragma unroll
     for (int u = 0; u < CB; ++u)
-      *reinterpret_cast<v4u32*>(dst + BM * kStepBytes + u * NW * 1024) =
-          lc < rem ? *reinterpret_cast<const v4u32*>(b + vb[u]) : zero;
+      dma(B1 ? b + u * (BK ? 16 : NW * 8) * g.ldb : b, vb[B1 ? 0 : u], dst + BM * kStepBytes + u * NW * 1024);
+  };
+  // The last step of rows that are no multiple of 128 bytes: zeros behind their end.  Of a k-major A whose
+  // rows end within the step: the last row again.
+  auto issue_rest = [&](SPEC_LDS char* dst, int t) {
+    dst += wave * 1024;
+    const char* a = A + t * stepA;
+    const char* b = B + t * stepB;
+    if constexpr (AK) {
+      const int last = krows - 1 - t * KROWS;
+#pragma unroll
+      for (int u = 0; u < CA; ++u) {
+        const int past = max((u * NW + wave) * (64 / LA) + lane / LA - last, 0);
+        dma(a + u * 16 * g.lda - (size_t)past * g.lda, va[0], dst + u * NW * 1024);
+      }
+#pragma unroll
+      for (int u = 0; u < CB; ++u)
+        dma(B1 ? b + u * (BK ? 16 : NW * 8) * g.ldb : b, vb[B1 ? 0 : u], dst + BM * kStepBytes + u * NW * 1024);
+    } else {
+      const v4u32 zero = {};
+      dst += lane * 16;
+#pragma unroll
+      for (int u = 0; u < CA; ++u)
+        *reinterpret_cast<SPEC_LDS v4u32*>(dst + u * NW * 1024) = lc < rem ? *reinterpret_cast<const v4u32*>(a + va[AK ? 0 : u]) : zero;
+#pragma unroll
+      for (int u = 0; u < CB; ++u)
+        *reinterpret_cast<SPEC_LDS v4u32*>(dst + BM * kStepBytes + u * NW * 1024) =
+            lc < rem ? *reinterpret_cast<const v4u32*>(b + vb[B1 ? 0 : u]) : zero;
+    }
   };
   auto issue = [&](int t) {
-    if (t < full) issue_whole(t);
-    else if (t < nk) issue_rest(t);
+    if (t < full) issue_whole(lds + (t % ST) * STAGE, t);
+    else if (t < nk) issue_rest(lds + (t % ST) * STAGE, t);
   };
 
   f32x4 c[MT][NT] = {};
   const int ra = (wi * MT * 16 + l16) * kStepBytes, rb = BM * kStepBytes + (wj * NT * 16 + l16) * kStepBytes;
+  // k-major: the lane's row of k within a group of four, its 8 bytes of the 32, its segment against the swizzle
+  const int kr = l16 >> 2, k8 = (l16 & 3) * 8, sz = kr | ((q & 1) << 2);
+  const int ta = (q * 8 + kr) * BM * ES + k8 + ((wi * MT) ^ sz) * 32;
+  const int tb = BM * kStepBytes + (q * 8 + kr) * BN * ES + k8 + ((wj * NT) ^ sz) * 32;
   struct Frag {
     v4u32 a[MT], b[NT];
   };
-  auto fetch = [&](Frag& f, int t, int kk) {
-    const char* src = lds + (t % ST) * STAGE + ((kk * 4 + q) ^ (lane & 7)) * 16;
+  auto fetch = [&](Frag& f, const SPEC_LDS char* base, int kk) {   // half kk of a step
+    const SPEC_LDS char* src = base + ((kk * 4 + q) ^ (lane & 7)) * 16;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) f.a[m] = *reinterpret_cast<const v4u32*>(src + ra + m * 16 * kStepBytes);
+    for (int m = 0; m < MT; ++m) {
+      if constexpr (AK) {
+        const SPEC_LDS char* p = base + ((ta ^ (m * 32)) + kk * 32 * BM * ES);
+        const v2u32 x = read_tr(p), y = read_tr(p + 4 * BM * ES);
+        f.a[m] = v4u32{x.x, x.y, y.x, y.y};
+      } else {
+        f.a[m] = *reinterpret_cast<const SPEC_LDS v4u32*>(src + ra + m * 16 * kStepBytes);
+      }
+    }
 #pragma unroll
-    for (int n = 0; n < NT; ++n) f.b[n] = *reinterpret_cast<const v4u32*>(src + rb + n * 16 * kStepBytes);
+    for (int n = 0; n < NT; ++n) {
+      if constexpr (BK) {
+        const SPEC_LDS char* p = base + ((tb ^ (n * 32)) + kk * 32 * BN * ES);
+        const v2u32 x = read_tr(p), y = read_tr(p + 4 * BN * ES);
+        f.b[n] = v4u32{x.x, x.y, y.x, y.y};
+      } else {
+        f.b[n] = *reinterpret_cast<const SPEC_LDS v4u32*>(src + rb + n * 16 * kStepBytes);
+      }
+    }
   };
+  constexpr int READS = MT * (AK ? 2 : 1) + NT * (BK ? 2 : 1);
   auto multiply = [&](const Frag& f) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int n = 0; n < NT; ++n) c[m][n] = mma<ES>(f.a[m], f.b[n], c[m][n]);
   };
-  // Half a step ahead: while one half step's operands are multiplied the next one's are read from LDS.
-  // The barrier stands in the middle of a step: behind it step t's buffer is free (every wave has read
-  // its second half) and step t + 1's has landed.
+  // Half a step ahead: while one half step's operands are multiplied the next one's are read from LDS (22.4
+  // -> 18.3 ms on the case above against reading them behind the barrier).  A
+  // turn starts behind the barrier: every wave has read all of step t (its second half, f1, is still to be
+  // multiplied), whose buffer takes step t + ST, and step t + 1 has landed.  The buffers are restrict
+  // arguments: the compiler would otherwise have every read wait for the loads in flight.
+  constexpr int MM = MT * NT * (ES == 2 ? 1 : 4);
+  Frag f0, f1;
+  auto turn = [&](SPEC_LDS char* __restrict__ free, const SPEC_LDS char* __restrict__ cur, int t) {
+    issue_whole(free, t + ST);
+    fetch(f0, cur, 0);
+    multiply(f1);
+    __builtin_amdgcn_sched_group_barrier(0x010, CA + CB, 0);   // the loads from memory first (last: kStats + 14%)
+    interleave<READS, MM>();
+    fetch(f1, cur, 1);
+    multiply(f0);
+    interleave<READS, MM>();
+  };
 #pragma unroll
   for (int t = 0; t < ST; ++t) issue(t);
   if (nk > 0) {
-    Frag f0, f1;
     if (nk >= ST) wait_barrier<(ST - 1) * (CA + CB)>();
     else wait_barrier<0>();
-    fetch(f0, 0, 0);
+    fetch(f0, lds, 0);
+    fetch(f1, lds, 1);
+    multiply(f0);
+    if (nk >= ST) wait_barrier<(ST - 2) * (CA + CB)>();
+    else wait_barrier<0>();
     int t = 0;
     for (; t + ST < full; ++t) {
-      fetch(f1, t, 1);
-      multiply(f0);
-      interleave<MT + NT, MT * NT * (ES == 2 ? 1 : 4)>();
+      turn(lds + (t % ST) * STAGE, lds + ((t + 1) % ST) * STAGE, t);
       wait_barrier<(ST - 2) * (CA + CB)>();
-      issue_whole(t + ST);
-      fetch(f0, t + 1, 0);
-      multiply(f1);
-      interleave<MT + NT, MT * NT * (ES == 2 ? 1 : 4)>();
     }
     for (; t + 1 < nk; ++t) {
-      fetch(f1, t, 1);
+      issue(t + ST);
+      fetch(f0, lds + ((t + 1) % ST) * STAGE, 0);
+      multiply(f1);
+      fetch(f1, lds + ((t + 1) % ST) * STAGE, 1);
       multiply(f0);
       wait_barrier<0>();
-      issue(t + ST);
-      fetch(f0, t + 1, 0);
-      multiply(f1);
     }
-    fetch(f1, t, 1);
-    multiply(f0);
     multiply(f1);
   }
 
@@ -315,11 +400,7 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
               if (g.first) atomicMin(&g.first[label], j);
             }
           }
-          if (j < g.rowsB && i < g.vpad) *reinterpret_cast<bf16x4*>(g.gn + (size_t)j * g.ldgn + (size_t)i * 2) = h;
-          if (j < g.npad)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (i + x < g.rowsA) *reinterpret_cast<__bf16*>(g.gt + (size_t)(i + x) * g.ldgt + (size_t)j * 2) = h[x];
+          if (j < g.npad && i < g.vpad) *reinterpret_cast<bf16x4*>(g.gn + (size_t)j * g.ldgn + (size_t)i * 2) = h;
         } else {
           if (j < g.rowsB && i < g.vpad) *reinterpret_cast<f32x4*>(g.gn + (size_t)j * g.ldgn + (size_t)i * 4) = o;
           if (j < g.npad)
@@ -406,47 +487,50 @@ __global__ __launch_bounds__(kCombineThreads) void xent_combine_kernel(const flo
   S = wave_sum(S);
   if (lane == 0) {
     const bool fin = M < INFINITY && M > -INFINITY && S > 0.0 && S < INFINITY;   // NaN sums fail too
-    const double l = (double)M + log(S);
+    const double ls = log(S);
     const int label = labels[row];
     int st = 0;
     if (label < -1 || label >= V) st |= SPEC_REQ_BAD_TOKEN;
     if (label != -1 && !fin) st |= SPEC_REQ_NONFINITE;
-    lse[row] = fin ? (float)l : NAN;
-    loss[row] = label == -1 ? 0.f : (st ? NAN : (float)(l - (double)zlab[row]));
+    lse[row] = fin ? (float)((double)M + ls) : NAN;
+    loss[row] = label == -1 ? 0.f : (st ? NAN : (float)((double)M - (double)zlab[row] + ls));
     if (status) status[row] = st;
   }
 }
 
-// out[c][r] = in[r][c], r < R valid and not left out (else 0) for r < rpad; 64 x 64 tiles.
-template <int ES>
+// fp32: out[c][r] = in[r][c], r < R valid and not left out (else 0) for r < rpad; 64 x 64 tiles.
 __global__ __launch_bounds__(256) void xent_transpose_kernel(const char* in, size_t ldi, int R, int C, char* out,
                                                              size_t ldo, int rpad, const int32_t* labels,
                                                              const float* lse, int V) {
-  constexpr int EPC = 16 / ES, CPR = 64 / EPC;   // elements per chunk, chunks per tile row
-  using E = typename std::conditional<ES == 2, uint16_t, uint32_t>::type;
-  __shared__ E t[64][64 + (ES == 2 ? 2 : 1)];
+  __shared__ uint32_t t[64][65];
   const int r0 = (int)blockIdx.x * 64, c0 = (int)blockIdx.y * 64, tid = threadIdx.x;
-  for (int u = tid; u < 64 * CPR; u += 256) {
-    const int r = u / CPR, cc = u % CPR;
+  for (int u = tid; u < 64 * 16; u += 256) {
+    const int r = u / 16, c = u % 16 * 4;
     v4u32 v = {};
-    const bool on = r0 + r < R && c0 + cc * EPC < C;
+    const bool on = r0 + r < R && c0 + c < C;
     if (on && (!labels || live_row(labels[r0 + r], lse[r0 + r], V)))
-      v = *reinterpret_cast<const v4u32*>(in + (size_t)(r0 + r) * ldi + (size_t)(c0 + cc * EPC) * ES);
-    const E* e = reinterpret_cast<const E*>(&v);
+      v = *reinterpret_cast<const v4u32*>(in + (size_t)(r0 + r) * ldi + (size_t)(c0 + c) * 4);
 #pragma unroll
-    for (int x = 0; x < EPC; ++x) t[r][cc * EPC + x] = e[x];
+    for (int x = 0; x < 4; ++x) t[r][c + x] = v[x];
   }
   __syncthreads();
-  for (int u = tid; u < 64 * CPR; u += 256) {
-    const int cc = u / CPR, rc = u % CPR;
-    if (c0 + cc < C && r0 + rc * EPC < rpad) {
-      v4u32 v;
-      E* e = reinterpret_cast<E*>(&v);
-#pragma unroll
-      for (int x = 0; x < EPC; ++x) e[x] = t[rc * EPC + x][cc];
-      *reinterpret_cast<v4u32*>(out + (size_t)(c0 + cc) * ldo + (size_t)(r0 + rc * EPC) * ES) = v;
-    }
+  for (int u = tid; u < 64 * 16; u += 256) {
+    const int c = u / 16, r = u % 16 * 4;
+    if (c0 + c < C && r0 + r < rpad)
+      *reinterpret_cast<v4u32*>(out + (size_t)(c0 + c) * ldo + (size_t)(r0 + r) * 4) =
+          v4u32{t[r][c], t[r + 1][c], t[r + 2][c], t[r + 3][c]};
   }
+}
+
+// bf16: H with zeros in the rows left out (and up to npad rows): 0 * inf would reach dW otherwise.
+__global__ __launch_bounds__(256) void xent_live_copy_kernel(const v4u32* in, int N, int d8, v4u32* out, long long n8,
+                                                             const int32_t* labels, const float* lse, int V) {
+  const long long t = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (t >= n8) return;
+  const int r = (int)(t / d8);
+  v4u32 v = {};
+  if (r < N && live_row(labels[r], lse[r], V)) v = in[t];
+  out[t] = v;
 }
 
 // grad_hidden = the sums, the parts of a shared tile added in order, rounded once; zeros for the rows
@@ -486,8 +570,9 @@ __global__ __launch_bounds__(256) void xent_finish_kernel(GemmArgs g, int bm, in
 
 // dW of the tokens that are labels (bf16): the label's entry of G, (p - 1) grad_loss, outweighs the rest of
 // its row together, and its rounding alone would add as much again to the gradient's error.  The product
-// leaves these tokens' sums unrounded at their first row; the workgroup of that row adds, in row order,
-// what the rounding left out times the hidden state of every row with the label, and rounds once.
+// leaves these tokens' sums unrounded at their first row; the workgroups of that row (one per 1024 columns)
+// add, in row order, what the rounding left out times the hidden state of every row with the label, and
+// round once.
 constexpr int kLabelThreads = 256;
 
 __global__ __launch_bounds__(kLabelThreads) void xent_fill_kernel(int32_t* p, int n) {
@@ -499,68 +584,63 @@ __global__ __launch_bounds__(kLabelThreads) void xent_label_rows_kernel(const in
                                                                         int V, int d, const float* glab,
                                                                         const int32_t* first, const float* side,
                                                                         const char* hidden, char* out) {
-  constexpr int NW = kLabelThreads / SPEC_WAVE, CHUNK = 4 * kLabelThreads, PER = 4;
+  constexpr int NW = kLabelThreads / SPEC_WAVE, CHUNK = 4 * kLabelThreads;
   __shared__ int32_t rows[CHUNK];
   __shared__ int cnt[NW];
   const int n = (int)blockIdx.x, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int label = labels[n];
   if (!live_row(label, lse[n], V) || first[label] != n) return;
-  const bf16x4* h4 = reinterpret_cast<const bf16x4*>(hidden);
-  const int d4 = d / 4;
-  for (int c0 = 0; c0 < d4; c0 += PER * kLabelThreads) {   // PER groups of four columns per thread
-    f32x4 s[PER];
+  const int d4 = d / 4, c = (int)blockIdx.y * kLabelThreads + tid, cc = min(c, d4 - 1);
+  const bf16x4* h4 = reinterpret_cast<const bf16x4*>(hidden) + cc;
+  f32x4 s = reinterpret_cast<const f32x4*>(side + (size_t)n * d)[cc];
+  for (int m0 = n; m0 < N; m0 += CHUNK) {
+    // the rows of the chunk with this label, in order: a wave takes 4 * 64 rows in a row
+    unsigned long long hit[4];
+    int mine = 0;
 #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-      const int c = min(c0 + u * kLabelThreads + tid, d4 - 1);
-      s[u] = reinterpret_cast<const f32x4*>(side + (size_t)n * d)[c];
+    for (int u = 0; u < 4; ++u) {
+      const int m = m0 + (wave * 4 + u) * SPEC_WAVE + lane, mc = min(m, N - 1);
+      hit[u] = __ballot(m < N && labels[mc] == label && fabsf(lse[mc]) < INFINITY);
+      mine += (int)__popcll(hit[u]);
     }
-    for (int m0 = n; m0 < N; m0 += CHUNK) {
-      // the rows of the chunk with this label, in order: a wave takes 4 * 64 rows in a row
-      unsigned long long hit[4];
-      int mine = 0;
+    __syncthreads();   // the last chunk's rows are read
+    if (lane == 0) cnt[wave] = mine;
+    __syncthreads();
+    int base = 0, total = 0;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int m = m0 + (wave * 4 + u) * SPEC_WAVE + lane, mc = min(m, N - 1);
-        hit[u] = __ballot(m < N && labels[mc] == label && fabsf(lse[mc]) < INFINITY);
-        mine += (int)__popcll(hit[u]);
-      }
-      __syncthreads();   // the last chunk's rows are read
-      if (lane == 0) cnt[wave] = mine;
-      __syncthreads();
-      int base = 0, total = 0;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        base += w < wave ? cnt[w] : 0;
-        total += cnt[w];
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if ((hit[u] >> lane) & 1ull)
-          rows[base + (int)__popcll(hit[u] & ((1ull << lane) - 1))] = m0 + (wave * 4 + u) * SPEC_WAVE + lane;
-        base += (int)__popcll(hit[u]);
-      }
-      __syncthreads();
-#pragma unroll 2
-      for (int e = 0; e < total; ++e) {
-        const int m = rows[e];
-        const float r = glab[m];
-#pragma unroll
-        for (int u = 0; u < PER; ++u) {
-          const bf16x4 x = h4[(size_t)m * d4 + min(c0 + u * kLabelThreads + tid, d4 - 1)];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) s[u][q] += r * (float)x[q];
-        }
-      }
+    for (int w = 0; w < NW; ++w) {
+      base += w < wave ? cnt[w] : 0;
+      total += cnt[w];
     }
 #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-      const int c = c0 + u * kLabelThreads + tid;
-      bf16x4 o;
+    for (int u = 0; u < 4; ++u) {
+      if ((hit[u] >> lane) & 1ull)
+        rows[base + (int)__popcll(hit[u] & ((1ull << lane) - 1))] = m0 + (wave * 4 + u) * SPEC_WAVE + lane;
+      base += (int)__popcll(hit[u]);
+    }
+    __syncthreads();
+    constexpr int U = 8;   // rows in flight
+    for (int e = 0; e < total; e += U) {
+      bf16x4 x[U];
+      float r[U];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) o[q] = (__bf16)s[u][q];
-      if (c < d4) reinterpret_cast<bf16x4*>(out + (size_t)label * d * 2)[c] = o;
+      for (int u = 0; u < U; ++u) {
+        const int m = rows[min(e + u, total - 1)];
+        r[u] = glab[m];
+        x[u] = h4[(size_t)m * d4];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (e + u >= total) break;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s[q] += r[u] * (float)x[u][q];
+      }
     }
   }
+  bf16x4 o;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) o[q] = (__bf16)s[q];
+  if (c < d4) reinterpret_cast<bf16x4*>(out + (size_t)label * d * 2)[c] = o;
 }
 
 // ---- host -------------------------------------------------------------------
@@ -637,7 +717,7 @@ void launch_tiles(GemmArgs& g, int tile, int whole, int parts, hipStream_t s) {
     hipLaunchKernelGGL((xent_gemm_kernel<ES, 256, 256, 2, 4, 2, KIND>), grid, dim3(512), 0, s, g);
   else if (tile == kMid)
     hipLaunchKernelGGL((xent_gemm_kernel<ES, 128, 128, 2, 2, 2, KIND>), grid, dim3(256), 0, s, g);
-  else
+  else if constexpr (KIND != kStore)
     hipLaunchKernelGGL((xent_gemm_kernel<ES, 128, 64, 2, 2, 3, KIND>), grid, dim3(256), 0, s, g);
 }
 
@@ -645,7 +725,8 @@ void launch_tiles(GemmArgs& g, int tile, int whole, int parts, hipStream_t s) {
 // the longer side of either.
 template <int ES, int KIND>
 void launch_gemm(const GemmArgs& g, hipStream_t s) {
-  const Shape sh = pick_shape(g.rowsA, g.rowsB, g.kbytes, ES);
+  Shape sh = pick_shape(g.rowsA, g.rowsB, g.kbytes, ES);
+  if (KIND == kStore && sh.tail == kThin) sh.tail = kMid;   // dW has no thin form
   const bool split = sh.head > 0 && (sh.along_a || KIND == kStore);
   GemmArgs h = g;
   if (split) {
@@ -653,14 +734,15 @@ void launch_gemm(const GemmArgs& g, hipStream_t s) {
     (sh.along_a ? f.rowsA : f.rowsB) = (int)sh.head;
     if (KIND == kGradZ) f.vpad = (int)sh.head;
     launch_tiles<ES, KIND>(f, kBig, INT32_MAX, 1, s);
+    constexpr bool KM = ES == 2 && KIND == kStore;   // k-major: rows of the product are columns in memory
     if (sh.along_a) {
-      h.A += (size_t)sh.head * g.lda;
+      h.A += KM ? (size_t)sh.head * ES : (size_t)sh.head * g.lda;
       h.rowsA -= (int)sh.head;
       if (KIND == kStats || KIND == kGradZ) h.v0 += (int)sh.head;
       if (KIND == kStats) h.part += (size_t)(sh.head / strip_rows(kBig)) * g.rowsB;
       if (KIND == kGradZ) {
         h.gn += (size_t)sh.head * ES;
-        h.gt += (size_t)sh.head * g.ldgt;
+        if (ES == 4) h.gt += (size_t)sh.head * g.ldgt;
         h.vpad -= (int)sh.head;
       }
       if (KIND == kStore) {
@@ -668,7 +750,7 @@ void launch_gemm(const GemmArgs& g, hipStream_t s) {
         h.side += sh.head;
       }
     } else {
-      h.B += (size_t)sh.head * g.ldb;
+      h.B += KM ? (size_t)sh.head * ES : (size_t)sh.head * g.ldb;
       h.rowsB -= (int)sh.head;
       h.out += (size_t)sh.head * g.ldo;
       h.v0 += (int)sh.head;
@@ -689,7 +771,7 @@ int stat_strips(long long V, long long N, int kbytes, int es) {
 // parts of kAcc add at most 16 times the tiles of two rounds).
 bool head_fits(long long N, long long V, long long d) {
   const long long most = 0xffffffffll - 256ll * 1024 * 32;
-  return (long long)ceil_div(V, 128) * ceil_div(N, 64) * 256 <= most && N * d / 4 + 256 <= most &&
+  return (long long)ceil_div(V, 128) * ceil_div(N, 64) * 256 <= most && N * round_to(d, 1024) / 4 + 256 <= most &&
          (long long)ceil_div(V, 128) * ceil_div(d, 64) * 256 <= most;
 }
 
@@ -709,7 +791,7 @@ struct BackPlan {
   size_t total() const { return gn + gt + wt + ht + acc + acc_parts + glab + first + side; }
 };
 
-constexpr long long kPieceBytes = 128ll << 20;   // of G (and of W^T) per piece
+constexpr long long kPieceBytes = 128ll << 20;   // of G (fp32: and of G^T and W^T) per piece
 constexpr int kMaxParts = 16, kPartSteps = 8;    // workgroups per tile at most; steps of one at least
 
 BackPlan back_plan(int N, int V, int d, int dtype) {
@@ -717,7 +799,8 @@ BackPlan back_plan(int N, int V, int d, int dtype) {
   p.es = dtype == SPEC_BF16 ? 2 : 4;
   p.step = kStepBytes / p.es;
   p.npad = round_to(N, p.step);
-  const long long widest = N > d ? N : d;
+  const long long rows = round_to(N, 256);                           // whole tiles of rows
+  const long long widest = p.es == 4 && d > rows ? d : rows;         // fp32: W^T of the piece, too
   long long vmax = kPieceBytes / (widest * p.es) / 256 * 256;
   if (vmax < 256) vmax = 256;
   p.pieces = ceil_div(V, vmax);
@@ -743,9 +826,11 @@ BackPlan back_plan(int N, int V, int d, int dtype) {
       }
     }
   }
-  p.gn = round256((size_t)N * p.vc * p.es);
-  p.gt = round256((size_t)p.vc * p.npad * p.es);
-  p.wt = round256((size_t)d * p.vc * p.es);
+  p.gn = round256((size_t)rows * p.vc * p.es);
+  if (p.es == 4) {   // transposed copies; bf16 operands are turned as they leave LDS
+    p.gt = round256((size_t)p.vc * p.npad * p.es);
+    p.wt = round256((size_t)d * p.vc * p.es);
+  }
   p.ht = round256((size_t)d * p.npad * p.es);
   p.acc = round256((size_t)N * d * sizeof(float));
   if (p.es == 2) {
@@ -802,10 +887,18 @@ int32_t run_backward(int N, int V, int d, int dtype, const void* hidden, const v
   if (first)
     hipLaunchKernelGGL(xent_fill_kernel, dim3(ceil_div(V, kLabelThreads)), dim3(kLabelThreads), 0, s, first, V);
   const size_t ld = (size_t)d * ES;
-  if (grad_weight)
-    hipLaunchKernelGGL(xent_transpose_kernel<ES>, dim3(ceil_div(p.npad, 64), ceil_div(d, 64)), dim3(256), 0, s,
-                       reinterpret_cast<const char*>(hidden), ld, N, d, ht, (size_t)p.npad * ES, (int)p.npad, labels,
-                       lse, V);
+  if (grad_weight) {
+    if constexpr (ES == 2) {
+      const long long n8 = p.npad * (d / 8);
+      hipLaunchKernelGGL(xent_live_copy_kernel, dim3(ceil_div(n8, 256)), dim3(256), 0, s,
+                         reinterpret_cast<const v4u32*>(hidden), N, d / 8, reinterpret_cast<v4u32*>(ht), n8, labels, lse,
+                         V);
+    } else {
+      hipLaunchKernelGGL(xent_transpose_kernel, dim3(ceil_div(p.npad, 64), ceil_div(d, 64)), dim3(256), 0, s,
+                         reinterpret_cast<const char*>(hidden), ld, N, d, ht, (size_t)p.npad * ES, (int)p.npad, labels,
+                         lse, V);
+    }
+  }
   for (int c = 0; c < p.pieces; ++c) {
     const int v0 = c * p.vc, nv = V - v0 < p.vc ? V - v0 : p.vc;
     const int vpad = (int)round_to(nv, p.step);
@@ -820,16 +913,26 @@ int32_t run_backward(int N, int V, int d, int dtype, const void* hidden, const v
     g.glab = h.glab; g.first = first;
     launch_gemm<ES, kGradZ>(g, s);
     if (grad_hidden) {
-      hipLaunchKernelGGL(xent_transpose_kernel<ES>, dim3(ceil_div(vpad, 64), ceil_div(d, 64)), dim3(256), 0, s, w, ld,
-                         nv, d, wt, (size_t)p.vc * ES, vpad, nullptr, nullptr, 0);
+      if constexpr (ES == 2) {
+        h.A = w; h.lda = ld; h.arows = nv;
+      } else {
+        hipLaunchKernelGGL(xent_transpose_kernel, dim3(ceil_div(vpad, 64), ceil_div(d, 64)), dim3(256), 0, s, w, ld,
+                           nv, d, wt, (size_t)p.vc * ES, vpad, nullptr, nullptr, 0);
+      }
       h.kbytes = vpad * ES;
       h.accumulate = c > 0;
       launch_tiles<ES, kAcc>(h, p.tile, p.whole, p.parts, s);
     }
     if (grad_weight) {
       GemmArgs w{};
-      w.A = ht; w.lda = (size_t)p.npad * ES; w.rowsA = d;
-      w.B = gt; w.ldb = (size_t)p.npad * ES; w.rowsB = nv;
+      w.A = ht; w.rowsA = d; w.rowsB = nv;
+      if constexpr (ES == 2) {
+        w.lda = ld; w.arows = (int)p.npad;
+        w.B = gn; w.ldb = (size_t)p.vc * ES;
+      } else {
+        w.lda = (size_t)p.npad * ES;
+        w.B = gt; w.ldb = (size_t)p.npad * ES;
+      }
       w.kbytes = (int)p.npad * ES;
       w.out = reinterpret_cast<char*>(grad_weight) + (size_t)v0 * ld; w.ldo = ld;
       w.v0 = v0; w.first = first; w.side = side; w.side_ld = d;
@@ -837,7 +940,7 @@ int32_t run_backward(int N, int V, int d, int dtype, const void* hidden, const v
     }
   }
   if (first)
-    hipLaunchKernelGGL(xent_label_rows_kernel, dim3(N), dim3(kLabelThreads), 0, s, labels, lse, N, V, d, h.glab, first,
+    hipLaunchKernelGGL(xent_label_rows_kernel, dim3(N, ceil_div(d, 4 * kLabelThreads)), dim3(kLabelThreads), 0, s, labels, lse, N, V, d, h.glab, first,
                        side, reinterpret_cast<const char*>(hidden), reinterpret_cast<char*>(grad_weight));
   if (grad_hidden)
     hipLaunchKernelGGL(xent_finish_kernel<ES>, dim3(ceil_div((long long)N * d / 4, 256)), dim3(256), 0, s, h,

@@ -14,6 +14,12 @@
 //       exp(z / T) are summed on the way, fp32 per thread and fp64 beyond.
 //   teacher_merge_kernel -- one workgroup per row: the same selection over the lists of a row's segments;
 //       and, also for whole rows, the status of the request.
+//
+// Bound by the read of the rows where there are many (MI355X: 256 x 16 rows of 151936 bf16, half of them live,
+// K = 64: 110-122 us, 5.1-5.6 TB/s).  672 rows of 129280 with K = 256 take 55 us, 3.2 TB/s: every row is in
+// flight at once, so the chip waits while all of them start (6 us) and select (12 us: listing 3, the K-th
+// largest 5, the order 3).  The selection's loops kept in registers and unrolled took as long: such code runs
+// once per row and is fetched cold.
 #include "common.hpp"
 #include "rowseg.hpp"
 #include "spec_verify.h"

@@ -201,7 +201,11 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
     for (int u = 0; u < CB; ++u) vb[u] = (uint32_t)min((u * NW + wave) * 8 + lr, g.rowsB - 1 - j0) * (uint32_t)g.ldb + lc;
   }
 
-  auto dma = [&](const char* src, uint32_t off, SPEC_LDS char* dst) {
+  constexpr int kOnce = BN == 64 ? 2 : 0;   // A of a thin tile is read once: nontemporal
+  auto dma_a = [&](const char* src, uint32_t off, SPEC_LDS char* dst) {
+    __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(src + off), (SPEC_LDS void*)dst, 16, 0, kOnce);
+  };
+  auto dma_b = [&](const char* src, uint32_t off, SPEC_LDS char* dst) {
     __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(src + off), (SPEC_LDS void*)dst, 16, 0, 0);
   };
   auto issue_whole = [&](SPEC_LDS char* dst, int t) {   // a step of 128 bytes
@@ -212,10 +216,10 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
     const char* a = A + oa;
     const char* b = B + ob;
 #pragma unroll
-    for (int u = 0; u < CA; ++u) dma(AK ? a + u * 16 * g.lda : a, va[AK ? 0 : u], dst + u * NW * 1024);
+    for (int u = 0; u < CA; ++u) dma_a(AK ? a + u * 16 * g.lda : a, va[AK ? 0 : u], dst + u * NW * 1024);
 #pragma unroll
     for (int u = 0; u < CB; ++u)
-      dma(B1 ? b + u * (BK ? 16 : NW * 8) * g.ldb : b, vb[B1 ? 0 : u], dst + BM * kStepBytes + u * NW * 1024);
+      dma_b(B1 ? b + u * (BK ? 16 : NW * 8) * g.ldb : b, vb[B1 ? 0 : u], dst + BM * kStepBytes + u * NW * 1024);
   };
   // The last step of rows that are no multiple of 128 bytes: zeros behind their end.  Of a k-major A whose
   // rows end within the step: the last row again.
@@ -228,11 +232,11 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
 #pragma unroll
       for (int u = 0; u < CA; ++u) {
         const int past = max((u * NW + wave) * (64 / LA) + lane / LA - last, 0);
-        dma(a + u * 16 * g.lda - (size_t)past * g.lda, va[0], dst + u * NW * 1024);
+        dma_a(a + u * 16 * g.lda - (size_t)past * g.lda, va[0], dst + u * NW * 1024);
       }
 #pragma unroll
       for (int u = 0; u < CB; ++u)
-        dma(B1 ? b + u * (BK ? 16 : NW * 8) * g.ldb : b, vb[B1 ? 0 : u], dst + BM * kStepBytes + u * NW * 1024);
+        dma_b(B1 ? b + u * (BK ? 16 : NW * 8) * g.ldb : b, vb[B1 ? 0 : u], dst + BM * kStepBytes + u * NW * 1024);
     } else {
       const v4u32 zero = {};
       dst += lane * 16;
@@ -483,7 +487,7 @@ __global__ __launch_bounds__(kCombineThreads) void xent_combine_kernel(const flo
   M = wave_max(M);
   double S = 0.0;
   for (int t = lane; t < H; t += SPEC_WAVE)
-    S += sm[wave][t] > -INFINITY ? ss[wave][t] * exp((double)sm[wave][t] - (double)M) : ss[wave][t];
+    S += sm[wave][t] > -INFINITY ? ss[wave][t] * (double)__builtin_amdgcn_exp2f((sm[wave][t] - M) * kLog2eF) : ss[wave][t];
   S = wave_sum(S);
   if (lane == 0) {
     const bool fin = M < INFINITY && M > -INFINITY && S > 0.0 && S < INFINITY;   // NaN sums fail too

@@ -201,9 +201,10 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
     for (int u = 0; u < CB; ++u) vb[u] = (uint32_t)min((u * NW + wave) * 8 + lr, g.rowsB - 1 - j0) * (uint32_t)g.ldb + lc;
   }
 
-  constexpr int kOnce = BN == 64 ? 2 : 0;   // A of a thin tile is read once: nontemporal
+  // a thin tile's rows of A are in no other tile: nontemporal (64 rows, V = 129280, d = 4096: 178 -> 163 us)
+  constexpr bool ONCE = BN == 64 && ST == 3;
   auto dma_a = [&](const char* src, uint32_t off, SPEC_LDS char* dst) {
-    __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(src + off), (SPEC_LDS void*)dst, 16, 0, kOnce);
+    __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(src + off), (SPEC_LDS void*)dst, 16, 0, ONCE ? 2 : 0);
   };
   auto dma_b = [&](const char* src, uint32_t off, SPEC_LDS char* dst) {
     __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(src + off), (SPEC_LDS void*)dst, 16, 0, 0);
@@ -653,20 +654,23 @@ inline int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 inline long long round_to(long long a, long long b) { return (a + b - 1) / b * b; }
 
 // Tile shapes of the product: 256 x 256 (8 waves, one workgroup per CU), 128 x 128 (4 waves, two per CU),
-// 128 x 64 (4 waves, two per CU; rowsB of at most 64).
-enum { kBig = 0, kMid = 1, kThin = 2 };
+// 128 x 64 (4 waves, two per CU; rowsB of at most 64), and 128 x 64 with six steps in flight (one per CU;
+// kStats and kGradZ), where there are few tiles and a step waits for its loads (against 128 x 128,
+// loss and gradients: 348 x 717, d = 3064 32 -> 24 and 85 -> 63 us; 1000 x 1000, d = 2048 28 -> 18 and
+// 71 -> 60; two rounds of such tiles lose: 1500 x 2000, d = 1024 19 -> 21).
+enum { kBig = 0, kMid = 1, kThin = 2, kDeep = 3 };
 
 inline int tile_m(int t) { return t == kBig ? 256 : 128; }
 inline int tile_n(int t) { return t == kBig ? 256 : t == kMid ? 128 : 64; }
 inline int strip_rows(int t) { return t == kBig ? 128 : 64; }   // of kStats
-inline int tile_slots(int t) { return t == kBig ? 256 : 512; }  // workgroups the chip holds at once
+inline int tile_slots(int t) { return t == kBig || t == kDeep ? 256 : 512; }  // workgroups the chip holds at once
 
 // Microseconds of one step of 128 bytes of k on a chip full of tiles, and on one with a tile per CU.
 // Measured on N = 4096, V = 151936, d = 4352 (bf16): 4.08 ms in 256 x 256 tiles, 5.24 in 128 x 128, 6.83
 // in 128 x 64.  fp32 is bound by the matrix units (a sixteenth of the bf16 rate): tiles cost their area.
 inline double step_us(int t, bool full, int es) {
   if (es == 4) return t == kBig ? 7.2 : t == kMid ? (full ? 3.7 : 1.9) : (full ? 1.9 : 1.0);
-  return t == kBig ? 1.6 : t == kMid ? (full ? 1.04 : 0.62) : (full ? 0.68 : 0.4);
+  return t == kBig ? 1.6 : t == kDeep ? 0.45 : t == kMid ? (full ? 1.04 : 0.62) : (full ? 0.68 : 0.4);
 }
 inline double tiles_us(long long tiles, int t, int steps, int es) {
   const long long slots = tile_slots(t), rounds = tiles / slots, rest = tiles % slots;
@@ -682,14 +686,18 @@ struct Shape {
   int tail;
 };
 
-Shape pick_shape(long long rowsA, long long rowsB, int kbytes, int es) {
+Shape pick_shape(long long rowsA, long long rowsB, int kbytes, int es, bool store = false) {
   const int steps = ceil_div(kbytes, kStepBytes);
   auto cost = [&](long long a, long long b, int t) {
     return a && b ? tiles_us((long long)ceil_div(a, tile_m(t)) * ceil_div(b, tile_n(t)), t, steps, es) : 0.0;
   };
-  Shape best{rowsA >= rowsB, 0, rowsB <= 64 ? kThin : kMid};
+  Shape best{rowsA >= rowsB, 0, rowsB <= 64 && !store ? kThin : kMid};   // dW has no narrow tiles
   double us = cost(rowsA, rowsB, best.tail);
   if (rowsB <= 64) return best;
+  if (!store && cost(rowsA, rowsB, kDeep) < us) {
+    best.tail = kDeep;
+    us = cost(rowsA, rowsB, kDeep);
+  }
   if (cost(rowsA, rowsB, kBig) <= us) {
     best.tail = kBig;
     us = cost(rowsA, rowsB, kBig);
@@ -717,20 +725,24 @@ void launch_tiles(GemmArgs& g, int tile, int whole, int parts, hipStream_t s) {
   g.whole = whole < tiles ? whole : tiles;
   g.parts = parts;
   const dim3 grid((unsigned)(g.whole + (tiles - g.whole) * parts));
-  if (tile == kBig)
+  if (tile == kBig) {
     hipLaunchKernelGGL((xent_gemm_kernel<ES, 256, 256, 2, 4, 2, KIND>), grid, dim3(512), 0, s, g);
-  else if (tile == kMid)
+  } else if (tile == kMid) {
     hipLaunchKernelGGL((xent_gemm_kernel<ES, 128, 128, 2, 2, 2, KIND>), grid, dim3(256), 0, s, g);
-  else if constexpr (KIND != kStore)
-    hipLaunchKernelGGL((xent_gemm_kernel<ES, 128, 64, 2, 2, 3, KIND>), grid, dim3(256), 0, s, g);
+  } else if constexpr (KIND != kStore) {
+    if (tile == kThin) {
+      hipLaunchKernelGGL((xent_gemm_kernel<ES, 128, 64, 2, 2, 3, KIND>), grid, dim3(256), 0, s, g);
+    } else if constexpr (KIND != kAcc) {
+      hipLaunchKernelGGL((xent_gemm_kernel<ES, 128, 64, 2, 2, 6, KIND>), grid, dim3(256), 0, s, g);
+    }
+  }
 }
 
 // A product in the shapes of pick_shape: kStats and kGradZ share out A's rows (the vocabulary), kStore
 // the longer side of either.
 template <int ES, int KIND>
 void launch_gemm(const GemmArgs& g, hipStream_t s) {
-  Shape sh = pick_shape(g.rowsA, g.rowsB, g.kbytes, ES);
-  if (KIND == kStore && sh.tail == kThin) sh.tail = kMid;   // dW has no thin form
+  const Shape sh = pick_shape(g.rowsA, g.rowsB, g.kbytes, ES, KIND == kStore);
   const bool split = sh.head > 0 && (sh.along_a || KIND == kStore);
   GemmArgs h = g;
   if (split) {
@@ -806,7 +818,10 @@ BackPlan back_plan(int N, int V, int d, int dtype) {
   const long long rows = round_to(N, 256);                           // whole tiles of rows
   const long long widest = p.es == 4 && d > rows ? d : rows;         // fp32: W^T of the piece, too
   long long vmax = kPieceBytes / (widest * p.es) / 256 * 256;
-  if (vmax < 256) vmax = 256;
+  // fewer rows than a tile per CU needs are no piece (fp32, 64 x 32768, d = 4096: four pieces of 140 us for
+  // kGradZ, 154 us in one)
+  const long long least = round_to(256ll * 128 * 64 / round_to(N, 64), 256);
+  if (vmax < least) vmax = least;
   p.pieces = ceil_div(V, vmax);
   p.vc = (int)round_to(ceil_div(V, p.pieces), 256);
   p.pieces = ceil_div(V, p.vc);

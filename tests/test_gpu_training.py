@@ -407,7 +407,8 @@ def _check_head(sv, h, w, y, gl):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("N,V,d", [(1, 1, 8), (1, 7, 16), (3, 257, 8), (5, 100, 72), (16, 1000, 256), (63, 129, 264),
                                    (64, 5000, 64), (65, 255, 136), (129, 1025, 128), (300, 3001, 40),
-                                   (257, 513, 1000), (1, 20011, 512), (130, 256, 24)])
+                                   (257, 513, 1000), (1, 20011, 512), (130, 256, 24), (348, 717, 3064),
+                                   (200, 3000, 640)])
 def test_head_xent(sv, N, V, d, dtype):
     print(f"head {N} {V} {d} {dtype}", flush=True)
     _check_head(sv, *_head_inputs(N + V + d, N, V, d, dtype))
@@ -464,7 +465,7 @@ def test_head_xent_one_label_for_many_rows(sv, dtype):
     _check_head(sv, h, w, y, gl)
 
 
-@pytest.mark.parametrize("dtype,V,d", [("bf16", 300001, 16), ("f32", 5001, 8200)])
+@pytest.mark.parametrize("dtype,V,d", [("bf16", 300001, 16), ("f32", 5001, 8200), ("f32", 40001, 1000)])
 def test_head_xent_pieces_for_one_gradient(sv, dtype, V, d):
     """A vocabulary in pieces for few rows, and each gradient alone."""
     print(f"head pieces {V} {d} {dtype}", flush=True)

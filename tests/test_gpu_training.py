@@ -16,7 +16,8 @@ Tolerances (u = 2^-24, half a step of fp32):
     x <= 104 before q is 0 in fp32, 312 u), a and b off by 220 u: 700 u q |g| / T, plus half a step of the
     storage type.
   head logits: products of d terms in fp32: dz = (d + 2) u sum_k |h_k w_k| bounds every order.
-    lse: max dz + (256 + 2 + 3 * 14.2) u (a strip adds at most 128 * 2 terms in fp32) < max dz + 310 u,
+    lse: max dz + (256 + 2 + 6 + 3 * 14.2) u (a strip adds at most 128 * 2 terms in fp32, and its sum is
+    scaled at most 3 times on its way to the row's, the exponents of all adding up to x) < max dz + 310 u,
     + u |lse|.  G: p (2 dz + dlse + 310 u) |g| + half a step of the type times |G| (its rounding for the
     product); the products' sums: |G| |W| (terms + 16) u, and half a step for the result.
 """

@@ -202,7 +202,7 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
   }
 
   // a thin tile's rows of A are in no other tile: nontemporal (64 rows, V = 129280, d = 4096: 178 -> 163 us)
-  constexpr bool ONCE = BN == 64 && ST == 3;
+  constexpr bool ONCE = ES == 2 && BN == 64 && ST == 3;
   auto dma_a = [&](const char* src, uint32_t off, SPEC_LDS char* dst) {
     __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(src + off), (SPEC_LDS void*)dst, 16, 0, ONCE ? 2 : 0);
   };
@@ -653,24 +653,27 @@ __global__ __launch_bounds__(kLabelThreads) void xent_label_rows_kernel(const in
 inline int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 inline long long round_to(long long a, long long b) { return (a + b - 1) / b * b; }
 
-// Tile shapes of the product: 256 x 256 (8 waves, one workgroup per CU), 128 x 128 (4 waves, two per CU),
-// 128 x 64 (4 waves, two per CU; rowsB of at most 64), and 128 x 64 with six steps in flight (one per CU;
-// kStats and kGradZ), where there are few tiles and a step waits for its loads (against 128 x 128,
-// loss and gradients: 348 x 717, d = 3064 32 -> 24 and 85 -> 63 us; 1000 x 1000, d = 2048 28 -> 18 and
-// 71 -> 60; two rounds of such tiles lose: 1500 x 2000, d = 1024 19 -> 21).
-enum { kBig = 0, kMid = 1, kThin = 2, kDeep = 3 };
+// Tile shapes of the product.  bf16: 256 x 256 (8 waves, one workgroup per CU); 128 x 128 and, for rowsB of at
+// most 64, 128 x 64 (4 waves, two per CU); and for kStats and kGradZ, where there are few tiles and a step
+// waits for its loads, 128 x 64 with six steps in flight (one per CU) and 64 x 64 with five (two per CU).
+// Loss and gradients of 348 x 717, d = 3064 by the three last shapes: 32, 24, 19.5 us and 85, 63, 55 us; of
+// 1000 x 1000, d = 2048: 28, 18, 15 and 72, 60, 56; of 246 x 6727, d = 2896 (two of the smallest tiles per
+// CU): 44, 29.7, 32.3.  fp32 is bound by the matrix units (a sixteenth of the bf16 rate), so what counts is
+// that every CU has its share: 128 x 64 (against 128 x 128 and 256 x 256, 200 x 20000, d = 1024: 132 -> 109 us;
+// gradients of 1000 x 1000, d = 2048: 197 -> 169), or 64 x 64 (76 -> 44 us; 169 -> 135).
+enum { kBig = 0, kMid = 1, kThin = 2, kDeep = 3, kSmall = 4 };
 
-inline int tile_m(int t) { return t == kBig ? 256 : 128; }
+inline int tile_m(int t) { return t == kBig ? 256 : t == kSmall ? 64 : 128; }
 inline int tile_n(int t) { return t == kBig ? 256 : t == kMid ? 128 : 64; }
-inline int strip_rows(int t) { return t == kBig ? 128 : 64; }   // of kStats
+inline int strip_rows(int t) { return tile_m(t) / 2; }          // of kStats
 inline int tile_slots(int t) { return t == kBig || t == kDeep ? 256 : 512; }  // workgroups the chip holds at once
 
 // Microseconds of one step of 128 bytes of k on a chip full of tiles, and on one with a tile per CU.
 // Measured on N = 4096, V = 151936, d = 4352 (bf16): 4.08 ms in 256 x 256 tiles, 5.24 in 128 x 128, 6.83
-// in 128 x 64.  fp32 is bound by the matrix units (a sixteenth of the bf16 rate): tiles cost their area.
+// in 128 x 64; the narrow ones on the shapes above.
 inline double step_us(int t, bool full, int es) {
-  if (es == 4) return t == kBig ? 7.2 : t == kMid ? (full ? 3.7 : 1.9) : (full ? 1.9 : 1.0);
-  return t == kBig ? 1.6 : t == kDeep ? 0.45 : t == kMid ? (full ? 1.04 : 0.62) : (full ? 0.68 : 0.4);
+  if (es == 4) return t == kSmall ? (full ? 1.1 : 0.6) : full ? 1.9 : 1.1;
+  return t == kBig ? 1.6 : t == kDeep ? 0.45 : t == kSmall ? (full ? 0.55 : 0.36) : t == kMid ? (full ? 1.04 : 0.62) : (full ? 0.68 : 0.4);
 }
 inline double tiles_us(long long tiles, int t, int steps, int es) {
   const long long slots = tile_slots(t), rounds = tiles / slots, rest = tiles % slots;
@@ -691,13 +694,16 @@ Shape pick_shape(long long rowsA, long long rowsB, int kbytes, int es, bool stor
   auto cost = [&](long long a, long long b, int t) {
     return a && b ? tiles_us((long long)ceil_div(a, tile_m(t)) * ceil_div(b, tile_n(t)), t, steps, es) : 0.0;
   };
+  if (es == 4) return Shape{rowsA >= rowsB, 0, cost(rowsA, rowsB, kSmall) < cost(rowsA, rowsB, kThin) ? kSmall : kThin};
   Shape best{rowsA >= rowsB, 0, rowsB <= 64 && !store ? kThin : kMid};   // dW has no narrow tiles
   double us = cost(rowsA, rowsB, best.tail);
   if (rowsB <= 64) return best;
-  if (!store && cost(rowsA, rowsB, kDeep) < us) {
-    best.tail = kDeep;
-    us = cost(rowsA, rowsB, kDeep);
-  }
+  if (!store)
+    for (int t : {kDeep, kSmall})
+      if (cost(rowsA, rowsB, t) < us) {
+        best.tail = t;
+        us = cost(rowsA, rowsB, t);
+      }
   if (cost(rowsA, rowsB, kBig) <= us) {
     best.tail = kBig;
     us = cost(rowsA, rowsB, kBig);
@@ -725,15 +731,19 @@ void launch_tiles(GemmArgs& g, int tile, int whole, int parts, hipStream_t s) {
   g.whole = whole < tiles ? whole : tiles;
   g.parts = parts;
   const dim3 grid((unsigned)(g.whole + (tiles - g.whole) * parts));
-  if (tile == kBig) {
-    hipLaunchKernelGGL((xent_gemm_kernel<ES, 256, 256, 2, 4, 2, KIND>), grid, dim3(512), 0, s, g);
-  } else if (tile == kMid) {
-    hipLaunchKernelGGL((xent_gemm_kernel<ES, 128, 128, 2, 2, 2, KIND>), grid, dim3(256), 0, s, g);
-  } else if constexpr (KIND != kStore) {
-    if (tile == kThin) {
-      hipLaunchKernelGGL((xent_gemm_kernel<ES, 128, 64, 2, 2, 3, KIND>), grid, dim3(256), 0, s, g);
-    } else if constexpr (KIND != kAcc) {
-      hipLaunchKernelGGL((xent_gemm_kernel<ES, 128, 64, 2, 2, 6, KIND>), grid, dim3(256), 0, s, g);
+  const auto go = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, s, g); };
+  if constexpr (ES == 4) {
+    if (tile == kSmall) go(xent_gemm_kernel<4, 64, 64, 2, 2, 4, KIND>, 256);
+    else go(xent_gemm_kernel<4, 128, 64, 2, 2, 3, KIND>, 256);
+  } else {
+    if (tile == kBig) go(xent_gemm_kernel<2, 256, 256, 2, 4, 2, KIND>, 512);
+    else if (tile == kMid) go(xent_gemm_kernel<2, 128, 128, 2, 2, 2, KIND>, 256);
+    if constexpr (KIND != kStore) {
+      if (tile == kThin) go(xent_gemm_kernel<2, 128, 64, 2, 2, 3, KIND>, 256);
+    }
+    if constexpr (KIND == kStats || KIND == kGradZ) {
+      if (tile == kDeep) go(xent_gemm_kernel<2, 128, 64, 2, 2, 6, KIND>, 256);
+      else if (tile == kSmall) go(xent_gemm_kernel<2, 64, 64, 2, 2, 5, KIND>, 256);
     }
   }
 }
@@ -830,7 +840,8 @@ BackPlan back_plan(int N, int V, int d, int dtype) {
   // 256 x 256 on 256 CUs: one round and 16 tiles by 16 workgroups, 1.06 rounds in place of 2)
   const int steps = p.vc / p.step;
   double best = 1e300;
-  for (int t = N <= 64 ? kThin : kBig; t <= (N <= 64 ? kThin : kMid); ++t) {
+  const int wide = p.es == 4 || N <= 64 ? kThin : kBig, narrow = p.es == 4 ? kSmall : N <= 64 ? kThin : kMid;
+  for (int t : {wide, narrow}) {
     const long long tiles = (long long)ceil_div(d, tile_m(t)) * ceil_div(N, tile_n(t));
     const long long whole = tiles / tile_slots(t) * tile_slots(t), rest = tiles - whole;
     for (int parts = 1; parts <= kMaxParts && (parts == 1 || steps / parts >= kPartSteps); ++parts) {

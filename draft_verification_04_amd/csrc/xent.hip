@@ -69,7 +69,7 @@ struct GemmArgs {
   char* gt;          // [rowsA, ldgt bytes]
   size_t ldgn, ldgt;
   int vpad, npad;    // columns of gn and gt that are written (zeros past the valid ones)
-  // bf16: the labels' entries of G (see xent_label_rows_kernel)
+  // bf16: the labels' entries of G (see finish_label)
   float* glab;       // [N] what the rounding of row n's left out
   int32_t* first;    // [V] the first row with the token as its label (kNoRow: none)
   float* side;       // [N, side_ld] dW of a label's token, unrounded, at its first row
@@ -527,10 +527,13 @@ __global__ __launch_bounds__(256) void xent_transpose_kernel(const char* in, siz
   }
 }
 
-// bf16: H with zeros in the rows left out (and up to npad rows): 0 * inf would reach dW otherwise.
-__global__ __launch_bounds__(256) void xent_live_copy_kernel(const v4u32* in, int N, int d8, v4u32* out, long long n8,
-                                                             const int32_t* labels, const float* lse, int V) {
+// bf16, before dW: H with zeros in the rows left out (and up to npad rows; 0 * inf would reach dW otherwise),
+// and no first rows yet.
+__global__ __launch_bounds__(256) void xent_prepare_kernel(const v4u32* in, int N, int d8, v4u32* out, long long n8,
+                                                           const int32_t* labels, const float* lse, int V,
+                                                           int32_t* first) {
   const long long t = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (t < V) first[t] = kNoRow;
   if (t >= n8) return;
   const int r = (int)(t / d8);
   v4u32 v = {};
@@ -541,9 +544,8 @@ __global__ __launch_bounds__(256) void xent_live_copy_kernel(const v4u32* in, in
 // grad_hidden = the sums, the parts of a shared tile added in order, rounded once; zeros for the rows
 // left out.
 template <int ES>
-__global__ __launch_bounds__(256) void xent_finish_kernel(GemmArgs g, int bm, int bn, char* out, const char* weight) {
+__device__ __forceinline__ void finish_hidden(const GemmArgs& g, int bm, int bn, char* out, const char* weight, size_t t) {
   const int d = g.rowsA, N = g.rowsB, d4 = d / 4;
-  const size_t t = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (t >= (size_t)N * d4) return;
   const int n = (int)(t / d4), i = (int)(t - (size_t)n * d4) * 4;
   f32x4 s = {};
@@ -580,22 +582,20 @@ __global__ __launch_bounds__(256) void xent_finish_kernel(GemmArgs g, int bm, in
 // round once.
 constexpr int kLabelThreads = 256;
 
-__global__ __launch_bounds__(kLabelThreads) void xent_fill_kernel(int32_t* p, int n) {
-  const int t = (int)blockIdx.x * kLabelThreads + (int)threadIdx.x;
-  if (t < n) p[t] = kNoRow;
-}
-
-__global__ __launch_bounds__(kLabelThreads) void xent_label_rows_kernel(const int32_t* labels, const float* lse, int N,
-                                                                        int V, int d, const float* glab,
-                                                                        const int32_t* first, const float* side,
-                                                                        const char* hidden, char* out) {
+__device__ __forceinline__ void finish_label(const GemmArgs& g, int n, int part, const char* hidden, char* out) {
+  const int32_t* labels = g.labels;
+  const float* lse = g.lse;
+  const float* glab = g.glab;
+  const int32_t* first = g.first;
+  const float* side = g.side;
+  const int N = g.rowsB, V = g.V, d = g.rowsA;
   constexpr int NW = kLabelThreads / SPEC_WAVE, CHUNK = 4 * kLabelThreads;
   __shared__ int32_t rows[CHUNK];
   __shared__ int cnt[NW];
-  const int n = (int)blockIdx.x, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int label = labels[n];
   if (!live_row(label, lse[n], V) || first[label] != n) return;
-  const int d4 = d / 4, c = (int)blockIdx.y * kLabelThreads + tid, cc = min(c, d4 - 1);
+  const int d4 = d / 4, c = part * kLabelThreads + tid, cc = min(c, d4 - 1);
   const bf16x4* h4 = reinterpret_cast<const bf16x4*>(hidden) + cc;
   f32x4 s = reinterpret_cast<const f32x4*>(side + (size_t)n * d)[cc];
   for (int m0 = n; m0 < N; m0 += CHUNK) {
@@ -646,6 +646,18 @@ __global__ __launch_bounds__(kLabelThreads) void xent_label_rows_kernel(const in
 #pragma unroll
   for (int q = 0; q < 4; ++q) o[q] = (__bf16)s[q];
   if (c < d4) reinterpret_cast<bf16x4*>(out + (size_t)label * d * 2)[c] = o;
+}
+
+// Both gradients' last step in one launch: `parts` workgroups per row for the labels' tokens of dW, then dH's.
+template <int ES>
+__global__ __launch_bounds__(kLabelThreads) void xent_finish_kernel(GemmArgs g, int parts, int bm, int bn,
+                                                                    const char* hidden, const char* weight,
+                                                                    char* grad_hidden, char* grad_weight) {
+  const unsigned nl = (unsigned)g.rowsB * (unsigned)parts;
+  if (ES == 2 && blockIdx.x < nl)
+    finish_label(g, (int)(blockIdx.x / (unsigned)parts), (int)(blockIdx.x % (unsigned)parts), hidden, grad_weight);
+  else
+    finish_hidden<ES>(g, bm, bn, grad_hidden, weight, (size_t)(blockIdx.x - nl) * kLabelThreads + threadIdx.x);
 }
 
 // ---- host -------------------------------------------------------------------
@@ -797,7 +809,7 @@ int stat_strips(long long V, long long N, int kbytes, int es) {
 // parts of kAcc add at most 16 times the tiles of two rounds).
 bool head_fits(long long N, long long V, long long d) {
   const long long most = 0xffffffffll - 256ll * 1024 * 32;
-  return (long long)ceil_div(V, 128) * ceil_div(N, 64) * 256 <= most && N * round_to(d, 1024) / 4 + 256 <= most &&
+  return (long long)ceil_div(V, 128) * ceil_div(N, 64) * 256 <= most && N * round_to(d, 1024) / 2 + 512 <= most &&
          (long long)ceil_div(V, 128) * ceil_div(d, 64) * 256 <= most;
 }
 
@@ -914,15 +926,13 @@ int32_t run_backward(int N, int V, int d, int dtype, const void* hidden, const v
   h.glab = reinterpret_cast<float*>(lab);
   int32_t* first = ES == 2 && grad_weight ? reinterpret_cast<int32_t*>(lab + p.glab) : nullptr;
   float* side = reinterpret_cast<float*>(lab + p.glab + p.first);
-  if (first)
-    hipLaunchKernelGGL(xent_fill_kernel, dim3(ceil_div(V, kLabelThreads)), dim3(kLabelThreads), 0, s, first, V);
   const size_t ld = (size_t)d * ES;
   if (grad_weight) {
     if constexpr (ES == 2) {
       const long long n8 = p.npad * (d / 8);
-      hipLaunchKernelGGL(xent_live_copy_kernel, dim3(ceil_div(n8, 256)), dim3(256), 0, s,
+      hipLaunchKernelGGL(xent_prepare_kernel, dim3(ceil_div(n8 > V ? n8 : V, 256)), dim3(256), 0, s,
                          reinterpret_cast<const v4u32*>(hidden), N, d / 8, reinterpret_cast<v4u32*>(ht), n8, labels, lse,
-                         V);
+                         V, first);
     } else {
       hipLaunchKernelGGL(xent_transpose_kernel, dim3(ceil_div(p.npad, 64), ceil_div(d, 64)), dim3(256), 0, s,
                          reinterpret_cast<const char*>(hidden), ld, N, d, ht, (size_t)p.npad * ES, (int)p.npad, labels,
@@ -969,13 +979,15 @@ int32_t run_backward(int N, int V, int d, int dtype, const void* hidden, const v
       launch_gemm<ES, kStore>(w, s);
     }
   }
-  if (first)
-    hipLaunchKernelGGL(xent_label_rows_kernel, dim3(N, ceil_div(d, 4 * kLabelThreads)), dim3(kLabelThreads), 0, s, labels, lse, N, V, d, h.glab, first,
-                       side, reinterpret_cast<const char*>(hidden), reinterpret_cast<char*>(grad_weight));
-  if (grad_hidden)
-    hipLaunchKernelGGL(xent_finish_kernel<ES>, dim3(ceil_div((long long)N * d / 4, 256)), dim3(256), 0, s, h,
-                       tile_m(p.tile), tile_n(p.tile), reinterpret_cast<char*>(grad_hidden),
-                       reinterpret_cast<const char*>(weight));
+  h.first = first;
+  h.side = side;
+  const int parts = first ? ceil_div(d, 4 * kLabelThreads) : 0;
+  const long long last = (long long)N * parts + (grad_hidden ? ceil_div((long long)N * d / 4, kLabelThreads) : 0);
+  if (last)
+    hipLaunchKernelGGL(xent_finish_kernel<ES>, dim3((unsigned)last), dim3(kLabelThreads), 0, s, h, parts,
+                       tile_m(p.tile), tile_n(p.tile), reinterpret_cast<const char*>(hidden),
+                       reinterpret_cast<const char*>(weight), reinterpret_cast<char*>(grad_hidden),
+                       reinterpret_cast<char*>(grad_weight));
   return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
 }
 

@@ -805,8 +805,8 @@ int stat_strips(long long V, long long N, int kbytes, int es) {
   return (int)(head / strip_rows(kBig)) + ceil_div(V - head, tile_m(tail)) * (tile_m(tail) / strip_rows(tail));
 }
 
-// Every launch's work-items fit the 32-bit grid size of the dispatch packet, whatever the tiles (the
-// parts of kAcc add at most 16 times the tiles of two rounds).
+// Every launch's work-items fit the 32-bit grid size of the dispatch packet, whatever the tiles (64 x 64
+// ones are taken up to some 7000 of them; the parts of kAcc add at most 16 times the tiles of two rounds).
 bool head_fits(long long N, long long V, long long d) {
   const long long most = 0xffffffffll - 256ll * 1024 * 32;
   return (long long)ceil_div(V, 128) * ceil_div(N, 64) * 256 <= most && N * round_to(d, 1024) / 2 + 512 <= most &&

@@ -16,7 +16,7 @@
 // The pieces bound the memory: G of one piece at a time instead of N V logits.
 //
 // Bound by the matrix units.  MI355X, N = 4096, V = 151936, d = 4352, bf16 (a product is 5.42 TFLOP): kStats
-// 3.98 ms (1360 TFLOP/s), kGradZ in 10 pieces 4.67 ms (1160), kAcc 4.19 ms (1290), kStore 4.28 ms (1270).
+// 3.98 ms (1360 TFLOP/s), kGradZ in 10 pieces 4.51 ms (1200), kAcc 4.19 ms (1290), kStore 4.28 ms (1270).
 //
 // Operands in LDS: a step of 128 bytes of k (64 bf16 or 32 fp32) per row, rows 128 bytes apart, the
 // 16-byte chunk c of row r stored at c ^ (r & 7), so that the 16 rows an MFMA operand read touches
@@ -377,34 +377,36 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
       }
     }
   } else if constexpr (KIND == kGradZ) {
+    const bool edge = i0 + BM > g.rowsA;
+    int labels[NT];
+    float lses[NT], scales[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {   // ahead of the stores, which would hold them up
+      const int jc = min(jw + n * 16, g.rowsB - 1);
+      labels[n] = g.labels[jc];
+      lses[n] = g.lse[jc];
+      scales[n] = g.grad_loss[jc];
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int j = jw + n * 16;
-      const int jc = min(j, g.rowsB - 1);
-      const int label = g.labels[jc];
-      const float lse = g.lse[jc];
+      const int label = labels[n];
+      const float lse = lses[n], s = scales[n];
       const bool live = j < g.rowsB && live_row(label, lse, g.V);
-      const float s = g.grad_loss[jc];
-      const int lab = label - g.v0;
+      auto prob = [&](float z) { return __builtin_amdgcn_exp2f((z - lse) * kLog2eF); };
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const int i = iw + m * 16;
         f32x4 o;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const float p = __builtin_amdgcn_exp2f((c[m][n][x] - lse) * kLog2eF);
-          o[x] = (live && i + x < g.rowsA) ? (p - (i + x == lab ? 1.f : 0.f)) * s : 0.f;
+          o[x] = live ? prob(c[m][n][x]) * s : 0.f;
+          if (edge && i + x >= g.rowsA) o[x] = 0.f;
         }
         if constexpr (ES == 2) {
           bf16x4 h;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            h[x] = (__bf16)o[x];
-            if (live && i + x == lab && i + x < g.rowsA) {
-              g.glab[j] = o[x] - (float)h[x];
-              if (g.first) atomicMin(&g.first[label], j);
-            }
-          }
+          for (int x = 0; x < 4; ++x) h[x] = (__bf16)o[x];
           if (j < g.npad && i < g.vpad) *reinterpret_cast<bf16x4*>(g.gn + (size_t)j * g.ldgn + (size_t)i * 2) = h;
         } else {
           if (j < g.rowsB && i < g.vpad) *reinterpret_cast<f32x4*>(g.gn + (size_t)j * g.ldgn + (size_t)i * 4) = o;
@@ -414,14 +416,40 @@ __global__ __launch_bounds__(WM * WN * 64) void xent_gemm_kernel(GemmArgs g) {
               if (i + x < g.rowsA) *reinterpret_cast<float*>(g.gt + (size_t)(i + x) * g.ldgt + (size_t)j * 4) = o[x];
         }
       }
+      // the label's entry over it, by the lane that holds its logit (out of the loop above: kGradZ of the case
+      // above 469 -> 451 us a piece)
+      const int lab = label - g.v0, rel = lab - iw;
+      if (live && rel >= 0 && rel < MT * 16 && (rel & 15) < 4 && lab < g.rowsA) {
+        float z = 0.f;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (rel == m * 16 + x) z = c[m][n][x];
+        const float o = (prob(z) - 1.f) * s;
+        if constexpr (ES == 2) {
+          const __bf16 h = (__bf16)o;
+          *reinterpret_cast<__bf16*>(g.gn + (size_t)j * g.ldgn + (size_t)lab * 2) = h;
+          g.glab[j] = o - (float)h;
+          if (g.first) atomicMin(&g.first[label], j);
+        } else {
+          *reinterpret_cast<float*>(g.gn + (size_t)j * g.ldgn + (size_t)lab * 4) = o;
+          *reinterpret_cast<float*>(g.gt + (size_t)lab * g.ldgt + (size_t)j * 4) = o;
+        }
+      }
     }
   } else {
+    int firsts[NT];
+    if constexpr (KIND == kStore && ES == 2) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) firsts[n] = g.first[g.v0 + min(jw + n * 16, g.rowsB - 1)];
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int j = jw + n * 16;
       if (j >= g.rowsB) continue;
       int first = kNoRow;
-      if constexpr (KIND == kStore && ES == 2) first = g.first[g.v0 + j];
+      if constexpr (KIND == kStore && ES == 2) first = firsts[n];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const int i = iw + m * 16;

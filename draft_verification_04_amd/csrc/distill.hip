@@ -428,12 +428,16 @@ __global__ __launch_bounds__(kSegThreads) void distill_grad_kernel(DistillArgs a
   float c_hi, c_lo;
   split_scale(T, c_hi, c_lo);
   const float m = (float)md, l2 = (float)sv[1];
-  const float f = (float)(s * sv[2]);
+  // the factor past fp32's range (grad_loss / T of 2^127 and more) is multiplied in two steps: as inf it would
+  // make the tokens without mass NaN
+  const double fd = s * sv[2];
+  const int up = fabs(fd) < INFINITY ? max(ilogb(fd) - 126, 0) : 0;
+  const float f = (float)ldexp(fd, -up);
   // every load of the segment is done in every wave before the first store (grad may be draft)
   memory_barrier();
   auto grad_of = [&](float z) {
     const float dz = z - m;   // q / r_s of a token outside the list
-    return f * __builtin_amdgcn_exp2f(fmaf(dz, c_lo, fmaf(dz, c_hi, -l2)));
+    return ldexpf(f * __builtin_amdgcn_exp2f(fmaf(dz, c_lo, fmaf(dz, c_hi, -l2))), up);
   };
 #pragma unroll
   for (int j = 0; j < kSegVecs; ++j) {

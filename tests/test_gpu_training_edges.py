@@ -1,0 +1,59 @@
+"""Edges of the drafter's training operators that ordinary rows do not reach (u = 2^-24, half a step of
+fp32; a term, a sum and a difference each bounded where it is tested)."""
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+import oracle
+
+DEV = "cuda:0"
+U = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def sv():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import draft_verification_04_amd as m
+    m.load_library()
+    return m
+
+
+def _np(t):
+    t = t.detach().cpu()
+    return (t.double() if t.is_floating_point() else t).numpy()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,g", [(1e-38, 10.0), (2.0 ** -100, 2.0 ** 35), (1.0, 2.0 ** 127)])
+def test_distill_gradient_with_factors_past_fp32(sv, dtype, T, g):
+    """grad_loss / T past fp32's largest value: tokens without mass still get 0, values in range stay right and
+    only those past the type's range are infinite.  Outside the list 2^10 equal logits share the draft's mass."""
+    V, K = 5000, 3
+    z = torch.full((1, 2, V), -1.0, device=DEV)
+    z[0, :, 1000:1000 + 2 ** 10] = 1.0
+    z[0, 1, 7] = 1.0                         # row 1: a listed token among them
+    d = z.to(DT[dtype])
+    ids = torch.tensor([[[7, 8, 9]] * 2], dtype=torch.int32, device=DEV)
+    vals = torch.tensor([[[0.5, 0.25, -1.0]] * 2], device=DEV)
+    temp = torch.tensor([T], device=DEV)
+    w = torch.tensor([[g, -g]], device=DEV)
+    ref = oracle.distill_loss(d, ids, vals, None, "kl", None, temp, w)
+    f = sv.distill_loss(d, ids, vals, None, sv.SPEC_DISTILL_KL, None, temp)
+    grad = sv.distill_loss_backward(d, ids, vals, f["saved"], w, sv.SPEC_DISTILL_KL, temp)
+    torch.cuda.synchronize()
+    got, want = _np(grad), ref["grad"]
+    big = np.abs(want) > float(torch.finfo(DT[dtype]).max)
+    assert (np.abs(want[0, 0, 1000:2024]) > 1e30).all() and not big[0, 0, 1000:2024].any()
+    assert np.isinf(got[big]).all() and (np.sign(got[big]) == np.sign(want[big])).all()
+    # q: 700 u (its sum and exponent), one rounding to the type; q below 2^-126 counts as 0
+    eps = torch.finfo(DT[dtype]).eps
+    scale = g / float(temp[0])
+    tol = 700 * U * ref["q"] * scale + eps / 2 * (1 + 2 ** -10) * np.abs(want) + 2.0 ** -126 * scale + 1e-37
+    assert (np.abs(got - want)[~big] <= tol[~big]).all()
+    if T < 1e-20:
+        assert (got[0, :, :1000][:, 10:] == 0).all()

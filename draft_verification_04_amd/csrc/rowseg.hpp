@@ -186,25 +186,36 @@ __device__ __forceinline__ void split_scale(float T, float& c_hi, float& c_lo) {
   c_lo = fmaxf((float)(c - (double)c_hi), 1.4e-45f);
 }
 
-// Sum of exp2(z c_f - M) over a vector, c_f = log2(e) / T rounded to fp32: one multiply-add per term.  M is
-// an integer, the same for the whole segment: the ceiling of the largest exponent of its first chunk
-// (pick_reference, which keeps that largest logit m).  The rounding of c_f shifts every exponent by
-// z (c - c_f) = m (c - c_f) + (z - m)(c - c_f): the first part is common to the segment and goes into its
-// reference in fp64, the second is at most 2^-25 |z - m| c, and e^-|z - m|/T weighs it.  A later value may
-// pass M by 2^100 before the sum leaves fp32's range (one of 70 T nats more than the largest of 32768);
-// such a segment, one whose first chunk has no value, one with NaN or +inf and one with exponents past
-// 2^22 (an fp32 reference no longer tells their neighbours apart) is summed again by exp_term in
-// segment_sum.
+// Added in pairs: log2 N roundings of a term.
 template <int N>
-__device__ __forceinline__ float exp_sum(const float (&z)[N], float c_f, float M) {
-  float e[N];
-#pragma unroll
-  for (int j = 0; j < N; ++j) e[j] = __builtin_amdgcn_exp2f(fmaf(z[j], c_f, -M));
+__device__ __forceinline__ float pair_sum(float (&e)[N]) {
 #pragma unroll
   for (int w = 1; w < N; w <<= 1)
 #pragma unroll
     for (int j = 0; j + w < N; j += 2 * w) e[j] += e[j + w];
   return e[0];
+}
+
+// Sum of exp2(z c_f - M) over a vector, c_f = log2(e) / T rounded to fp32: one multiply-add per term.  M is
+// an integer, the same for the whole segment: the ceiling of the largest exponent of its first chunk
+// (pick_reference, which keeps that largest logit m).  With u = 2^-24, the sum is off by (relative)
+//  - the rounding of c_f, which shifts every exponent by z (c - c_f): the shift of the logit whose exponent is the
+//    sum's own, M + log2(sum), is common to the segment and goes into its reference in fp64 (segment_sum); what is
+//    left is at most u |x| per term, x its distance from there in nats, and over a softmax of V terms
+//    E|x| <= ln V + 1.4;
+//  - the rounding of each exponent, half a step: below 2^6 in size 2^-19, 22 u of its term, and terms further
+//    below have no weight beside the largest.  A later value may stand 2^63 above M before a thread's sum says
+//    so (one of 43 T nats more than the largest of 32768): past that the exponents' rounding would grow to 2^-18,
+//    44 u, and the segment is summed again by exp_term in segment_sum.  So is one whose first chunk has no
+//    value, one with NaN or +inf and one with exponents past 2^22 (an fp32 reference no longer tells their
+//    neighbours apart);
+//  - an ulp of exp2 (2 u) and 44 roundings of a thread's sum: together below 110 u for every V.
+template <int N>
+__device__ __forceinline__ float exp_sum(const float (&z)[N], float c_f, float M) {
+  float e[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) e[j] = __builtin_amdgcn_exp2f(fmaf(z[j], c_f, -M));
+  return pair_sum(e);
 }
 
 // exp2((z - m) c) against the segment's largest value m: the difference first, so that it, not the
@@ -230,7 +241,7 @@ struct SegSumShared {
 struct Reference {
   double c;      // log2(e) / T
   float c_f, M;
-  double ref;    // M and the shared part of c_f's rounding: the sum is S * 2^ref
+  double ref;    // M and the shift of m by c_f's rounding: the sum is S * 2^ref
   bool ok;       // false: there is no reference
 };
 
@@ -261,7 +272,7 @@ __device__ __forceinline__ SegSum segment_sum(SegSumShared& sh, float S1, const 
   using Seg = RowSeg<BF16>;
   const int wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
   const double ws = wave_sum((double)S1);
-  const int wo = __ballot(!(S1 <= 0x1p100f)) != 0;
+  const int wo = __ballot(!(S1 <= 0x1p63f)) != 0;
   if (lane == 0) {
     sh.s[wave] = ws;
     sh.odd[wave] = wo;
@@ -275,7 +286,11 @@ __device__ __forceinline__ SegSum segment_sum(SegSumShared& sh, float S1, const 
     odd |= sh.odd[w];
   }
   bad = 0;
-  if (!odd) return t;
+  if (!odd) {
+    // from m's shift to that of the sum's own exponent, log2(sum) / c further (1 <= 2 sum)
+    t.ref += (double)ilogb(t.sum) * (1.0 - (double)rf.c_f / rf.c);
+    return t;
+  }
   t.sum = 0.0;
   float c_hi, c_lo;
   split_scale(T, c_hi, c_lo);
@@ -299,7 +314,8 @@ __device__ __forceinline__ SegSum segment_sum(SegSumShared& sh, float S1, const 
     float z[Seg::EPV];
     Seg::unpack(again(v), z);
 #pragma unroll
-    for (int e = 0; e < Seg::EPV; ++e) S += exp_term(z[e], mr, c_hi, c_lo);
+    for (int e = 0; e < Seg::EPV; ++e) z[e] = exp_term(z[e], mr, c_hi, c_lo);
+    S += pair_sum(z);
   }
   const int wb = __ballot(!(S < INFINITY) || !(m < INFINITY)) != 0;
   const double s2 = wave_sum((double)S);

@@ -57,3 +57,51 @@ def test_distill_gradient_with_factors_past_fp32(sv, dtype, T, g):
     assert (np.abs(got - want)[~big] <= tol[~big]).all()
     if T < 1e-20:
         assert (got[0, :, :1000][:, 10:] == 0).all()
+
+
+def _lse_of(sv, z, T):
+    """spec_teacher_topk's normalisers of the rows z [B, V] (one position a request: 512 requests or more are walked
+    whole, a workgroup a row)."""
+    t = torch.stack([z, z], 1).contiguous()
+    o = sv.teacher_topk(t, 1, None, T)
+    torch.cuda.synchronize()
+    assert not o["status"].any()
+    return _np(o["lse"])[:, 0]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_normaliser_of_a_value_far_above_the_first_chunk(sv, dtype):
+    """One token stands 20 to 69 nats above the row's first 64 KB, which the exponents are taken against.  Its
+    own term is nearly all of the sum: an exponent below 64 is rounded by 2^-19 at most (22 u of its term), the
+    scale's rounding leaves 2 binary orders of itself (1.4 u) and exp2 an ulp (2 u); a larger one is summed against
+    the row's largest value, where this term is exactly 1.  Half a step of the result besides."""
+    rng = np.random.default_rng(17)
+    B, V = 512, 50021
+    T = torch.from_numpy(rng.uniform(0.6, 1.4, B).astype(np.float32))
+    top = torch.from_numpy(rng.uniform(-2, 2, B).astype(np.float32)).to(torch.bfloat16)
+    low = (top.float() - torch.from_numpy(rng.uniform(20, 69, B).astype(np.float32)) * T).to(torch.bfloat16)
+    z = low.to(DEV)[:, None].repeat(1, V)
+    z[:, 50000] = top.to(DEV)
+    got = _lse_of(sv, z.to(DT[dtype]), T.to(DEV))
+    t = _np(T)
+    want = np.logaddexp(_np(top) / t, _np(low) / t + np.log(V - 1))
+    err = np.abs(got - want) / U
+    assert (err <= 26 + np.abs(want)).all(), (err.max(), int(err.argmax()))
+
+
+def test_normaliser_of_rows_summed_again(sv):
+    """Rows whose first 64 KB are masked have no reference and are summed a second time: 256 equal terms per
+    thread and the row's largest.  They are added in pairs, then vector by vector: 3 + 33 roundings, an ulp of
+    exp2 (2 u), 3 u of the exponent, half a step of the result."""
+    rng = np.random.default_rng(18)
+    B, V, first = 512, 163840, 32768
+    T = torch.from_numpy(rng.uniform(0.6, 1.4, B).astype(np.float32))
+    v = torch.from_numpy(rng.uniform(-0.25, 0, B).astype(np.float32)).to(torch.bfloat16)
+    z = v.to(DEV)[:, None].repeat(1, V)
+    z[:, :first] = -float("inf")
+    z[:, V - 1] = 0.0
+    got = _lse_of(sv, z, T.to(DEV))
+    x = _np(v) / _np(T)
+    want = np.log(1.0 + (V - first - 1) * np.exp(x))
+    err = np.abs(got - want) / U
+    assert (err <= 38 + 3 * np.abs(x) + np.abs(want)).all(), (err.max(), int(err.argmax()))

@@ -789,6 +789,13 @@ def _list_size(K):
     return K
 
 
+def _int32(**sizes):
+    """The C ABI's sizes are int32: ctypes would cut a larger one down to its low bits."""
+    for name, n in sizes.items():
+        if not -(1 << 31) <= n < 1 << 31:
+            raise ValueError(f"{name} = {n} does not fit 32 bits")
+
+
 def teacher_topk(target: torch.Tensor, K: int, lengths: Optional[torch.Tensor] = None,
                  temperature: Optional[torch.Tensor] = None, out: Optional[dict] = None,
                  workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
@@ -803,6 +810,7 @@ def teacher_topk(target: torch.Tensor, K: int, lengths: Optional[torch.Tensor] =
         raise ValueError("target must be [B, gamma+1, V]")
     B, G1, V = target.shape
     G, K = G1 - 1, _list_size(K)
+    _int32(B=B, gamma=G, V=V, K=K)
     for name, t in (("lengths", lengths), ("temperature", temperature)):
         _vec(t, name, B)
     _dev(target, "target", (torch.float32, torch.bfloat16), 3)
@@ -841,6 +849,7 @@ def _list_inputs(draft, ids, values, temperature):
     if not isinstance(ids, torch.Tensor) or ids.dim() != 3 or tuple(ids.shape[:2]) != (B, G):
         raise ValueError("ids must be [B, gamma, K]")
     K = ids.shape[2]
+    _int32(B=B, gamma=G, V=V, K=K)
     _shape(values, "values", (B, G, K))
     _vec(temperature, "temperature", B)
     _dev(draft, "draft", (torch.float32, torch.bfloat16), 3)
@@ -940,6 +949,7 @@ def _head_inputs(hidden, weight, labels):
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2 or weight.shape[1] != d:
         raise ValueError("weight must be [V, d] with hidden's d")
     V = weight.shape[0]
+    _int32(N=N, V=V, d=d)
     _vec(labels, "labels", N)
     _dev(hidden, "hidden", (torch.float32, torch.bfloat16), 2)
     _dev(weight, "weight", hidden.dtype, 2)

@@ -465,16 +465,40 @@ __global__ __launch_bounds__(kMergeThreads) void teacher_merge_kernel(TeacherArg
   }
 }
 
-// Candidates a segment may list: on Gaussian rows 22 (K = 1) to 460 (K = 256) reach tau on average, 700 at
-// most seen of 160 segments; a short row may have no full wave to take tau from (at most 64 vectors and
-// 14 scalars, all listed then).  Vectors reaching one of the earlier bounds: one such lot per doubling.
-int list_cap(int K) { return 3 * K + 640 + (K & 1); }   // even: the vectors behind the keys lie on 16 bytes
-int hit_cap(int K) { return 6 * K + 288; }
+// Candidates a segment of at most `vecs` vectors of EPV values may list: on Gaussian rows 22 (K = 1) to 460
+// (K = 256) reach tau on average, 700 at most seen of 160 segments.  Where the full waves are too few to take
+// tau from (more than 64 values of each: a row of fewer than 258 vectors), everything is listed.  (By the first
+// rule alone rows of 1500 bf16 with K = 200 took the 53 counting passes of tied rows.)
+constexpr int least_waves(int vecs) { return vecs < 66 ? 0 : vecs >= 514 ? kSegWaves : (vecs - 2) >> 6; }
+constexpr bool no_bound(int vecs, int K) { return K > SPEC_WAVE * least_waves(vecs); }
+constexpr int list_cap(int vecs, int epv, int K) {   // even: the vectors behind the keys lie on 16 bytes
+  const int some = 3 * K + 640 + (K & 1), all = vecs * epv + 14;
+  return no_bound(vecs, K) && all > some ? all + (all & 1) : some;
+}
+// Vectors reaching one of the earlier bounds: one such lot per doubling, and each vector once at most.
+constexpr int hit_cap(int vecs, int K) { return vecs < 6 * K + 288 ? vecs + 1 : 6 * K + 288; }
+
+constexpr bool lists_fit() {
+  for (int epv : {4, 8})
+    for (int K : {1, 64, 65, 128, 129, 192, 193, 256})
+      for (int vecs = 0; vecs < 700; ++vecs)
+        // a segment of vecs or up to two fewer vectors, and 14 scalars, without a bound
+        if (K > SPEC_WAVE * (vecs < 66 ? 0 : (vecs - 2) / SPEC_WAVE) && vecs * epv + 14 > list_cap(vecs, epv, K)) return false;
+  return true;
+}
+static_assert(lists_fit(), "a segment that has no bound lists all of its values");
+static_assert(!no_bound(kSegChunk / 2, SPEC_MAX_TEACHER_K), "segments of a row cut into several have a bound");
 static_assert(3 * SPEC_MAX_TEACHER_K + 641 + SPEC_MAX_TEACHER_K <= kMergeKeys, "a list fits a round of the merge");
 
+// Vectors of a segment at most.
+int segment_vecs(int V, int dtype, int nseg) { return (V / (dtype == SPEC_BF16 ? 8 : 4) + nseg - 1) / nseg; }
+
 size_t segs_bytes(size_t rows, int nseg) { return round256(rows * nseg * sizeof(TeacherSeg)); }
-size_t keys_bytes(size_t rows, int nseg, int K) {
-  return nseg > 1 ? round256(rows * nseg * (size_t)list_cap(K) * sizeof(uint64_t)) : 0;
+size_t keys_bytes(size_t rows, int nseg, int cap) {
+  return nseg > 1 ? round256(rows * nseg * (size_t)cap * sizeof(uint64_t)) : 0;
+}
+int teacher_cap(int V, int dtype, int nseg, int K) {
+  return list_cap(segment_vecs(V, dtype, nseg), dtype == SPEC_BF16 ? 8 : 4, K);
 }
 
 }  // namespace
@@ -488,7 +512,7 @@ extern "C" size_t spec_teacher_workspace_size(int32_t B, int32_t gamma, int32_t 
   size_t most = 0;
   for (int dtype : {SPEC_F32, SPEC_BF16}) {   // the larger of the two storage types'
     const int nseg = row_segments((int64_t)rows, V, dtype);
-    const size_t n = segs_bytes(rows, nseg) + keys_bytes(rows, nseg, K);
+    const size_t n = segs_bytes(rows, nseg) + keys_bytes(rows, nseg, teacher_cap(V, dtype, nseg, K));
     if (n > most) most = n;
   }
   return most;
@@ -507,8 +531,8 @@ extern "C" int32_t spec_teacher_topk(int32_t B, int32_t gamma, int32_t V, int32_
   a.B = B; a.G = gamma; a.V = V; a.K = K;
   const uint64_t rows = (uint64_t)B * gamma;
   a.nseg = row_segments((int64_t)rows, V, dtype);
-  a.cap = list_cap(K);
-  a.hits = hit_cap(K);
+  a.cap = teacher_cap(V, dtype, a.nseg, K);
+  a.hits = hit_cap(segment_vecs(V, dtype, a.nseg), K);
   if (rows * a.nseg * kSegThreads > 0xffffffffull) return SPEC_ERR_UNSUPPORTED;
   a.target = target_logits; a.lengths = lengths; a.temperature = temperature;
   a.ids = ids_out; a.values = values_out; a.lse = lse_out; a.status = status;

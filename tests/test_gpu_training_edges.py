@@ -105,3 +105,23 @@ def test_normaliser_of_rows_summed_again(sv):
     want = np.log(1.0 + (V - first - 1) * np.exp(x))
     err = np.abs(got - want) / U
     assert (err <= 38 + 3 * np.abs(x) + np.abs(want)).all(), (err.max(), int(err.argmax()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,K", [(500, 256), (520, 64), (531, 65), (1000, 65), (1000, 119), (1100, 152), (1500, 129),
+                                 (1500, 200), (1800, 193), (2047, 256), (2060, 256), (1025, 256), (263, 256)])
+def test_lists_of_rows_without_a_bound(sv, dtype, V, K):
+    """Short rows with long lists: too few full waves to take a bound from, every value is a candidate."""
+    rng = np.random.default_rng(V + K)
+    B, G = 5, 3
+    t = torch.from_numpy(rng.normal(0, 3, (B, G + 1, V)).astype(np.float32))
+    t[1] = torch.arange(V) / 64.0                      # rising
+    t[2] = torch.from_numpy(rng.integers(-2, 3, (G + 1, V)).astype(np.float32))
+    t[3, :, rng.random(V) < 0.5] = -np.inf
+    t = t.to(DT[dtype]).to(DEV)
+    print(f"lists {V} {K} {dtype}", flush=True)
+    got = sv.teacher_topk(t, K)
+    torch.cuda.synchronize()
+    ref = oracle.teacher_topk(t, K)
+    assert (_np(got["ids"]) == ref["ids"]).all() and np.array_equal(_np(got["values"]), ref["values"])
+    assert (np.abs(_np(got["lse"]) - ref["lse"]) <= U * (110 + np.abs(ref["lse"]))).all()

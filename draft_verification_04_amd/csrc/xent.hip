@@ -12,7 +12,9 @@
 //   kStore  dW of the piece: A = H^T, B = G^T; rounded to the storage type.
 // W^T, H^T and G^T are read as they lie, turned by the transposing LDS read, in bf16; fp32 has no such read
 // and takes transposed copies (bf16 by copies: 18.1 ms in place of 17.4 on the case below).
-// G is rounded to bf16 for its products; its one large entry per row, the label's, is corrected in fp32.
+// G is rounded to bf16 for its products; the label's entry, as large as the rest of its row together, is corrected
+// in fp32.  (An entry as large, of another token that the row is sure of, stays rounded: half a step of bf16,
+// as much as the rounding of the result.)
 // The pieces bound the memory: G of one piece at a time instead of N V logits.
 //
 // Bound by the matrix units.  MI355X, N = 4096, V = 151936, d = 4352, bf16 (a product is 5.42 TFLOP): kStats
@@ -603,7 +605,7 @@ __device__ __forceinline__ void finish_hidden(const GemmArgs& g, int bm, int bn,
   }
 }
 
-// dW of the tokens that are labels (bf16): the label's entry of G, (p - 1) grad_loss, outweighs the rest of
+// dW of the tokens that are labels (bf16): the label's entry of G, (p - 1) grad_loss, is as large as the rest of
 // its row together, and its rounding alone would add as much again to the gradient's error.  The product
 // leaves these tokens' sums unrounded at their first row; the workgroups of that row (one per 1024 columns)
 // add, in row order, what the rounding left out times the hidden state of every row with the label, and

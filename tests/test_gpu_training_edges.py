@@ -125,3 +125,43 @@ def test_lists_of_rows_without_a_bound(sv, dtype, V, K):
     ref = oracle.teacher_topk(t, K)
     assert (_np(got["ids"]) == ref["ids"]).all() and np.array_equal(_np(got["values"]), ref["values"])
     assert (np.abs(_np(got["lse"]) - ref["lse"]) <= U * (110 + np.abs(ref["lse"]))).all()
+
+
+@pytest.mark.parametrize("N,V,d", [(60, 500, 64), (200, 1000, 208), (300, 2500, 1208), (1100, 3000, 1104)])
+def test_label_entries_of_the_head_gradients_are_rounded_once(sv, N, V, d):
+    """Hidden states and weights of one value per row, each in a column of its own: every entry of both gradients
+    is one entry of G times one factor.  A label's entry of G takes part unrounded, so its products carry
+    half a step of bf16, the others' half a step of G besides.  (z is exact; lse is off by 310 u + u |lse|, the
+    exponential by 310 u, u = 2^-24, and the fp32 products and sums by 8 u.)"""
+    g = torch.Generator().manual_seed(N)
+    a = (torch.randn(N, generator=g) * 1.5).to(torch.bfloat16)
+    b = (torch.randn(min(V, d), generator=g) * 1.5).to(torch.bfloat16)
+    h, w = torch.zeros((N, d), dtype=torch.bfloat16), torch.zeros((V, d), dtype=torch.bfloat16)
+    h[torch.arange(N), torch.arange(N)] = a
+    w[torch.arange(len(b)), torch.arange(len(b))] = b
+    y = (torch.arange(N) * 7 + 3) % 50
+    gl = torch.randn(N, generator=g)
+    H, W, Y, L = h.to(DEV), w.to(DEV), y.to(torch.int32).to(DEV), gl.to(DEV)
+    f = sv.head_xent(H, W, Y)
+    out = sv.head_xent_backward(H, W, Y, f["lse"], L)
+    torch.cuda.synchronize()
+    z = np.zeros((N, V))
+    z[np.arange(N), np.arange(N)] = _np(a) * _np(b)[:N]
+    lse = np.log(np.exp(z).sum(1, keepdims=True))
+    p, hot = np.exp(z - lse), np.eye(V)[y.numpy()]
+    G, scale = (p - hot) * _np(gl)[:, None], np.abs(_np(gl))[:, None]
+    e32 = p * scale * U * (620 + 2 * np.abs(lse)) + 8 * U * np.abs(G)
+    half = 2.0 ** -8 * (1 + 2 ** -10)
+    rounded = _np(torch.from_numpy(G).to(torch.bfloat16))
+    n = len(b)
+    for name, got, x, e, k, label in (
+            ("grad_hidden", _np(out["grad_hidden"])[:, :n], G[:, :n], e32[:, :n], _np(b)[None], hot[:, :n]),
+            ("grad_weight", _np(out["grad_weight"])[:, :N], G.T, e32.T, _np(a)[None], hot.T)):
+        want, label = x * k, label.astype(bool)
+        once = e * np.abs(k) + half * np.abs(want) + 1e-37
+        err = np.abs(got - want)
+        assert (err <= once + ~label * half * np.abs(want)).all(), name
+        # the bound tells them apart: of the label's entries, G rounded before the product passes it
+        twice = _np(torch.from_numpy((rounded[:, :n] if name == "grad_hidden" else rounded.T) * k).to(torch.bfloat16))
+        assert (np.abs(twice - want) > once)[label].any(), name
+    assert not _np(out["grad_hidden"])[:, n:].any() and not _np(out["grad_weight"])[:, N:].any()

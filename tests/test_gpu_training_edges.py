@@ -165,3 +165,60 @@ def test_label_entries_of_the_head_gradients_are_rounded_once(sv, N, V, d):
         twice = _np(torch.from_numpy((rounded[:, :n] if name == "grad_hidden" else rounded.T) * k).to(torch.bfloat16))
         assert (np.abs(twice - want) > once)[label].any(), name
     assert not _np(out["grad_hidden"])[:, n:].any() and not _np(out["grad_weight"])[:, N:].any()
+
+
+@pytest.mark.parametrize("mode", ["kl", "tv"])
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_gradients_against_differences(sv, mode, tail):
+    """Central differences of step e = 2^-4 on rows where teacher and draft stand well apart, so that no p = q lies
+    within a step and the entries looked at are several times the difference's own error: the losses are off by
+    400 u each (u = 2^-24), so the quotient by 400 u / e, and by e^2 / 6 times a third derivative, at most
+    1 / (8 T^3) of a sum of probabilities, 1 / (10 T^3) of a logarithm of one and, with a tail, of a second."""
+    B, G, V, K, e = 3, 2, 40, 6, 2.0 ** -4
+    rng = np.random.default_rng(5)
+    d = np.zeros((B, G, V), dtype=np.float32)
+    ids = np.zeros((B, G, K), dtype=np.int32)
+    vals = np.tile(np.arange(4.0, 1.0, -0.5, dtype=np.float32), (B, G, 1))
+    far = np.zeros((B, G), dtype=np.int64)
+    for i in range(B):
+        for k in range(G):
+            at = rng.permutation(V)
+            ids[i, k], far[i, k] = at[:K], at[K]
+            d[i, k, at[:K]] = vals[i, k, ::-1]      # the list's logits the other way round
+            d[i, k, at[K]] = 2.5                    # and a token outside it
+    T = np.array([0.75, 1.0, 1.25], dtype=np.float32)
+    lse = np.log(np.exp(vals / T[:, None, None].astype(np.float64)).sum(2)) + 0.1
+    c = lambda x: torch.from_numpy(x).to(DEV)
+    D, ID, VA, TE, W = c(d), c(ids), c(vals), c(T), torch.ones((B, G), device=DEV)
+    LS = c(lse.astype(np.float32)) if tail else None
+    m = sv.SPEC_DISTILL_KL if mode == "kl" else sv.SPEC_DISTILL_TV
+    f = sv.distill_loss(D, ID, VA, LS, m, None, TE)
+    grad = _np(sv.distill_loss_backward(D, ID, VA, f["saved"], W, m, TE))
+    loss = lambda x: sv.distill_loss(x, ID, VA, LS, m, None, TE)["loss"]
+    seen = 0
+    same = np.ones((B, G), dtype=bool)
+    for j in range(K + 1):
+        at = c(np.concatenate([ids, far[..., None].astype(np.int32)], 2)[..., j:j + 1].astype(np.int64))
+        x, y = (D.scatter_add(2, at, torch.full(at.shape, s * e, device=DEV)) for s in (1, -1))
+        if mode == "tv":
+            assert min(oracle.distill_loss(t, ID, VA, LS, "tv", None, TE)["margin"].min() for t in (x, y)) > 440 * U
+            # rows whose comparisons all fall the same way on both sides (each q is monotone in between)
+            sides = [_sides(t, ids, vals, lse if tail else None, T) for t in (_np(x), _np(y))]
+            same = (sides[0] == sides[1]).all(axis=2)
+        diff = (_np(loss(x)) - _np(loss(y))) / (2 * e)
+        g = np.take_along_axis(grad, at.cpu().numpy(), 2)[..., 0]
+        third = (0.125 if mode == "tv" else 0.2) / T[:, None].astype(np.float64) ** 3
+        tol = 400 * U * (1 + np.abs(_np(f["loss"]))) / e + e * e / 6 * third + 1e-6
+        assert (np.abs(diff - g) <= tol)[same].all(), (j, np.abs(diff - g).max())
+        seen += (np.abs(g) > 8 * tol)[same].sum()
+    assert seen >= 3 * B * G, seen
+
+
+def _sides(x, ids, vals, lse, T):
+    t = T[:, None, None].astype(np.float64)
+    q = np.exp(x / t)
+    q /= q.sum(2, keepdims=True)
+    p = np.exp(vals / t)
+    p /= p.sum(2, keepdims=True) if lse is None else np.exp(lse)[..., None]
+    s = np.take_along_axis(q, ids.astype(np.int64), 2)
+    return np.concatenate([p > s, (1 - p.sum(2, keepdims=True)) > (1 - s.sum(2, keepdims=True))], 2)

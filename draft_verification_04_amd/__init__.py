@@ -803,7 +803,7 @@ def teacher_topk(target: torch.Tensor, K: int, lengths: Optional[torch.Tensor] =
 
     target [B, gamma+1, V] (float32 or bfloat16; row gamma is not read), lengths [B] int32 or None,
     temperature [B] float32 (default ones, > 0).  Returns dict(ids [B, gamma, K] int32, values
-    [B, gamma, K] float32, lse [B, gamma] float32, status [B] int32).
+    [B, gamma, K] float32, lse [B, gamma] float32, status [B] int32), constants to autograd.
     """
     lib = load_library()
     if not isinstance(target, torch.Tensor) or target.dim() != 3:
@@ -871,6 +871,9 @@ def distill_loss(draft: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
     bucket (None: the list is renormalised); mode SPEC_DISTILL_KL or SPEC_DISTILL_TV; lengths [B] int32;
     temperature [B] float32 (default ones, > 0).  Returns dict(loss [B, gamma] float32, saved (for
     distill_loss_backward), status [B] int32).
+
+    No autograd graph is built, also where draft requires a gradient: the loss comes back detached, and the
+    gradient is distill_loss_backward's (call the two from a torch.autograd.Function to train through them).
     """
     lib = load_library()
     B, G, V, K = _list_inputs(draft, ids, values, temperature)
@@ -912,7 +915,8 @@ def distill_loss_backward(draft: torch.Tensor, ids: torch.Tensor, values: torch.
     respect to the draft logits, [B, gamma, V] in draft's dtype.
 
     draft, ids, values, mode and temperature as given to distill_loss, `saved` its output.  in_place
-    writes the gradient over `draft`.
+    writes the gradient over `draft`, unseen by autograd: not for logits that other operations saved for
+    their backward.
     """
     lib = load_library()
     B, G, V, K = _list_inputs(draft, ids, values, temperature)
@@ -965,6 +969,10 @@ def head_xent(hidden: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor, 
     hidden [N, d] and weight [V, d] (both float32 or both bfloat16; rows of a multiple of 16 bytes),
     labels [N] int32 (-1: the row is left out, loss 0).  The logits are not stored.  Returns dict(loss
     [N] float32, lse [N] float32 (for head_xent_backward), status [N] int32).
+
+    No autograd graph is built, also where hidden or weight requires a gradient: the loss comes back detached,
+    and the gradients are head_xent_backward's (call the two from a torch.autograd.Function to train through
+    them).
     """
     lib = load_library()
     N, V, d = _head_inputs(hidden, weight, labels)

@@ -222,3 +222,49 @@ def _sides(x, ids, vals, lse, T):
     p /= p.sum(2, keepdims=True) if lse is None else np.exp(lse)[..., None]
     s = np.take_along_axis(q, ids.astype(np.int64), 2)
     return np.concatenate([p > s, (1 - p.sum(2, keepdims=True)) > (1 - s.sum(2, keepdims=True))], 2)
+
+
+def test_losses_from_an_autograd_function(sv):
+    """As documented: the calls come back detached where an input requires a gradient, and train through a
+    torch.autograd.Function that makes both of them."""
+    class Xent(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, h, w, y):
+            o = sv.head_xent(h, w, y)
+            ctx.save_for_backward(h, w, y, o["lse"])
+            return o["loss"]
+
+        @staticmethod
+        def backward(ctx, g):
+            h, w, y, lse = ctx.saved_tensors
+            o = sv.head_xent_backward(h, w, y, lse, g.contiguous())
+            return o["grad_hidden"], o["grad_weight"], None
+
+    class Distill(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, d, ids, vals):
+            o = sv.distill_loss(d, ids, vals)
+            ctx.save_for_backward(d, ids, vals, o["saved"])
+            return o["loss"]
+
+        @staticmethod
+        def backward(ctx, g):
+            d, ids, vals, saved = ctx.saved_tensors
+            return sv.distill_loss_backward(d, ids, vals, saved, g.contiguous()), None, None
+
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    h = torch.randn((30, 64), generator=g, device=DEV, requires_grad=True)
+    w = torch.randn((400, 64), generator=g, device=DEV, requires_grad=True)
+    y = torch.randint(400, (30,), generator=g, device=DEV).to(torch.int32)
+    d = torch.randn((2, 3, 500), generator=g, device=DEV, requires_grad=True)
+    t = sv.teacher_topk(torch.randn((2, 4, 500), generator=g, device=DEV), 8)
+    o, f = sv.head_xent(h, w, y), sv.distill_loss(d, t["ids"], t["values"])
+    assert not any(x.requires_grad for x in (*o.values(), *f.values()))
+    c, e = torch.rand((30,), generator=g, device=DEV), torch.rand((2, 3), generator=g, device=DEV)
+    ((Xent.apply(h, w, y) * c).sum() + (Distill.apply(d, t["ids"], t["values"]) * e).sum()).backward()
+    b = sv.head_xent_backward(h, w, y, o["lse"], c)
+    torch.cuda.synchronize()
+    assert torch.equal(h.grad, b["grad_hidden"]) and torch.equal(w.grad, b["grad_weight"])
+    assert torch.equal(d.grad, sv.distill_loss_backward(d, t["ids"], t["values"], f["saved"], e))
+    assert not b["grad_hidden"].requires_grad

@@ -17,12 +17,14 @@ inline int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 inline long long round_to(long long a, long long b) { return (a + b - 1) / b * b; }
 inline size_t round_bytes(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Tile shapes of the product.  bf16: 256 x 256 (8 waves, one workgroup per CU); 128 x 128 and, for rowsB of at
+// Tile shapes of the product.  bf16: 256 x 256 (8 waves, one workgroup per CU); 128 x 128 or, for rowsB of at
 // most 64, 128 x 64 (4 waves, two per CU); and for kStats and kGradZ, where there are few tiles and a step
 // waits for its loads, 128 x 64 with six steps in flight (one per CU) and 64 x 64 with five (two per CU).
 // Loss and gradients of 348 x 717, d = 3064 by the three last shapes: 32, 24, 19.5 us and 85, 63, 55 us; of
 // 1000 x 1000, d = 2048: 28, 18, 15 and 72, 60, 56; of 246 x 6727, d = 2896 (two of the smallest tiles per
-// CU): 44, 29.7, 32.3.  fp32 is bound by the matrix units (a sixteenth of the bf16 rate), so what counts is
+// CU): 44, 29.7, 32.3.  At most 64 rows by 128 x 64 and by 64 x 64: 1 x 1000, d = 4096: 30.0, 20.8 us and 40.5,
+// 35.1; 64 x 717, d = 3064: 23.0, 18.8 and 39.6, 34.7; 64 x 8000, d = 2048: 21.3, 16.0 and 57.2, 49.0; from
+// some 20000 tokens on there are two 128 x 64 tiles per CU and they stay.  fp32 is bound by the matrix units (a sixteenth of the bf16 rate), so what counts is
 // that every CU has its share: 128 x 64 (against 128 x 128 and 256 x 256, 200 x 20000, d = 1024: 132 -> 109 us;
 // gradients of 1000 x 1000, d = 2048: 197 -> 169), or 64 x 64 (76 -> 44 us; 169 -> 135).
 enum { kBig = 0, kMid = 1, kThin = 2, kDeep = 3, kSmall = 4 };
@@ -61,7 +63,6 @@ inline Shape pick_shape(long long rowsA, long long rowsB, int kbytes, int es, bo
   if (es == 4) return Shape{rowsA >= rowsB, 0, cost(rowsA, rowsB, kSmall) < cost(rowsA, rowsB, kThin) ? kSmall : kThin};
   Shape best{rowsA >= rowsB, 0, rowsB <= 64 && !store ? kThin : kMid};   // dW has no narrow tiles
   double us = cost(rowsA, rowsB, best.tail);
-  if (rowsB <= 64) return best;
   if (!store)
     for (int t : {kDeep, kSmall})
       if (cost(rowsA, rowsB, t) < us) {

@@ -14,7 +14,9 @@ PKG = os.path.join(ROOT, "draft_verification_04_amd")
 
 # (N, V, d, dtype): stats, gradz, store, acc, pieces
 PLANS = {
-    (61, 4500, 200, "bf16"): ("thin", "thin", "mid", ("thin", False, True), 1),
+    (61, 4500, 200, "bf16"): ("small", "small", "mid", ("thin", False, True), 1),
+    (1, 1000, 4096, "bf16"): ("small", "small", "mid", ("thin", False, True), 1),
+    (61, 45000, 200, "bf16"): ("thin", "thin", "big", ("thin", False, True), 1),
     (5, 300001, 16, "bf16"): ("thin", "thin", "mid", ("thin", False, True), 2),
     (40, 90000, 512, "bf16"): ("thin", "thin", "big", ("thin", False, True), 1),
     (348, 717, 3064, "bf16"): ("small", "small", "mid", ("mid", False, False), 1),

@@ -268,3 +268,41 @@ def test_losses_from_an_autograd_function(sv):
     assert torch.equal(h.grad, b["grad_hidden"]) and torch.equal(w.grad, b["grad_weight"])
     assert torch.equal(d.grad, sv.distill_loss_backward(d, t["ids"], t["values"], f["saved"], e))
     assert not b["grad_hidden"].requires_grad
+
+
+def test_head_fp32_sums_of_long_rows(sv):
+    """Sums of equal terms, whose roundings all fall the same way.  A product is rounded 256 times at most in its
+    block and once per block of 256 (and once as a product): 256 + k / 256 + 2 roundings, not k."""
+    g = torch.Generator().manual_seed(3)
+    N, V, d = 64, 40, 16384
+    a, b = torch.rand(N, generator=g) + 0.5, (torch.rand(V, generator=g) - 0.3) * (3.0 / d)
+    h, w = a[:, None].repeat(1, d).contiguous().to(DEV), b[:, None].repeat(1, d).contiguous().to(DEV)
+    y = (torch.arange(N) % V).to(torch.int32).to(DEV)
+    o = sv.head_xent(h, w, y)
+    torch.cuda.synchronize()
+    z = d * np.outer(_np(a), _np(b))
+    lse = np.log(np.exp(z).sum(1))
+    loss = lse - z[np.arange(N), np.arange(N) % V]
+    dz = (256 + d / 256 + 2) * U * np.abs(z).max(1)
+    assert (np.abs(_np(o["lse"]) - lse) <= dz + U * (310 + np.abs(lse))).all()
+    assert (np.abs(_np(o["loss"]) - loss) <= 2 * dz + U * (310 + np.abs(lse) + np.abs(loss))).all()
+    # grad_weight: as many equal rows
+    N, V, d = 8192, 6, 8
+    a, b = torch.rand(d, generator=g) + 0.5, torch.randn((V, d), generator=g)
+    h, w = a.repeat(N, 1).contiguous().to(DEV), b.to(DEV)
+    y = torch.full((N,), 2, dtype=torch.int32, device=DEV)
+    gl = torch.full((N,), 0.7, device=DEV)
+    o = sv.head_xent(h, w, y)
+    gw = sv.head_xent_backward(h, w, y, o["lse"], gl, need_hidden=False)["grad_weight"]
+    torch.cuda.synchronize()
+    z = _np(b) @ _np(a)
+    lse = np.log(np.exp(z).sum())
+    p = np.exp(z - lse)
+    G = p.copy()
+    G[2] -= 1.0
+    G *= float(gl[0])
+    want = N * np.outer(G, _np(a))
+    dz = (d + 2) * U * (np.abs(_np(b)) @ np.abs(_np(a)))
+    eG = p * 0.7 * (2 * dz + dz.max() + U * (620 + np.abs(lse))) * 1.01 + 4 * U * np.abs(G)
+    tol = N * np.outer(eG, _np(a)) + (256 + N / 256 + 2) * U * np.abs(want)
+    assert (np.abs(_np(gw) - want) <= tol).all()

@@ -536,6 +536,14 @@ extern "C" int32_t spec_distill_loss_backward(int32_t B, int32_t gamma, int32_t 
   a.nseg = vecs <= kSegChunk ? 1 : (vecs + kSegChunk - 1) / kSegChunk;   // a chunk each: held in registers
   const uint64_t rows = (uint64_t)B * gamma;
   if (rows * a.nseg * kSegThreads > 0xffffffffull) return SPEC_ERR_UNSUPPORTED;
+  // a workgroup reads its part of the logits before it writes it; of any other place nothing is known
+  const size_t bytes = rows * (size_t)V * (dtype == SPEC_BF16 ? 2 : 4), list = rows * K * sizeof(float);
+  if ((grad_out != draft_logits && overlap(grad_out, bytes, draft_logits, bytes)) ||
+      overlap(grad_out, bytes, teacher_ids, list) || overlap(grad_out, bytes, teacher_values, list) ||
+      overlap(grad_out, bytes, saved, rows * SPEC_DISTILL_SAVED * sizeof(double)) ||
+      overlap(grad_out, bytes, grad_loss, rows * sizeof(float)) ||
+      overlap(grad_out, bytes, temperature, B * sizeof(float)))
+    return SPEC_ERR_INVALID_ARG;
   a.draft = draft_logits; a.ids = teacher_ids; a.values = teacher_values; a.temperature = temperature;
   a.saved = const_cast<double*>(saved); a.grad_loss = grad_loss; a.grad = grad_out;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);

@@ -346,6 +346,10 @@ constexpr uint32_t kNegInfKey = 0x007fffffu;   // order_key(-inf)
 bool shape_ok(int B, int G, int V, int dtype);
 bool aligned16(const void* p);
 inline bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {   // NULL overlaps nothing
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + bn && y < x + an;
+}
 inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace spec

@@ -29,6 +29,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "common.hpp"
 #include "rowseg.hpp"
 #include "spec_verify.h"
@@ -929,6 +931,13 @@ extern "C" int32_t spec_head_xent_backward(int32_t N, int32_t V, int32_t d, int3
   if (!workspace || !aligned256(workspace) ||
       workspace_bytes < spec_head_xent_backward_workspace_size(N, V, d, dtype))
     return SPEC_ERR_WORKSPACE;
+  // the inputs are read after the first piece's gradients are written
+  const size_t row = (size_t)d * (dtype == SPEC_BF16 ? 2 : 4), h_bytes = N * row, w_bytes = V * row;
+  for (auto [g, n] : {std::pair<const void*, size_t>{grad_hidden, h_bytes}, {grad_weight, w_bytes}})
+    if (overlap(g, n, hidden, h_bytes) || overlap(g, n, weight, w_bytes) || overlap(g, n, labels, N * sizeof(int32_t)) ||
+        overlap(g, n, lse, N * sizeof(float)) || overlap(g, n, grad_loss, N * sizeof(float)))
+      return SPEC_ERR_INVALID_ARG;
+  if (overlap(grad_hidden, h_bytes, grad_weight, w_bytes)) return SPEC_ERR_INVALID_ARG;
   if (!head_fits(N, V, d)) return SPEC_ERR_UNSUPPORTED;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   char* ws = reinterpret_cast<char*>(workspace);

@@ -647,7 +647,7 @@ int32_t spec_teacher_topk(int32_t B, int32_t gamma, int32_t V, int32_t dtype, co
  *   grad_out     [B, gamma, V] dtype, 16-byte aligned; may be draft_logits
  *                itself (each logit is read before its gradient is written)
  * No workspace; one kernel (512 work-items per row and 64 KB of a row).  Errors:
- * as above.
+ * as above; SPEC_ERR_INVALID_ARG where grad_out overlaps an input in any other way.
  */
 size_t spec_distill_workspace_size(int32_t B, int32_t gamma, int32_t V, int32_t K);
 
@@ -700,7 +700,7 @@ int32_t spec_distill_loss_backward(int32_t B, int32_t gamma, int32_t V, int32_t 
  *   grad_hidden, grad_weight: 16-byte aligned, distinct from the inputs
  *   workspace    at least spec_head_xent_backward_workspace_size(N, V, d, dtype)
  * Errors: SPEC_ERR_INVALID_ARG (shape, dtype, alignment, null pointer, both
- * gradients NULL), SPEC_ERR_WORKSPACE, SPEC_ERR_UNSUPPORTED (a launch past 2^32
+ * gradients NULL, a gradient that overlaps an input or the other one), SPEC_ERR_WORKSPACE, SPEC_ERR_UNSUPPORTED (a launch past 2^32
  * work-items).
  */
 size_t spec_head_xent_workspace_size(int32_t N, int32_t V, int32_t d, int32_t dtype);

@@ -1,4 +1,7 @@
-"""Sizes that do not fit the C ABI's int32 are refused by the binding (ctypes would pass their low 32 bits on)."""
+"""Training calls that would be answered wrongly are refused: sizes that do not fit the C ABI's int32 (ctypes
+would pass their low 32 bits on), and gradients that would overwrite what the call still reads."""
+
+import ctypes
 
 import pytest
 import torch
@@ -31,3 +34,33 @@ def test_sizes_past_32_bits_are_refused():
     for name, call in calls:
         with pytest.raises(ValueError, match=f"^{name} = "):
             call()
+
+
+def test_gradients_over_inputs_are_refused():
+    """The buffer is host memory: every call below is refused before anything is enqueued."""
+    lib = sv.load_library()
+    N, V, d, dt = 4, 16, 64, 1                       # hidden 512 bytes, weight 2048
+    ws = lib.spec_head_xent_backward_workspace_size(N, V, d, dt)
+    buf = (ctypes.c_uint8 * (ws + 16384))()
+    base = (ctypes.addressof(buf) + 255) & ~255
+    at = lambda n: ctypes.c_void_p(base + n)
+    where = dict(h=0, W=512, y=2560, ls=2576, g=2592, gh=3072, gw=3584)
+    work = at(8192)
+
+    def call(**moved):
+        w = {**where, **moved}
+        return lib.spec_head_xent_backward(N, V, d, dt, at(w["h"]), at(w["W"]), at(w["y"]), at(w["ls"]), at(w["g"]),
+                                           at(w["gh"]), at(w["gw"]), work, ws, None)
+    for moved in (dict(gh=0), dict(gh=256), dict(gh=2048), dict(gw=512), dict(gw=0), dict(gw=1024), dict(gh=2544),
+                  dict(gh=2560), dict(gw=2576), dict(gh=4096), dict(gw=3072)):
+        assert call(**moved) == 1, moved
+
+    B, G, V, K = 2, 2, 64, 4                         # logits 512 bytes, the list 64 + 64, saved 256
+    where2 = dict(x=0, i=512, v=576, T=640, sv=656, g=912)
+
+    def back(o):
+        w = {k: at(n) for k, n in where2.items()}
+        return lib.spec_distill_loss_backward(B, G, V, dt, w["x"], K, w["i"], w["v"], 0, w["T"], w["sv"], w["g"], at(o),
+                                              None)
+    for o in (16, 256, 496, 512, 576, 640, 656, 896, 912):
+        assert back(o) == 1, o

@@ -18,7 +18,9 @@ namespace spec {
 
 constexpr int kSegThreads = 512;
 constexpr int kSegWaves = kSegThreads / SPEC_WAVE;
-constexpr int kSegVecs = 8;   // 16-byte vectors per thread: 32 registers, 8 waves per SIMD
+// 16-byte vectors per thread: 32 registers; the kernels that read rows keep within 64 (8 waves per SIMD), the
+// distillation gradient takes 66 (7)
+constexpr int kSegVecs = 8;
 constexpr int kSegWorkgroups = 512;   // a call's workgroups, at least, where rows are long enough
 constexpr double kLog2eSeg = 1.44269504088896340736;
 

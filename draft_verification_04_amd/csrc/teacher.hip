@@ -468,7 +468,7 @@ __global__ __launch_bounds__(kMergeThreads) void teacher_merge_kernel(TeacherArg
 // Candidates a segment of at most `vecs` vectors of EPV values may list: on Gaussian rows 22 (K = 1) to 460
 // (K = 256) reach tau on average, 700 at most seen of 160 segments.  Where the full waves are too few to take
 // tau from (more than 64 values of each: a row of fewer than 258 vectors), everything is listed.  (By the first
-// rule alone rows of 1500 bf16 with K = 200 took the 53 counting passes of tied rows.)
+// rule alone they took the 53 counting passes of tied rows: 256 x 16 of 1500 bf16, K = 200: 281 us in place of 197.)
 constexpr int least_waves(int vecs) { return vecs < 66 ? 0 : vecs >= 514 ? kSegWaves : (vecs - 2) >> 6; }
 constexpr bool no_bound(int vecs, int K) { return K > SPEC_WAVE * least_waves(vecs); }
 constexpr int list_cap(int vecs, int epv, int K) {   // even: the vectors behind the keys lie on 16 bytes

@@ -26,7 +26,8 @@ inline size_t round_bytes(size_t x) { return (x + 255) & ~(size_t)255; }
 // 35.1; 64 x 717, d = 3064: 23.0, 18.8 and 39.6, 34.7; 64 x 8000, d = 2048: 21.3, 16.0 and 57.2, 49.0; from
 // some 20000 tokens on there are two 128 x 64 tiles per CU and they stay.  fp32 is bound by the matrix units (a sixteenth of the bf16 rate), so what counts is
 // that every CU has its share: 128 x 64 (against 128 x 128 and 256 x 256, 200 x 20000, d = 1024: 132 -> 109 us;
-// gradients of 1000 x 1000, d = 2048: 197 -> 169), or 64 x 64 (76 -> 44 us; 169 -> 135).
+// gradients of 1000 x 1000, d = 2048: 197 -> 169), or 64 x 64 (76 -> 44 us; 169 -> 135; each before the sums in
+// blocks, which add 1 to 3 %).
 enum { kBig = 0, kMid = 1, kThin = 2, kDeep = 3, kSmall = 4 };
 
 inline int tile_m(int t) { return t == kBig ? 256 : t == kSmall ? 64 : 128; }

@@ -44,7 +44,7 @@ def test_gradients_over_inputs_are_refused():
     buf = (ctypes.c_uint8 * (ws + 16384))()
     base = (ctypes.addressof(buf) + 255) & ~255
     at = lambda n: ctypes.c_void_p(base + n)
-    where = dict(h=0, W=512, y=2560, ls=2576, g=2592, gh=3072, gw=3584)
+    where = dict(h=0, W=512, y=2560, ls=2576, g=2592, gh=3328, gw=4096)
     work = at(8192)
 
     def call(**moved):
@@ -52,7 +52,7 @@ def test_gradients_over_inputs_are_refused():
         return lib.spec_head_xent_backward(N, V, d, dt, at(w["h"]), at(w["W"]), at(w["y"]), at(w["ls"]), at(w["g"]),
                                            at(w["gh"]), at(w["gw"]), work, ws, None)
     for moved in (dict(gh=0), dict(gh=256), dict(gh=2048), dict(gw=512), dict(gw=0), dict(gw=1024), dict(gh=2544),
-                  dict(gh=2560), dict(gw=2576), dict(gh=4096), dict(gw=3072)):
+                  dict(gh=2560), dict(gw=2576), dict(gh=4608), dict(gw=3584)):
         assert call(**moved) == 1, moved
 
     B, G, V, K = 2, 2, 64, 4                         # logits 512 bytes, the list 64 + 64, saved 256

@@ -611,7 +611,8 @@ int32_t spec_teacher_topk(int32_t B, int32_t gamma, int32_t V, int32_t dtype, co
  *   p_e = exp(v_e / T_i - t), t = ln sum_e exp(v_e / T_i) without teacher_lse
  *         (the list renormalised), t = teacher_lse[i, k] with it;
  *   r_t = max(0, 1 - sum_e p_e) with teacher_lse, else 0;  r_s = sum_{v not in S} q_v
- *         (the two tails: one bucket for every token outside the list);
+ *         (the two tails: one bucket for every token outside the list; r_t is 0
+ *         where S holds all V tokens, whatever the rounding of teacher_lse leaves);
  *   KL: loss = sum_e p_e (ln p_e - ln q_e) + r_t (ln r_t - ln r_s)
  *   TV: loss = sum_e max(p_e - q_e, 0) + max(r_t - r_s, 0)
  *       (without teacher_lse this is the total variation distance of the

@@ -43,6 +43,8 @@ REQ_BAD_CONFIDENCE = 32
 REQ_OVER_BUDGET = 64
 REQ_BAD_ROWS = 128
 REQ_BAD_LIST = 256
+REQ_BAD_PENALTY = 512
+REQ_BAD_MASK = 1024
 
 # name -> (restype, argtypes)
 _P = ctypes.c_void_p
@@ -88,6 +90,13 @@ EXPORTS = {
     "spec_head_xent": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
     "spec_head_xent_backward_workspace_size": (_Z, [_I, _I, _I, _I]),
     "spec_head_xent_backward": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    "spec_head_norm": (_I, [_I, _I, _I, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P, _P]),
+    "spec_head_norm_backward_workspace_size": (_Z, [_I, _I]),
+    "spec_head_norm_backward": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    "spec_head_quantize": (_I, [_I, _I, _I, _P, _P, _P, _P]),
+    "spec_head_logits": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "spec_adjust_logits": (_I, [_I, _I, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _I,
+                                _P, _P, _P, _P]),
 }
 
 _lib_handle = None
@@ -1033,3 +1042,257 @@ def head_xent_backward(hidden: torch.Tensor, weight: torch.Tensor, labels: torch
     ws = _device_workspace(int(lib.spec_head_xent_backward_workspace_size(N, V, d, dt)), dev, workspace, mine)
     _check("spec_head_xent_backward", _launch_on(dev, stream, mine, call))
     return out
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+_E4M3 = torch.float8_e4m3fn
+
+
+def _rows(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be [N, d]")
+    _int32(N=t.shape[0], d=t.shape[1])
+    return t.shape
+
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+def head_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+              quantize: bool = False, out: Optional[dict] = None, stream=None) -> dict:
+    """spec_head_norm: h = x + residual and its root-mean-square norm, y = h / sqrt(mean(h^2) + eps) * weight.
+
+    x and residual [N, d], weight [d] (all float32 or all bfloat16).  Returns dict(y [N, d], h [N, d] (x itself
+    without a residual), rstd [N] float32); quantize (d a multiple of 16) gives codes [N, d] float8_e4m3fn and
+    scales [N, ceil(d / 128)] float32 in place of y.  `out` may hold x or the residual as its h or y.
+
+    No autograd graph is built: the gradients are head_norm_backward's.
+    """
+    lib = load_library()
+    N, d = _rows(x, "x")
+    _vec(weight, "weight", d)
+    _shape(residual, "residual", (N, d))
+    _dev(x, "x", _FLOATS, 2)
+    _dev(weight, "weight", x.dtype, 1)
+    _dev(residual, "residual", x.dtype, 2)
+    dev = x.device
+    _on(dev, weight=weight, residual=residual)
+    mine = []
+    if out is None:
+        out = dict(rstd=torch.empty(N, dtype=torch.float32, device=dev))
+        if quantize:
+            out["codes"] = torch.empty((N, d), dtype=_E4M3, device=dev)
+            out["scales"] = torch.empty((N, _blocks(d)), dtype=torch.float32, device=dev)
+        else:
+            out["y"] = torch.empty_like(x)
+        if residual is not None:
+            out["h"] = torch.empty_like(x)
+        mine.extend(out.values())
+    else:
+        _check_out(out, dict(y=((N, d), x.dtype, not quantize), codes=((N, d), _E4M3, quantize),
+                             scales=((N, _blocks(d)), torch.float32, quantize),
+                             h=((N, d), x.dtype, residual is not None), rstd=((N,), torch.float32, False)), dev)
+    code = _launch_on(dev, stream, mine, lambda sp: lib.spec_head_norm(
+        N, d, _logit_dtype(x), _ptr(x), _ptr(residual), _ptr(weight), float(eps), _ptr(out.get("h")),
+        _ptr(out.get("y")), _ptr(out.get("codes")), _ptr(out.get("scales")), _ptr(out.get("rstd")), sp))
+    _check("spec_head_norm", code)
+    if residual is None and "h" not in out:
+        out = dict(out, h=x)
+    return out
+
+
+def head_norm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                       grad_h: Optional[torch.Tensor] = None, need_weight: bool = True, out: Optional[dict] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """spec_head_norm_backward: the gradients of head_norm, from grad_y [N, d] and, where h goes on along the
+    residual stream, the gradient grad_h [N, d] that comes back along it.
+
+    h, weight and rstd as head_norm took and gave them.  Returns dict(grad_x [N, d] (of x and of the residual
+    alike), grad_weight [d]) in h's dtype; need_weight=False (or an `out` without it) leaves grad_weight out.
+    """
+    lib = load_library()
+    N, d = _rows(grad_y, "grad_y")
+    _shape(h, "h", (N, d))
+    _vec(weight, "weight", d)
+    _vec(rstd, "rstd", N)
+    _shape(grad_h, "grad_h", (N, d))
+    _dev(grad_y, "grad_y", _FLOATS, 2)
+    _dev(h, "h", grad_y.dtype, 2)
+    _dev(weight, "weight", grad_y.dtype, 1)
+    _dev(rstd, "rstd", torch.float32, 1)
+    _dev(grad_h, "grad_h", grad_y.dtype, 2)
+    dev = grad_y.device
+    _on(dev, h=h, weight=weight, rstd=rstd, grad_h=grad_h)
+    mine = []
+    if out is None:
+        out = dict(grad_x=torch.empty_like(grad_y))
+        if need_weight:
+            out["grad_weight"] = torch.empty_like(weight)
+        mine.extend(out.values())
+    else:
+        _check_out(out, dict(grad_x=((N, d), grad_y.dtype, True), grad_weight=((d,), grad_y.dtype, False)), dev)
+    ws = None
+    if out.get("grad_weight") is not None:
+        ws = _device_workspace(int(lib.spec_head_norm_backward_workspace_size(N, d)), dev, workspace, mine)
+    code = _launch_on(dev, stream, mine, lambda sp: lib.spec_head_norm_backward(
+        N, d, _logit_dtype(grad_y), _ptr(grad_y), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(grad_h),
+        _ptr(out["grad_x"]), _ptr(out.get("grad_weight")), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+        sp))
+    _check("spec_head_norm_backward", code)
+    return out
+
+
+def head_quantize(weight: torch.Tensor, out: Optional[dict] = None, stream=None) -> dict:
+    """spec_head_quantize: weight [V, d] (float32 or bfloat16, d a multiple of 16) in 8 bits: dict(codes [V, d]
+    float8_e4m3fn, scales [ceil(V / 128), ceil(d / 128)] float32), a scale for each block of 128 x 128."""
+    lib = load_library()
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be [V, d]")
+    V, d = weight.shape
+    _int32(V=V, d=d)
+    _dev(weight, "weight", _FLOATS, 2)
+    dev = weight.device
+    mine = []
+    if out is None:
+        out = dict(codes=torch.empty((V, d), dtype=_E4M3, device=dev),
+                   scales=torch.empty((_blocks(V), _blocks(d)), dtype=torch.float32, device=dev))
+        mine.extend(out.values())
+    else:
+        _check_out(out, dict(codes=((V, d), _E4M3, True), scales=((_blocks(V), _blocks(d)), torch.float32, True)), dev)
+    code = _launch_on(dev, stream, mine, lambda sp: lib.spec_head_quantize(
+        V, d, _logit_dtype(weight), _ptr(weight), _ptr(out["codes"]), _ptr(out["scales"]), sp))
+    _check("spec_head_quantize", code)
+    return out
+
+
+def head_logits(codes: torch.Tensor, scales: torch.Tensor, weight_codes: torch.Tensor, weight_scales: torch.Tensor,
+                dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """spec_head_logits: the logits [N, V] (float32 or bfloat16) of hidden states against a vocabulary head, both
+    in 8 bits.
+
+    codes [N, d] and scales [N, ceil(d / 128)] as head_norm(quantize=True) gives them, weight_codes [V, d] and
+    weight_scales [ceil(V / 128), ceil(d / 128)] as head_quantize does.  `out` is written where given (the view of a
+    [B, gamma + 1, V] block as [B * (gamma + 1), V], say).
+    """
+    lib = load_library()
+    N, d = _rows(codes, "codes")
+    if not isinstance(weight_codes, torch.Tensor) or weight_codes.dim() != 2 or weight_codes.shape[1] != d:
+        raise ValueError("weight_codes must be [V, d] with the codes' d")
+    V = weight_codes.shape[0]
+    _int32(V=V)
+    _shape(scales, "scales", (N, _blocks(d)))
+    _shape(weight_scales, "weight_scales", (_blocks(V), _blocks(d)))
+    _shape(out, "out", (N, V))
+    if dtype not in _FLOATS:
+        raise TypeError(f"logits are float32 or bfloat16, got {dtype}")
+    _dev(codes, "codes", _E4M3, 2)
+    _dev(weight_codes, "weight_codes", _E4M3, 2)
+    _dev(scales, "scales", torch.float32, 2)
+    _dev(weight_scales, "weight_scales", torch.float32, 2)
+    _dev(out, "out", _FLOATS, 2)
+    dev = codes.device
+    _on(dev, scales=scales, weight_codes=weight_codes, weight_scales=weight_scales, out=out)
+    mine = []
+    if out is None:
+        out = torch.empty((N, V), dtype=dtype, device=dev)
+        mine.append(out)
+    code = _launch_on(dev, stream, mine, lambda sp: lib.spec_head_logits(
+        N, V, d, _logit_dtype(out), _ptr(codes), _ptr(scales), _ptr(weight_codes), _ptr(weight_scales), _ptr(out), sp))
+    _check("spec_head_logits", code)
+    return out
+
+
+def adjust_logits(logits: torch.Tensor, draft_tokens: Optional[torch.Tensor] = None,
+                  lengths: Optional[torch.Tensor] = None, *, history: Optional[torch.Tensor] = None,
+                  history_len: Optional[torch.Tensor] = None, prompt_len: Optional[torch.Tensor] = None,
+                  repetition: Optional[torch.Tensor] = None, frequency: Optional[torch.Tensor] = None,
+                  presence: Optional[torch.Tensor] = None, bias: Optional[tuple] = None,
+                  mask: Optional[torch.Tensor] = None, mask_index: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, in_place: bool = False, status: Optional[torch.Tensor] = None,
+                  stream=None) -> dict:
+    """spec_adjust_logits: penalties for repeated tokens, biases and masks on the rows of draft blocks.
+
+    logits [B, R, V] (float32 or bfloat16): target rows (R = gamma + 1) or draft rows (R = gamma) of blocks whose
+    draft_tokens are [B, gamma] int32 (None: R = 1, single tokens); lengths [B] int32: only rows k < L_i (+ 1 for
+    target rows) are adjusted.  history [B, H] int32 (-1 holes count for nothing), history_len and prompt_len [B]
+    int32; repetition, frequency and presence [B] float32; bias = (offsets [B + 1] int32, tokens int32, values
+    float32); mask [M, R, ceil(V / 32)] int32 bits (set: allowed) and mask_index [B] int32 (-1: none; None: mask i).
+    in_place writes over `logits` (only the values that change), unseen by autograd; otherwise `out`, or a new tensor
+    whose rows past a length or with a status are undefined.  Returns dict(logits, status [B] int32).
+    """
+    lib = load_library()
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 3:
+        raise ValueError("logits must be [B, R, V]")
+    B, R, V = logits.shape
+    G = 0
+    if draft_tokens is not None:
+        if not isinstance(draft_tokens, torch.Tensor) or draft_tokens.dim() != 2 or draft_tokens.shape[0] != B:
+            raise ValueError("draft_tokens must be [B, gamma]")
+        G = draft_tokens.shape[1]
+    if R not in (G, G + 1):
+        raise ValueError(f"logits hold {R} rows for blocks of {G} draft tokens")
+    H = 0
+    if history is not None:
+        if not isinstance(history, torch.Tensor) or history.dim() != 2 or history.shape[0] != B:
+            raise ValueError("history must be [B, H]")
+        H = history.shape[1]
+    elif history_len is not None or prompt_len is not None:
+        raise ValueError("history_len and prompt_len need a history")
+    if history is not None and H == 0:   # of no tokens: the lengths can only be 0
+        history = history_len = prompt_len = None
+    for name, t in (("lengths", lengths), ("history_len", history_len), ("prompt_len", prompt_len),
+                    ("repetition", repetition), ("frequency", frequency), ("presence", presence),
+                    ("mask_index", mask_index), ("status", status)):
+        _vec(t, name, B)
+    offsets, tokens, values = bias if bias is not None else (None, None, None)
+    nb = 0
+    if bias is not None:
+        _vec(offsets, "bias offsets", B + 1)
+        nb = tokens.numel() if isinstance(tokens, torch.Tensor) else -1
+        _vec(tokens, "bias tokens", nb)
+        _vec(values, "bias values", nb)
+    M = 0
+    if mask is not None:
+        if not isinstance(mask, torch.Tensor) or mask.dim() != 3 or tuple(mask.shape[1:]) != (R, -(-V // 32)):
+            raise ValueError(f"mask must be [M, {R}, {-(-V // 32)}]")
+        M = mask.shape[0]
+    elif mask_index is not None:
+        raise ValueError("mask_index needs a mask")
+    _shape(out, "out", (B, R, V))
+    _int32(B=B, R=R, V=V, H=H, nb=nb, M=M)
+    _dev(logits, "logits", _FLOATS, 3)
+    i32 = dict(draft_tokens=draft_tokens, lengths=lengths, history=history, history_len=history_len,
+               prompt_len=prompt_len, mask_index=mask_index, status=status)
+    f32 = dict(repetition=repetition, frequency=frequency, presence=presence)
+    if bias is not None:
+        i32.update(bias_offsets=offsets, bias_tokens=tokens)
+        f32.update(bias_values=values)
+    for name, t in i32.items():
+        _dev(t, name, torch.int32)
+    for name, t in f32.items():
+        _dev(t, name, torch.float32)
+    _dev(mask, "mask", (torch.int32, torch.uint32) if hasattr(torch, "uint32") else torch.int32)
+    _dev(out, "out", logits.dtype)
+    dev = logits.device
+    _on(dev, mask=mask, out=out, **i32, **f32)
+    if in_place and out is not None:
+        raise ValueError("pass out or in_place, not both")
+    mine = []
+    if in_place:
+        out = logits
+    elif out is None:
+        out = torch.empty_like(logits)
+        mine.append(out)
+    if status is None:
+        status = torch.empty(B, dtype=torch.int32, device=dev)
+        mine.append(status)
+    # an empty list has no storage to point to: any address that is not NULL will do, none of it is read
+    if nb == 0 and bias is not None:
+        tokens, values = offsets, offsets
+    code = _launch_on(dev, stream, mine, lambda sp: lib.spec_adjust_logits(
+        B, R, V, _logit_dtype(logits), _ptr(logits), G, _ptr(draft_tokens) if G else None, _ptr(lengths), _ptr(history), H,
+        _ptr(history_len), _ptr(prompt_len), _ptr(repetition), _ptr(frequency), _ptr(presence), _ptr(offsets),
+        _ptr(tokens), _ptr(values), nb, _ptr(mask), M, _ptr(mask_index), _ptr(out), _ptr(status), sp))
+    _check("spec_adjust_logits", code)
+    return dict(logits=out, status=status)

@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libspecverify.so")
 
 SOURCES = ["verify.hip", "emit.hip", "schedule.hip", "overlap.hip", "draft.hip", "calibrate.hip", "teacher.hip",
-           "distill.hip", "xent.hip", "measure.hip", "api.cpp"]
+           "distill.hip", "xent.hip", "head.hip", "logits.hip", "adjust.hip", "measure.hip", "api.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950",

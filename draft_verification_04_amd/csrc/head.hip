@@ -1,0 +1,470 @@
+// The norm in front of the vocabulary head on gfx950, its gradients, and the head's weight in 8 bits.
+//
+//   h = x + residual;  rstd = 1 / sqrt(mean(h^2) + eps);  y = h rstd w
+//   8 bits: amax over each 128 of a row, at least 2^-100; scale = amax / 448; code = e4m3(y 448 / amax)
+//   gradients, with xh = h rstd and g = grad_y w:
+//     grad_x = rstd (g - xh mean(g xh)) + grad_h;  grad_w = sum over the rows of grad_y xh
+//   weight: the same codes with an amax for each block of 128 x 128
+//
+// All of them are bound by memory: a row is read once into registers (16 values a thread at most, 8 of them in a
+// row), and everything else is done there.  16 lanes hold 128 values, one group of the scales: its amax is a
+// reduction within a DPP row.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <tuple>
+#include <utility>
+
+#include "common.hpp"
+#include "rowseg.hpp"
+#include "spec_verify.h"
+#include "xent_plan.hpp"
+
+namespace spec {
+namespace {
+
+typedef unsigned int v2u32 __attribute__((ext_vector_type(2)));
+
+constexpr float kCodeMax = 448.f;        // e4m3's largest value
+constexpr float kAmaxFloor = 0x1p-100f;  // so that 448 / amax stays in range (and a block of zeros has a scale)
+constexpr int kBackGroups = 1024;        // workgroups of the backward kernel, at most
+constexpr int kSumSlices = 32, kSumCols = 32;
+
+struct NormArgs {
+  const void* x;
+  const void* residual;
+  const void* w;
+  void* h;
+  void* y;          // in the inputs' type, or
+  uint8_t* codes;   // [N, d]
+  float* scales;    // [N, groups]
+  float* rstd;
+  int d, groups;
+  float eps;
+};
+
+struct BackArgs {
+  const void* grad_y;
+  const void* h;
+  const void* w;
+  const float* rstd;
+  const void* grad_h;
+  void* grad_x;
+  float* part;      // [gridDim.x, d], or NULL
+  int N, d;
+};
+
+// 8 consecutive values of a row from index c; zeros past d.  VEC: the rows are multiples of 16 bytes.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void load8(const void* p, size_t row, int c, int d, float (&v)[8]) {
+#pragma unroll
+  for (int x = 0; x < 8; ++x) v[x] = 0.f;
+  if constexpr (VEC && BF16) {
+    if (c < d) {
+      const v4u32 t = *reinterpret_cast<const v4u32*>(reinterpret_cast<const uint16_t*>(p) + row + c);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        v[2 * x] = bf16_lo(t[x]);
+        v[2 * x + 1] = bf16_hi(t[x]);
+      }
+    }
+  } else if constexpr (VEC) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (c + 4 * q >= d) break;
+      const v4u32 t = *reinterpret_cast<const v4u32*>(reinterpret_cast<const float*>(p) + row + c + 4 * q);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[4 * q + x] = __uint_as_float(t[x]);
+    }
+  } else {
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      if (c + x < d) v[x] = load_elem<BF16>(p, (int64_t)(row + c + x));
+  }
+}
+
+__device__ __forceinline__ uint32_t bf16_bits(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
+
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void store8(void* p, size_t row, int c, int d, const float (&v)[8]) {
+  if constexpr (VEC && BF16) {
+    if (c < d) {
+      v4u32 t;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) t[x] = bf16_bits(v[2 * x]) | bf16_bits(v[2 * x + 1]) << 16;
+      *reinterpret_cast<v4u32*>(reinterpret_cast<uint16_t*>(p) + row + c) = t;
+    }
+  } else if constexpr (VEC) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (c + 4 * q >= d) break;
+      *reinterpret_cast<v4u32*>(reinterpret_cast<float*>(p) + row + c + 4 * q) =
+          v4u32{__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                __float_as_uint(v[4 * q + 3])};
+    }
+  } else {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      if (c + x >= d) break;
+      if constexpr (BF16) reinterpret_cast<uint16_t*>(p)[row + c + x] = (uint16_t)bf16_bits(v[x]);
+      else reinterpret_cast<float*>(p)[row + c + x] = v[x];
+    }
+  }
+}
+
+// Sum over the workgroup, in wave order; `sh` holds a word per wave and is free until the next but one call
+// where the callers alternate between two.
+template <int T>
+__device__ __forceinline__ float block_sum(float x, float* sh) {
+  x = wave_reduce(x, [](float a, float b) { return a + b; });
+  if constexpr (T == SPEC_WAVE) return x;
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
+  __syncthreads();
+  float s = sh[0];
+#pragma unroll
+  for (int w = 1; w < T / SPEC_WAVE; ++w) s += sh[w];
+  return s;
+}
+
+// Largest magnitude as its bits: NaN above infinity above every finite value.
+template <int T>
+__device__ __forceinline__ uint32_t block_amax(uint32_t x, float* sh) {
+  x = wave_reduce(x, [](uint32_t a, uint32_t b) { return max(a, b); });
+  if constexpr (T == SPEC_WAVE) return x;
+  uint32_t* s = reinterpret_cast<uint32_t*>(sh);
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
+  __syncthreads();
+  uint32_t m = s[0];
+#pragma unroll
+  for (int w = 1; w < T / SPEC_WAVE; ++w) m = max(m, s[w]);
+  return m;
+}
+
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// Four values in [-448 (1 + 2^-23), 448 (1 + 2^-23)] (or NaN) as e4m3, ties to even.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+}
+
+template <bool BF16, bool VEC, bool Q8, int T, int K>
+__global__ __launch_bounds__(T) void norm_kernel(NormArgs a) {
+  __shared__ float sh[2][T / SPEC_WAVE];
+  const int tid = threadIdx.x, d = a.d;
+  const size_t row = (size_t)blockIdx.x * d;
+  float v[K][8], w[K][8];
+#pragma unroll
+  for (int k = 0; k < K; ++k) load8<BF16, VEC>(a.x, row, (k * T + tid) * 8, d, v[k]);
+  if (a.residual) {
+    float r[K][8];
+#pragma unroll
+    for (int k = 0; k < K; ++k) load8<BF16, VEC>(a.residual, row, (k * T + tid) * 8, d, r[k]);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[k][x] += r[k][x];
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) load8<BF16, VEC>(a.w, 0, (k * T + tid) * 8, d, w[k]);
+  // the norm is taken of the sum in fp32; only what is stored of it is rounded
+  if (a.h)
+#pragma unroll
+    for (int k = 0; k < K; ++k) store8<BF16, VEC>(a.h, row, (k * T + tid) * 8, d, v[k]);
+  float ss = 0.f;
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int x = 0; x < 8; ++x) ss += v[k][x] * v[k][x];
+  ss = block_sum<T>(ss, sh[0]);
+  float rs = 1.f / sqrtf(ss / (float)d + a.eps), rstd = rs;
+  if (!(ss >= 0x1p-90f && ss <= 0x1p120f)) {
+    // the squares left fp32's range (or nearly): taken again of the row scaled by a power of two
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int x = 0; x < 8; ++x) m = max(m, magnitude(v[k][x]));
+    m = block_amax<T>(m, sh[1]);
+    if (m != 0 && m < 0x7f800000u) {
+      const int e = ilogbf(__uint_as_float(m));
+      ss = 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          v[k][x] = ldexpf(v[k][x], -e);
+          ss += v[k][x] * v[k][x];
+        }
+      __syncthreads();   // sh[0] and sh[1] are read
+      ss = block_sum<T>(ss, sh[0]);
+      const double r = 1.0 / sqrt(ldexp((double)ss / d, 2 * e) + (double)a.eps);
+      rs = (float)ldexp(r, e);
+      rstd = (float)r;
+    }
+  }
+  if (a.rstd && tid == 0) a.rstd[blockIdx.x] = rstd;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * T + tid) * 8;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) v[k][x] = v[k][x] * rs * w[k][x];
+    if constexpr (!Q8) {
+      store8<BF16, VEC>(a.y, row, c, d, v[k]);
+    } else {
+      uint32_t m = __float_as_uint(kAmaxFloor);
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (c < d) m = max(m, magnitude(v[k][x]));   // past the row: 0, but 0 * inf where the row's norm is
+      auto mx = [](uint32_t p, uint32_t q) { return max(p, q); };
+      m = mx(m, dpp_move<dpp::kQuadXor1>(m, m));
+      m = mx(m, dpp_move<dpp::kQuadXor2>(m, m));
+      m = mx(m, dpp_move<dpp::kRowHalfMirror>(m, m));
+      m = mx(m, dpp_move<dpp::kRowMirror>(m, m));
+      const float amax = __uint_as_float(m), r = kCodeMax / amax;
+      if (c < d) {
+        v2u32 q;
+        q.x = codes4(v[k][0] * r, v[k][1] * r, v[k][2] * r, v[k][3] * r);
+        q.y = codes4(v[k][4] * r, v[k][5] * r, v[k][6] * r, v[k][7] * r);
+        *reinterpret_cast<v2u32*>(a.codes + row + c) = q;
+        if ((tid & 15) == 0) a.scales[(size_t)blockIdx.x * a.groups + (c >> 7)] = amax / kCodeMax;
+      }
+    }
+  }
+}
+
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ...; the weight and its gradient's share stay in registers.
+template <bool BF16, bool VEC, int T, int K>
+__global__ __launch_bounds__(T) void norm_backward_kernel(BackArgs a) {
+  __shared__ float sh[2][T / SPEC_WAVE];
+  const int tid = threadIdx.x, d = a.d;
+  float w[K][8], dw[K][8] = {};
+#pragma unroll
+  for (int k = 0; k < K; ++k) load8<BF16, VEC>(a.w, 0, (k * T + tid) * 8, d, w[k]);
+  int turn = 0;
+  for (int n = blockIdx.x; n < a.N; n += gridDim.x, turn ^= 1) {
+    const size_t row = (size_t)n * d;
+    const float rstd = a.rstd[n];
+    float gy[K][8], xh[K][8], gh[K][8];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      load8<BF16, VEC>(a.grad_y, row, (k * T + tid) * 8, d, gy[k]);
+      load8<BF16, VEC>(a.h, row, (k * T + tid) * 8, d, xh[k]);
+      // single values take an address each: behind the sum, or the registers do not do
+      if (VEC && a.grad_h) load8<BF16, VEC>(a.grad_h, row, (k * T + tid) * 8, d, gh[k]);
+    }
+    float dot = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        xh[k][x] *= rstd;
+        dw[k][x] += gy[k][x] * xh[k][x];
+        gy[k][x] *= w[k][x];
+        dot += gy[k][x] * xh[k][x];
+      }
+    dot = block_sum<T>(dot, sh[turn]) / (float)d;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (!VEC && a.grad_h) load8<BF16, VEC>(a.grad_h, row, (k * T + tid) * 8, d, gh[k]);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        gy[k][x] = rstd * (gy[k][x] - xh[k][x] * dot);
+        if (a.grad_h) gy[k][x] += gh[k][x];
+      }
+      store8<BF16, VEC>(a.grad_x, row, (k * T + tid) * 8, d, gy[k]);
+    }
+  }
+  if (a.part)
+#pragma unroll
+    for (int k = 0; k < K; ++k) store8<false, VEC>(a.part, (size_t)blockIdx.x * d, (k * T + tid) * 8, d, dw[k]);
+}
+
+// grad_w: the workgroups' shares in order, in fp64, rounded once.
+template <bool BF16>
+__global__ __launch_bounds__(kSumSlices* kSumCols) void norm_weight_kernel(const float* part, int P, int d, void* out) {
+  __shared__ double sh[kSumSlices][kSumCols];
+  const int s = threadIdx.x / kSumCols, c = threadIdx.x % kSumCols, col = blockIdx.x * kSumCols + c;
+  double sum = 0.0;
+  if (col < d)
+#pragma unroll 8
+    for (int p = s; p < P; p += kSumSlices) sum += (double)part[(size_t)p * d + col];
+  sh[s][c] = sum;
+  __syncthreads();
+  if (s == 0 && col < d) {
+#pragma unroll
+    for (int q = 1; q < kSumSlices; ++q) sum += sh[q][c];
+    if constexpr (BF16) reinterpret_cast<uint16_t*>(out)[col] = (uint16_t)bf16_bits((float)sum);
+    else reinterpret_cast<float*>(out)[col] = (float)sum;
+  }
+}
+
+// A block of 128 x 128 per workgroup: 16 lanes take 128 columns of a row, 16 rows at a time.
+template <bool BF16>
+__global__ __launch_bounds__(256) void quantize_kernel(const void* w, int V, int d, int groups, uint8_t* codes,
+                                                       float* scales) {
+  __shared__ float sh[4];
+  const int tid = threadIdx.x, g = blockIdx.x, c = g * 128 + (tid & 15) * 8;
+  const int r0 = blockIdx.y * 128 + (tid >> 4);
+  float v[8][8];
+  uint32_t m = __float_as_uint(kAmaxFloor);
+#pragma unroll
+  for (int u = 0; u < 8; ++u) load8<BF16, true>(w, (size_t)min(r0 + 16 * u, V - 1) * d, c, d, v[u]);
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+#pragma unroll
+    for (int x = 0; x < 8; ++x) m = max(m, magnitude(v[u][x]));
+  const float amax = __uint_as_float(block_amax<256>(m, sh));
+  // w 448 / amax to the nearest fp32 (a quotient of two bf16 values often lies halfway between two codes, where the
+  // last bit decides): both scaled to amax in [1, 2), one correction of the product with the reciprocal
+  const int e = ilogbf(amax);
+  const float as = ldexpf(amax, -e), r = kCodeMax / as;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    float q[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const float ws = ldexpf(v[u][x], -e), p = ws * r;
+      q[x] = fmaf(fmaf(-p, as, ws * kCodeMax), 1.f / as, p);
+    }
+    if (r0 + 16 * u < V && c < d)
+      *reinterpret_cast<v2u32*>(codes + (size_t)(r0 + 16 * u) * d + c) =
+          v2u32{codes4(q[0], q[1], q[2], q[3]), codes4(q[4], q[5], q[6], q[7])};
+  }
+  if (tid == 0) scales[(size_t)blockIdx.y * groups + g] = amax / kCodeMax;
+}
+
+// ---- host -------------------------------------------------------------------
+
+// Threads and vectors per thread of a row of d values: 16 values a thread, or 8 where a wave holds the row so.
+template <class F>
+void with_shape(int d, F f) {
+  if (d <= 512) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+  else if (d <= 1024) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+  else if (d <= 2048) f(std::integral_constant<int, 128>{}, std::integral_constant<int, 2>{});
+  else if (d <= 4096) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+  else if (d <= 8192) f(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
+  else f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+}
+
+template <class F>
+void with_type(int dtype, bool vec, F f) {
+  if (dtype == SPEC_BF16) {
+    if (vec) f(std::true_type{}, std::true_type{});
+    else f(std::true_type{}, std::false_type{});
+  } else {
+    if (vec) f(std::false_type{}, std::true_type{});
+    else f(std::false_type{}, std::false_type{});
+  }
+}
+
+bool norm_ok(int N, int d, int dtype) {
+  return (dtype == SPEC_F32 || dtype == SPEC_BF16) && N >= 1 && N <= SPEC_MAX_HEAD_ROWS && d >= 1 &&
+         d <= SPEC_MAX_HEAD_WIDTH;
+}
+
+bool vector_rows(int d, int dtype) { return d * (dtype == SPEC_BF16 ? 2 : 4) % 16 == 0; }
+
+int back_groups(int N) { return N < kBackGroups ? N : kBackGroups; }
+
+int32_t launched() { return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ERR_HIP; }
+
+}  // namespace
+}  // namespace spec
+
+using namespace spec;
+
+extern "C" int32_t spec_head_norm(int32_t N, int32_t d, int32_t dtype, const void* x, const void* residual,
+                                  const void* weight, float eps, void* h_out, void* y_out, uint8_t* codes_out,
+                                  float* scales_out, float* rstd_out, void* stream) {
+  if (!norm_ok(N, d, dtype) || !(eps >= 0.f) || !(eps < INFINITY)) return SPEC_ERR_INVALID_ARG;
+  if (!x || !weight || (residual && !h_out) || (!y_out == !codes_out) || (!codes_out != !scales_out))
+    return SPEC_ERR_INVALID_ARG;
+  for (const void* p : {x, residual, weight, (const void*)h_out, (const void*)y_out, (const void*)codes_out})
+    if (!aligned16(p)) return SPEC_ERR_INVALID_ARG;
+  if (codes_out && d % 16) return SPEC_ERR_INVALID_ARG;
+  const size_t n = (size_t)N * d, bytes = n * (dtype == SPEC_BF16 ? 2 : 4), wbytes = bytes / N;
+  const size_t groups = (size_t)ceil_div(d, 128), sbytes = N * groups * sizeof(float);
+  // a row is read whole before anything of it is written: h and y may be x or the residual themselves
+  for (auto [p, m, same] : {std::tuple<const void*, size_t, bool>{h_out, bytes, true}, {y_out, bytes, true},
+                            {codes_out, n, false}, {scales_out, sbytes, false}, {rstd_out, N * sizeof(float), false}}) {
+    if (!(same && p == x) && overlap(p, m, x, bytes)) return SPEC_ERR_INVALID_ARG;
+    if (!(same && p == residual) && overlap(p, m, residual, bytes)) return SPEC_ERR_INVALID_ARG;
+    if (overlap(p, m, weight, wbytes)) return SPEC_ERR_INVALID_ARG;
+  }
+  const std::pair<const void*, size_t> outs[] = {{h_out, bytes}, {y_out, bytes}, {codes_out, n}, {scales_out, sbytes},
+                                                 {rstd_out, N * sizeof(float)}};
+  for (int i = 0; i < 5; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i].first, outs[i].second, outs[j].first, outs[j].second)) return SPEC_ERR_INVALID_ARG;
+  const NormArgs a{x, residual, weight, h_out, y_out, codes_out, scales_out, rstd_out, d, (int)groups, eps};
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  with_shape(d, [&](auto T, auto K) {
+    with_type(dtype, vector_rows(d, dtype), [&](auto BF, auto VEC) {
+      if (!codes_out)
+        hipLaunchKernelGGL((norm_kernel<BF(), VEC(), false, T(), K()>), dim3(N), dim3(T()), 0, s, a);
+      else if constexpr (VEC())   // multiples of 16 values
+        hipLaunchKernelGGL((norm_kernel<BF(), true, true, T(), K()>), dim3(N), dim3(T()), 0, s, a);
+    });
+  });
+  return launched();
+}
+
+extern "C" size_t spec_head_norm_backward_workspace_size(int32_t N, int32_t d) {
+  return norm_ok(N, d, SPEC_F32) ? round256((size_t)back_groups(N) * round_to(d, 4) * sizeof(float)) : 0;
+}
+
+extern "C" int32_t spec_head_norm_backward(int32_t N, int32_t d, int32_t dtype, const void* grad_y, const void* h,
+                                           const void* weight, const float* rstd, const void* grad_h, void* grad_x,
+                                           void* grad_weight, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!norm_ok(N, d, dtype)) return SPEC_ERR_INVALID_ARG;
+  if (!grad_y || !h || !weight || !rstd || !grad_x) return SPEC_ERR_INVALID_ARG;
+  for (const void* p : {grad_y, h, weight, grad_h, (const void*)grad_x, (const void*)grad_weight})
+    if (!aligned16(p)) return SPEC_ERR_INVALID_ARG;
+  if (grad_weight && (!workspace || !aligned256(workspace) || workspace_bytes < spec_head_norm_backward_workspace_size(N, d)))
+    return SPEC_ERR_WORKSPACE;
+  const size_t bytes = (size_t)N * d * (dtype == SPEC_BF16 ? 2 : 4), wbytes = bytes / N;
+  for (const void* p : {grad_y, h, grad_h})   // a row is read before its gradient is written
+    if (p != grad_x && overlap(grad_x, bytes, p, bytes)) return SPEC_ERR_INVALID_ARG;
+  if (overlap(grad_x, bytes, weight, wbytes) || overlap(grad_x, bytes, rstd, N * sizeof(float)) ||
+      overlap(grad_x, bytes, grad_weight, wbytes))
+    return SPEC_ERR_INVALID_ARG;
+  for (auto [p, m] : {std::pair<const void*, size_t>{grad_y, bytes}, {h, bytes}, {grad_h, bytes}, {weight, wbytes},
+                      {rstd, N * sizeof(float)}})
+    if (overlap(grad_weight, wbytes, p, m)) return SPEC_ERR_INVALID_ARG;
+  const int P = back_groups(N);
+  const BackArgs a{grad_y, h, weight, rstd, grad_h, grad_x, grad_weight ? reinterpret_cast<float*>(workspace) : nullptr,
+                   N, d};
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  with_shape(d, [&](auto T, auto K) {
+    with_type(dtype, vector_rows(d, dtype), [&](auto BF, auto VEC) {
+      hipLaunchKernelGGL((norm_backward_kernel<BF(), VEC(), T(), K()>), dim3(P), dim3(T()), 0, s, a);
+    });
+  });
+  if (grad_weight) {
+    const dim3 grid(ceil_div(d, kSumCols)), block(kSumSlices * kSumCols);
+    if (dtype == SPEC_BF16) hipLaunchKernelGGL(norm_weight_kernel<true>, grid, block, 0, s, a.part, P, d, grad_weight);
+    else hipLaunchKernelGGL(norm_weight_kernel<false>, grid, block, 0, s, a.part, P, d, grad_weight);
+  }
+  return launched();
+}
+
+extern "C" int32_t spec_head_quantize(int32_t V, int32_t d, int32_t dtype, const void* weight, uint8_t* codes_out,
+                                      float* scales_out, void* stream) {
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
+  if (V < 1 || V > SPEC_MAX_V || d < 16 || d > SPEC_MAX_HEAD_WIDTH || d % 16) return SPEC_ERR_INVALID_ARG;
+  if (!weight || !codes_out || !scales_out || !aligned16(weight) || !aligned16(codes_out)) return SPEC_ERR_INVALID_ARG;
+  const size_t n = (size_t)V * d, bytes = n * (dtype == SPEC_BF16 ? 2 : 4);
+  const size_t sbytes = (size_t)ceil_div(V, 128) * ceil_div(d, 128) * sizeof(float);
+  if (overlap(codes_out, n, weight, bytes) || overlap(scales_out, sbytes, weight, bytes) ||
+      overlap(codes_out, n, scales_out, sbytes))
+    return SPEC_ERR_INVALID_ARG;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const dim3 grid(ceil_div(d, 128), ceil_div(V, 128));
+  if (dtype == SPEC_BF16)
+    hipLaunchKernelGGL(quantize_kernel<true>, grid, dim3(256), 0, s, weight, V, d, (int)grid.x, codes_out, scales_out);
+  else
+    hipLaunchKernelGGL(quantize_kernel<false>, grid, dim3(256), 0, s, weight, V, d, (int)grid.x, codes_out, scales_out);
+  return launched();
+}

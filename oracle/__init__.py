@@ -31,6 +31,9 @@ from the DSpark pages:
                        calibration);
   * `teacher_topk`, `distill_loss`, `head_xent` -- the drafter's training
                        losses and their gradients (DSpark paper, §3.3);
+  * `head_norm`, `quantize`, `head_logits`, `adjust_logits` -- from the last
+                       hidden state to the logits: the norm and its gradients,
+                       numbers in 8 bits, their product, penalties and masks;
   * `philox`        -- the counter-based generator the draws come from
                        (Philox4x64-10, Salmon et al., SC'11).
 
@@ -58,6 +61,17 @@ from .overlap import overlap_mass  # noqa: F401
 from .drafting import markov_draft, round_bf16  # noqa: F401
 from .calibration import ece, sts_apply, sts_fit  # noqa: F401
 from .training import STATUS_BAD_LIST, distill_loss, head_xent, teacher_topk  # noqa: F401
+from .head import (  # noqa: F401
+    STATUS_BAD_MASK,
+    STATUS_BAD_PENALTY,
+    adjust_logits,
+    e4m3,
+    e4m3_step,
+    head_logits,
+    head_norm,
+    head_norm_grad,
+    quantize,
+)
 from .scheduling import (  # noqa: F401
     capacity,
     survival,

@@ -1,0 +1,268 @@
+"""GPU parity of spec_adjust_logits with the fp64 oracle.
+
+Tolerances (u = 2^-24): the repetition's quotient or product, frequency * count, two differences and the bias's sum are
+an fp32 rounding each: 5 u of the largest magnitude on the way (the oracle's `mass`), and half a step of the storage
+type.  Values that no penalty, bias or mask reaches are the same bits.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+import oracle
+
+DEV = "cuda:0"
+U = 2.0 ** -24 * (1 + 2.0 ** -10)
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def sv():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import draft_verification_04_amd as m
+    m.load_library()
+    return m
+
+
+def _bits(t):
+    return t.view(torch.int16 if t.dtype == torch.bfloat16 else torch.int32).cpu().numpy()
+
+
+def _check(sv, z, toks=None, L=None, **kw):
+    """Out of place (around a filled buffer) and in place against the oracle; returns the result."""
+    ref = oracle.adjust_logits(z, toks, L, **kw)
+    B, R, V = z.shape
+    G = 0 if toks is None else toks.shape[1]
+    live = np.zeros((B, R), dtype=bool)
+    for b in range(B):
+        if ref["status"][b] == 0:
+            live[b, :(G if L is None else int(L[b])) + R - G] = True
+    out = torch.full_like(z, 7.0)
+    here = z.clone()
+    o = sv.adjust_logits(z, toks, L, out=out, **kw)
+    i = sv.adjust_logits(here, toks, L, in_place=True, **kw)
+    torch.cuda.synchronize()
+    assert o["logits"] is out and i["logits"] is here
+    for s in (o["status"], i["status"]):
+        assert s.tolist() == ref["status"].tolist(), (s.tolist(), ref["status"].tolist())
+    assert (out.float().cpu().numpy()[~live] == 7).all()
+    assert np.array_equal(_bits(here)[~live], _bits(z)[~live])
+    assert np.array_equal(_bits(here)[live], _bits(out)[live])
+    same = live[..., None] & ~ref["touched"]
+    assert np.array_equal(_bits(out)[same], _bits(z)[same])
+    g, r = out.float().cpu().double().numpy()[live], ref["logits"][live]
+    r = np.where(np.abs(r) > torch.finfo(z.dtype).max, np.sign(r) * np.inf, r)
+    fin = np.isfinite(r)
+    assert np.array_equal(g[~fin], r[~fin], equal_nan=True)
+    err = np.abs(g[fin] - r[fin])
+    tol = 5 * U * ref["mass"][live][fin] + torch.finfo(z.dtype).eps / 2 * (1 + 2 ** -10) * np.abs(r[fin]) + 1e-40
+    assert (err <= tol).all(), (err / tol).max()
+    return out
+
+
+def _inputs(seed, B, G, R, V, H, dtype, ragged=True):
+    g = torch.Generator().manual_seed(seed)
+    rand = lambda *s: torch.rand(s, generator=g)
+    z = (3 * torch.randn((B, R, V), generator=g)).to(DT[dtype]).to(DEV)
+    text = lambda *s: (V * rand(*s) ** 3).to(torch.int32).clamp(max=V - 1)
+    c = lambda t: t.to(DEV)
+    hist = text(B, H) if H else None
+    kw = dict(history=None, history_len=None, prompt_len=None)
+    if H:
+        hist[rand(B, H) < 0.05] = -1
+        hl = (rand(B) * (H + 1)).to(torch.int32)
+        hl[0] = H
+        kw = dict(history=c(hist), history_len=c(hl), prompt_len=c((hl * rand(B)).to(torch.int32)))
+    plain = rand(B) < 0.2
+    kw.update(repetition=c(torch.where(plain, 1.0, 0.7 + 0.8 * rand(B))),
+              frequency=c(torch.where(plain, 0.0, 2 * rand(B) - 1)), presence=c(torch.where(plain, 0.0, 2 * rand(B) - 1)))
+    toks = c(text(B, G)) if G else None
+    L = c(torch.randint(0, G + 1, (B,), generator=g, dtype=torch.int32)) if ragged and G else None
+    return z, toks, L, kw, g
+
+
+def _bias(g, B, V, most):
+    n = torch.randint(0, most + 1, (B,), generator=g, dtype=torch.int32)
+    off = torch.zeros(B + 1, dtype=torch.int32)
+    off[1:] = n.cumsum(0)
+    m = int(off[-1])
+    vals = torch.randn(m, generator=g) * 4
+    vals[torch.rand(m, generator=g) < 0.1] = -math.inf
+    return off.to(DEV), torch.randint(0, V, (m,), generator=g, dtype=torch.int32).to(DEV), vals.to(DEV)
+
+
+def _mask(g, M, R, V, allow):
+    on = torch.rand((M, R, -(-V // 32) * 32), generator=g) < torch.tensor(allow)[torch.arange(M) % len(allow)][:, None, None]
+    w = (on.view(M, R, -1, 32).long() << torch.arange(32)).sum(3)
+    return torch.where(w >= 2 ** 31, w - 2 ** 32, w).to(torch.int32).to(DEV)
+
+
+SHAPES = [(1, 0, 1, 1, 0), (1, 0, 1, 1000, 5), (3, 0, 1, 33, 100), (2, 1, 1, 31, 7), (2, 1, 2, 257, 50), (4, 3, 3, 1003, 300),
+          (5, 3, 4, 8191, 64), (3, 4, 5, 8192, 1000), (2, 2, 3, 8193, 1000), (2, 16, 17, 20011, 2000), (2, 64, 64, 500, 90),
+          (1, 64, 65, 301, 0), (9, 7, 8, 5003, 400), (2, 2, 3, 151936, 3000), (1, 3, 4, 262144, 9000), (300, 1, 2, 130, 3)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_adjust(sv, shape, dtype):
+    B, G, R, V, H = shape
+    z, toks, L, kw, g = _inputs(V + B, B, G, R, V, H, dtype)
+    allow = [0.5, 0.01, 0.99, 1.0, 0.0]
+    idx = torch.randint(-1, 3, (B,), generator=g, dtype=torch.int32).to(DEV)
+    for name, more in (("penalties", {}), ("bias", dict(bias=_bias(g, B, V, 40))),
+                       ("masks", dict(mask=_mask(g, B, R, V, allow))),
+                       ("all", dict(bias=_bias(g, B, V, 9), mask=_mask(g, 3, R, V, allow), mask_index=idx))):
+        print(f"adjust {shape} {dtype} {name}", flush=True)
+        _check(sv, z, toks, L, **kw, **more)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_single_arguments(sv, dtype):
+    """Each array alone, the others left out."""
+    z, toks, L, kw, g = _inputs(2, 4, 3, 4, 611, 200, dtype, ragged=False)
+    h = kw["history"]
+    print("nothing", flush=True)
+    assert np.array_equal(_bits(_check(sv, z, toks)), _bits(z))
+    for k in ("repetition", "frequency", "presence"):
+        print(k, flush=True)
+        _check(sv, z, toks, **{k: kw[k]})                          # the drafts alone
+        _check(sv, z, toks, **{k: kw[k], "history": h})            # all of it output
+        _check(sv, z, toks, **{k: kw[k], "history": h, "prompt_len": kw["prompt_len"] * 0 + 200})
+    e = torch.zeros(0, dtype=torch.int32, device=DEV)
+    none = (torch.zeros(5, dtype=torch.int32, device=DEV), e, e.float())
+    assert np.array_equal(_bits(_check(sv, z, toks, bias=none)), _bits(z))
+    _check(sv, z, toks, **dict(kw, history=h[:, :0].contiguous(), history_len=None, prompt_len=None))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_odd_values(sv, dtype):
+    """Infinities, NaN, zeros of either sign and the type's lowest value under every adjustment; rows whose mask
+    leaves nothing; a row masked with the lowest value everywhere; one token all through a long history."""
+    B, G, V, H = 3, 2, 700, 5000
+    z, toks, L, kw, g = _inputs(3, B, G, G + 1, V, H, dtype, ragged=False)
+    odd = torch.tensor([math.inf, -math.inf, math.nan, 0.0, -0.0, torch.finfo(DT[dtype]).min, torch.finfo(DT[dtype]).max, 1e-40])
+    z[:, :, :640] = odd.repeat(80).to(DT[dtype]).to(DEV)
+    z[1, 1] = torch.finfo(DT[dtype]).min
+    kw["history"][2] = 9
+    kw["repetition"][:] = torch.tensor([1.25, 3.0, 0.5])
+    kw["frequency"][:] = torch.tensor([0.5, -0.75, 1e-3])
+    off, t, v = _bias(g, B, V, 60)
+    m = _mask(g, B, G + 1, V, [0.5])
+    m[0, 1] = 0
+    for more in ({}, dict(bias=(off, t, v)), dict(mask=m), dict(bias=(off, t, v), mask=m)):
+        print(f"odd {dtype} {sorted(more)}", flush=True)
+        out = _check(sv, z, toks, **kw, **more)
+    assert torch.isneginf(out[0, 1]).all()
+
+
+def test_a_token_listed_twice(sv):
+    """The last entry of a token counts, whichever workgroup's thread comes first; so over many entries."""
+    V, n = 900, 20000
+    g = torch.Generator().manual_seed(4)
+    z = torch.randn((2, 1, V), generator=g).to(DEV)
+    t = torch.randint(0, 40, (n,), generator=g, dtype=torch.int32).to(DEV)
+    off = torch.tensor([0, 13000, n], dtype=torch.int32, device=DEV)
+    for _ in range(5):
+        _check(sv, z, None, None, bias=(off, t, torch.randn(n, generator=g).to(DEV)))
+
+
+def test_long_histories(sv):
+    z, toks, L, kw, g = _inputs(5, 3, 3, 4, 40000, 120001, "bf16")
+    _check(sv, z, toks, L, **kw)
+
+
+def test_status(sv):
+    """Each kind of bad data, on its own request; their rows stay as they are, the others are adjusted.  What no
+    adjusted row needs is not looked at."""
+    B, G, V, H = 24, 3, 9001, 70
+    z, toks, _, kw, g = _inputs(6, B, G, G + 1, V, H, "f32", ragged=False)
+    for k in ("repetition", "frequency", "presence"):
+        kw[k][:] = 1.25
+    kw["history_len"][:], kw["prompt_len"][:] = H, 20
+    L = torch.full((B,), G, dtype=torch.int32, device=DEV)
+    off = torch.arange(B + 1, dtype=torch.int32, device=DEV) * 2
+    t = torch.arange(2 * B, dtype=torch.int32, device=DEV)
+    v = torch.ones(2 * B, device=DEV)
+    idx = torch.full((B,), -1, dtype=torch.int32, device=DEV)
+    mask = _mask(g, 2, G + 1, V, [0.5])
+    L[1], L[2] = -1, G + 1
+    kw["history_len"][3], kw["history_len"][4], kw["prompt_len"][5], kw["prompt_len"][6] = -1, H + 1, -1, H + 1
+    kw["history"][7, 5], kw["history"][8, 69], toks[9, 2], toks[10, 0] = V, -2, V, -1
+    kw["repetition"][11], kw["repetition"][12], kw["repetition"][13] = 0.0, -1.0, math.nan
+    kw["frequency"][14], kw["presence"][15] = math.inf, math.nan
+    t[32], t[35], idx[18], idx[19] = V, -1, 2, -2          # requests 16 and 17
+    toks[20, 2], L[20] = V, 2                              # the draft behind the last adjusted row
+    kw["history"][21, 60], kw["history_len"][21] = V, 60
+    toks[22, 0], kw["history"][22, 0] = V, V               # neutral penalties: neither is read
+    kw["repetition"][22], kw["frequency"][22], kw["presence"][22] = 1.0, 0.0, 0.0
+    out = _check(sv, z, toks, L, **kw, bias=(off, t, v), mask=mask, mask_index=idx)
+    st = sv.adjust_logits(z, toks, L, out=out, **kw, bias=(off, t, v), mask=mask, mask_index=idx)["status"].tolist()
+    assert st == [0, 8, 8, 8, 8, 8, 8, 1, 1, 1, 1, 512, 512, 512, 512, 512, 1, 1, 1024, 1024, 0, 0, 0, 0]
+    off[5], off[6], off[10] = 11, 9, 2 * B + 1
+    _check(sv, z, toks, L, **kw, bias=(off, t, v))
+
+
+def test_draft_rows_match_target_rows(sv):
+    """gamma rows and gamma + 1 rows of the same blocks agree on the rows that both have."""
+    z, toks, L, kw, g = _inputs(7, 5, 4, 5, 3001, 300, "bf16")
+    a = _check(sv, z, toks, L, **kw)
+    b = _check(sv, z[:, :4].contiguous(), toks, L, **kw)
+    for i in range(5):
+        n = int(L[i])
+        assert torch.equal(a[i, :n], b[i, :n])
+
+
+def test_offsets_past_32_bits(sv):
+    """Logits of 4.8 GB: the last request's rows against the same request alone."""
+    B, G, V = 90, 50, 524288
+    z = torch.zeros((B, G + 1, V), dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(8)
+    z[-1] = torch.randn((G + 1, V), generator=g, device=DEV)
+    toks = torch.randint(V, (B, G), generator=g, device=DEV).to(torch.int32)
+    hist = torch.randint(V, (B, 400), generator=g, device=DEV).to(torch.int32)
+    rep = torch.full((B,), 1.5, device=DEV)
+    mask = torch.randint(-2 ** 31, 2 ** 31 - 1, (1, G + 1, V // 32), generator=g, device=DEV).to(torch.int32)
+    idx = torch.full((B,), -1, dtype=torch.int32, device=DEV)
+    idx[-1] = 0
+    one = sv.adjust_logits(z[-1:].clone(), toks[-1:], history=hist[-1:], repetition=rep[-1:], presence=rep[-1:], mask=mask)
+    out = sv.adjust_logits(z, toks, history=hist, repetition=rep, presence=rep, mask=mask, mask_index=idx)
+    torch.cuda.synchronize()
+    assert torch.equal(out["logits"][-1], one["logits"][0])
+    assert int((out["logits"][0, 0] != 0).sum()) == len(hist[0].unique())
+    del out
+    sv.adjust_logits(z, toks, history=hist, repetition=rep, presence=rep, mask=mask, mask_index=idx, in_place=True)
+    torch.cuda.synchronize()
+    assert torch.equal(z[-1], one["logits"][0])
+    assert int((z[0, 0] != 0).sum()) == len(hist[0].unique())
+
+
+def test_streams_and_a_captured_graph(sv):
+    z, toks, L, kw, g = _inputs(9, 20, 4, 5, 30011, 500, "bf16")
+    bias, mask = _bias(g, 20, 30011, 30), _mask(g, 20, 5, 30011, [0.5, 0.02])
+    call = lambda **k: sv.adjust_logits(z, toks, L, **kw, bias=bias, mask=mask, **k)
+    ref = torch.zeros_like(z)
+    call(out=ref)
+    outs = [torch.zeros_like(z) for _ in range(3)]
+    torch.cuda.synchronize()
+    for o in outs:
+        call(out=o, stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    assert all(np.array_equal(_bits(o), _bits(ref)) for o in outs)
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    status = torch.zeros(20, dtype=torch.int32, device=DEV)
+    with torch.cuda.graph(graph, stream=s):
+        call(out=outs[0], status=status)
+    for rep in range(3):
+        outs[0].zero_()
+        call(out=outs[1])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        print(f"graph replay {rep}", flush=True)
+        assert np.array_equal(_bits(outs[0]), _bits(ref)) and status.tolist() == [0] * 20

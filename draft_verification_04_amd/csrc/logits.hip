@@ -25,6 +25,14 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int v8i32 __attribute__((ext_vector_type(8)));
 
+// 16 bytes at any address of the output (its rows start on no boundary where V is odd).
+struct __attribute__((packed, aligned(2))) Any16 {
+  v4u32 v;
+};
+
+#define SPEC_GLOBAL __attribute__((address_space(1)))
+#define SPEC_LDS __attribute__((address_space(3)))
+
 struct LogitArgs {
   const uint8_t* x;    // [N, d]
   const float* sx;     // [N, groups]
@@ -162,12 +170,241 @@ __global__ __launch_bounds__(KW * 64, 2) void logits_rows_kernel(LogitArgs a) {
   }
 }
 
+// Waits until at most N of the wave's loads are in flight and its LDS accesses are done, then the workgroup barrier.
+template <int N>
+__device__ __forceinline__ void wait_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// Tile of block `bid` of `total`: each of the 8 XCDs takes a contiguous run of tiles.
+__device__ __forceinline__ int xcd_tile(int bid, int total) {
+  const int x = bid & 7, i = bid >> 3, q = total >> 3, rem = total & 7;
+  return x < rem ? x * (q + 1) + i : rem * (q + 1) + (x - rem) * q + i;
+}
+
+// Many rows: tiles of BM tokens and BN rows, WM x WN waves.  A step is one block of k: 128 bytes of every row of the
+// tile, brought to LDS directly (16 bytes per lane, chunk c of row r at c ^ (r & 7), so that the 16 rows that an
+// operand read touches fall into different banks), ST - 1 steps ahead, with the rows' scales of the block.
+//
+// A wave goes through its MT operands of the vocabulary one after the other, each against the NT of the rows (a unit:
+// NT matrix instructions); while a unit runs, the unit before it is scaled and added and the operands of the next but
+// one are read from LDS.  The last two units of a step run behind the barrier, with the first reads of the next step.
+template <bool F32, int BM, int BN, int WM, int WN, int ST>
+__global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs a, int ti, int tj) {
+  constexpr int NW = WM * WN, NTHR = NW * 64, MT = BM / WM / 16, NT = BN / WN / 16;
+  constexpr int CA = BM * 8 / NTHR, CB = BN * 8 / NTHR, DMA = CA + CB + 1;
+  constexpr int SCALES = NW * 64, STAGE = (BM + BN) * kStepBytes + SCALES * 4;
+  static_assert(MT >= 4 && BM / WM <= 128 && SCALES >= BN, "tile");
+  __shared__ __attribute__((aligned(128))) char lds_[ST * STAGE];
+  __shared__ float sws[(BM + 127) / 128][SPEC_MAX_HEAD_WIDTH / 128];
+  SPEC_LDS char* const lds = (SPEC_LDS char*)lds_;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wi = wave % WM, wj = wave / WM, l16 = lane & 15, q = lane >> 4;
+  // bands of up to 8 tiles of rows: the workgroups of an XCD share a few strips of either operand in its L2
+  const int tile = xcd_tile((int)blockIdx.x, ti * tj), band = tile / (8 * ti), in = tile - band * 8 * ti;
+  const int bw = min(8, tj - band * 8);
+  const int i0 = in / bw * BM, j0 = (band * 8 + in % bw) * BN;
+  const int nk = a.groups, full = a.d / kStepBytes, rem = a.d % kStepBytes;
+
+  for (int k = tid; k < (BM + 127) / 128 * nk; k += NTHR) {
+    const int s = k / nk, g = k - s * nk, row = min(i0 / 128 + s, (a.V - 1) / 128);
+    sws[s][g] = a.sw[(size_t)row * nk + g];
+  }
+
+  const int lr = lane >> 3, lc = ((lane & 7) ^ lr) * 16;
+  const uint8_t* A = a.w + (size_t)i0 * a.d;
+  const uint8_t* B = a.x + (size_t)j0 * a.d;
+  // chunk u of the thread: row 8 NW u + 8 wave + lr of the tile, or the last one that exists
+  const uint32_t va = (uint32_t)(wave * 8 + lr) * (uint32_t)a.d + lc, step = NW * 8 * (uint32_t)a.d;
+  const uint32_t lastA = (uint32_t)min(BM - 1, a.V - 1 - i0) * (uint32_t)a.d, lastB = (uint32_t)min(BN - 1, a.N - 1 - j0) * (uint32_t)a.d;
+  auto row_a = [&](int u) { return min(va + u * step, lastA + lc); };
+  auto row_b = [&](int u) { return min(va + u * step, lastB + lc); };
+  // the scale of row tid of the tile (past BN: of any row, into words that are not read)
+  const float* S = a.sx + (size_t)j0 * nk;
+  const uint32_t vs = (uint32_t)min(tid % BN, a.N - 1 - j0) * (uint32_t)nk * 4;
+
+  auto dma = [&](const void* src, uint32_t off, SPEC_LDS char* dst) {
+    __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(reinterpret_cast<const char*>(src) + off),
+                                     (SPEC_LDS void*)dst, 16, 0, 0);
+  };
+  auto issue_scales = [&](SPEC_LDS char* dst, int t) {
+    __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(reinterpret_cast<const char*>(S + t) + vs),
+                                     (SPEC_LDS void*)(dst + (BM + BN) * kStepBytes + wave * 256), 4, 0, 0);
+  };
+  auto issue_whole = [&](SPEC_LDS char* dst, int t) {
+    size_t o = (size_t)t * kStepBytes;
+    asm("" : "+s"(o));   // scalar base + 32-bit lane offset
+#pragma unroll
+    for (int u = 0; u < CA; ++u) dma(A + o, row_a(u), dst + (u * NW + wave) * 1024);
+#pragma unroll
+    for (int u = 0; u < CB; ++u) dma(B + o, row_b(u), dst + BM * kStepBytes + (u * NW + wave) * 1024);
+    issue_scales(dst, t);
+  };
+  auto issue = [&](int t) {
+    SPEC_LDS char* dst = lds + (t % ST) * STAGE;
+    if (t < full) {
+      issue_whole(dst, t);
+    } else if (t < nk) {   // rows that are no multiple of 128 bytes: zeros behind their end
+      const v4u32 zero = {};
+      const size_t o = (size_t)t * kStepBytes;
+#pragma unroll 1
+      for (int u = 0; u < CA; ++u)
+        *reinterpret_cast<SPEC_LDS v4u32*>(dst + (u * NW + wave) * 1024 + lane * 16) =
+            lc < rem ? *reinterpret_cast<const v4u32*>(A + o + row_a(u)) : zero;
+#pragma unroll 1
+      for (int u = 0; u < CB; ++u)
+        *reinterpret_cast<SPEC_LDS v4u32*>(dst + BM * kStepBytes + (u * NW + wave) * 1024 + lane * 16) =
+            lc < rem ? *reinterpret_cast<const v4u32*>(B + o + row_b(u)) : zero;
+      issue_scales(dst, t);
+    }
+  };
+
+  f32x4 acc[MT][NT] = {};
+  const int ra = (wi * MT * 16 + l16) * kStepBytes + ((q ^ (lane & 7)) * 16);
+  const int rb = (BM + wj * NT * 16 + l16) * kStepBytes + ((q ^ (lane & 7)) * 16);
+  const int rs = (BM + BN) * kStepBytes + (wj * NT * 16 + l16) * 4;
+  auto read = [&](const SPEC_LDS char* st, int at) {   // chunks q and q + 4
+    return Codes{*reinterpret_cast<const SPEC_LDS v4u32*>(st + at), *reinterpret_cast<const SPEC_LDS v4u32*>(st + (at ^ 64))};
+  };
+  Codes ca[MT];
+  Frag<F32> fb[NT];
+  float s[NT];
+  f32x4 p[2][NT];
+  auto read_a = [&](const SPEC_LDS char* st, int m) { ca[m] = read(st, ra + m * 16 * kStepBytes); };
+  auto read_b = [&](const SPEC_LDS char* st, int n) { fb[n].set(read(st, rb + n * 16 * kStepBytes)); };
+  auto read_s = [&](const SPEC_LDS char* st, int t) {
+    const float w = sws[wi * (BM / WM) / 128][t];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) s[n] = *reinterpret_cast<const SPEC_LDS float*>(st + rs + n * 64) * w;
+  };
+  auto add = [&](int m) {   // the sums of unit m
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) acc[m][n][x] = fmaf(p[m & 1][n][x], s[n], acc[m][n][x]);
+  };
+  auto multiply = [&](int m) {
+    Frag<F32> fa;
+    fa.set(ca[m]);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) p[m & 1][n] = product(fa, fb[n]);
+  };
+
+#pragma unroll
+  for (int t = 0; t < ST; ++t) issue(t);
+  // units 0 .. MT - 3 of a step whose first operands are there
+  auto head = [&](const SPEC_LDS char* cur) {
+#pragma unroll
+    for (int m = 0; m < MT - 2; ++m) {
+      if (m + 2 < MT) read_a(cur, m + 2);
+      multiply(m);
+      if (m > 0) add(m - 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto first = [&](int t) {
+    const SPEC_LDS char* cur = lds + (t % ST) * STAGE;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) read_b(cur, n);
+    read_s(cur, t);
+    read_a(cur, 0);
+    read_a(cur, 1);
+  };
+  // step 0
+  if (nk >= ST) wait_barrier<(ST - 1) * DMA>();
+  else wait_barrier<0>();
+  first(0);
+  head(lds);
+  auto turn = [&](SPEC_LDS char* __restrict__ free, const SPEC_LDS char* __restrict__ cur, int t, bool whole) {
+    if (whole) issue_whole(free, t + ST - 1);
+    else issue(t + ST - 1);
+    read_a(cur, 0);
+    multiply(MT - 2);
+    add(MT - 3);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(MT - 1);
+    add(MT - 2);
+    read_a(cur, 1);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) read_b(cur, n);
+    __builtin_amdgcn_sched_barrier(0);
+    add(MT - 1);
+    read_s(cur, t);
+    head(cur);
+  };
+  int t = 1;
+  for (; t + ST - 1 < full; ++t) {
+    wait_barrier<(ST - 2) * DMA>();
+    turn(lds + ((t + ST - 1) % ST) * STAGE, lds + (t % ST) * STAGE, t, true);
+  }
+  for (; t < nk; ++t) {
+    wait_barrier<0>();
+    turn(lds + ((t + ST - 1) % ST) * STAGE, lds + (t % ST) * STAGE, t, false);
+  }
+  multiply(MT - 2);
+  add(MT - 3);
+  multiply(MT - 1);
+  add(MT - 2);
+  add(MT - 1);
+
+  // acc[m][n][x]: token i0 + wi MT 16 + 16 m + 4 q + x of row j0 + wj NT 16 + 16 n + l16.  Each wave turns its part
+  // around in LDS, 16 rows at a time, so that a row's values leave it side by side.
+  constexpr int ES = F32 ? 4 : 2, VE = 16 / ES, ROW = MT * 16 * ES, PITCH = ROW + 16, LANES = ROW / 16;
+  static_assert(NW * 16 * PITCH <= ST * STAGE, "epilogue");
+  wait_barrier<0>();
+  SPEC_LDS char* const mine = lds + wave * 16 * PITCH;
+  const int iw = i0 + wi * MT * 16;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      SPEC_LDS char* p = mine + l16 * PITCH + (m * 16 + q * 4) * ES;
+      if constexpr (F32) {
+        *reinterpret_cast<SPEC_LDS f32x4*>(p) = acc[m][n];
+      } else {
+        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+        bf16x4 h;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) h[x] = (__bf16)acc[m][n][x];
+        *reinterpret_cast<SPEC_LDS bf16x4*>(p) = h;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 16; r += 64 / LANES) {
+      const int row = r + lane / LANES, c = lane % LANES * VE, j = j0 + (wj * NT + n) * 16 + row, i = iw + c;
+      const v4u32 v = *reinterpret_cast<const SPEC_LDS v4u32*>(mine + row * PITCH + c * ES);
+      char* dst = reinterpret_cast<char*>(a.out) + ((size_t)j * a.V + i) * ES;
+      if (j < a.N && i + VE <= a.V) {
+        reinterpret_cast<Any16*>(dst)->v = v;
+      } else if (j < a.N) {
+#pragma unroll
+        for (int x = 0; x < VE; ++x)
+          if (i + x < a.V) {
+            if constexpr (F32) reinterpret_cast<uint32_t*>(dst)[x] = v[x];
+            else reinterpret_cast<uint16_t*>(dst)[x] = (uint16_t)(v[x / 2] >> (x & 1 ? 16 : 0));
+          }
+      }
+    }
+  }
+}
+
 template <bool F32>
 void run_logits(const LogitArgs& a, hipStream_t s) {
   const unsigned gx = (unsigned)ceil_div(a.V, 64);
-  if (a.N <= 16) hipLaunchKernelGGL((logits_rows_kernel<F32, 1, 4>), dim3(gx, 1), dim3(256), 0, s, a);
-  else if (a.N <= 32) hipLaunchKernelGGL((logits_rows_kernel<F32, 2, 4>), dim3(gx, 1), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((logits_rows_kernel<F32, 4, 4>), dim3(gx, (unsigned)ceil_div(a.N, 64)), dim3(256), 0, s, a);
+  if (a.N <= 16) {
+    hipLaunchKernelGGL((logits_rows_kernel<F32, 1, 4>), dim3(gx, 1), dim3(256), 0, s, a);
+  } else if (a.N <= 32) {
+    hipLaunchKernelGGL((logits_rows_kernel<F32, 2, 4>), dim3(gx, 1), dim3(256), 0, s, a);
+  } else if (a.N <= 64) {
+    hipLaunchKernelGGL((logits_rows_kernel<F32, 4, 4>), dim3(gx, 1), dim3(256), 0, s, a);
+  } else {
+    constexpr int BM = F32 ? 128 : 256, BN = F32 ? 128 : 256;
+    const int ti = ceil_div(a.V, BM), tj = ceil_div(a.N, BN);
+    if constexpr (F32)
+      hipLaunchKernelGGL((logits_tile_kernel<true, 128, 128, 2, 2, 2>), dim3((unsigned)(ti * tj)), dim3(256), 0, s, a, ti, tj);
+    else
+      hipLaunchKernelGGL((logits_tile_kernel<false, 256, 256, 2, 4, 2>), dim3((unsigned)(ti * tj)), dim3(512), 0, s, a, ti, tj);
+  }
 }
 
 }  // namespace

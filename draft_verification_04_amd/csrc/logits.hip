@@ -182,9 +182,11 @@ __device__ __forceinline__ int xcd_tile(int bid, int total) {
   return x < rem ? x * (q + 1) + i : rem * (q + 1) + (x - rem) * q + i;
 }
 
+constexpr int kScaleSteps = 4;
+
 // Many rows: tiles of BM tokens and BN rows, WM x WN waves.  A step is one block of k: 128 bytes of every row of the
 // tile, brought to LDS directly (16 bytes per lane, chunk c of row r at c ^ (r & 7), so that the 16 rows that an
-// operand read touches fall into different banks), ST - 1 steps ahead, with the rows' scales of the block.
+// operand read touches fall into different banks), ST - 1 steps ahead.
 //
 // A wave goes through its MT operands of the vocabulary one after the other, each against the NT of the rows (a unit:
 // NT matrix instructions); while a unit runs, the unit before it is scaled and added and the operands of the next but
@@ -192,10 +194,11 @@ __device__ __forceinline__ int xcd_tile(int bid, int total) {
 template <bool F32, int BM, int BN, int WM, int WN, int ST>
 __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs a, int ti, int tj) {
   constexpr int NW = WM * WN, NTHR = NW * 64, MT = BM / WM / 16, NT = BN / WN / 16;
-  constexpr int CA = BM * 8 / NTHR, CB = BN * 8 / NTHR, DMA = CA + CB + 1;
-  constexpr int SCALES = NW * 64, STAGE = (BM + BN) * kStepBytes + SCALES * 4;
-  static_assert(MT >= 4 && BM / WM <= 128 && SCALES >= BN, "tile");
+  constexpr int CA = BM * 8 / NTHR, CB = BN * 8 / NTHR, CS = BN * kScaleSteps / NTHR;
+  constexpr int STAGE = (BM + BN) * kStepBytes;
+  static_assert(MT >= 4 && BM / WM <= 128 && CS >= 1 && ST <= kScaleSteps, "tile");
   __shared__ __attribute__((aligned(128))) char lds_[ST * STAGE];
+  __shared__ float sxs[2 * BN * kScaleSteps];
   __shared__ float sws[(BM + 127) / 128][SPEC_MAX_HEAD_WIDTH / 128];
   SPEC_LDS char* const lds = (SPEC_LDS char*)lds_;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -219,17 +222,24 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
   const uint32_t lastA = (uint32_t)min(BM - 1, a.V - 1 - i0) * (uint32_t)a.d, lastB = (uint32_t)min(BN - 1, a.N - 1 - j0) * (uint32_t)a.d;
   auto row_a = [&](int u) { return min(va + u * step, lastA + lc); };
   auto row_b = [&](int u) { return min(va + u * step, lastB + lc); };
-  // the scale of row tid of the tile (past BN: of any row, into words that are not read)
+  // the rows' scales: kScaleSteps blocks at a time, lanes side by side along a row (a line of memory each would cost
+  // the loads as much as the operands)
   const float* S = a.sx + (size_t)j0 * nk;
-  const uint32_t vs = (uint32_t)min(tid % BN, a.N - 1 - j0) * (uint32_t)nk * 4;
-
+  const int sr = tid / kScaleSteps, sg = tid % kScaleSteps;
   auto dma = [&](const void* src, uint32_t off, SPEC_LDS char* dst) {
     __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(reinterpret_cast<const char*>(src) + off),
                                      (SPEC_LDS void*)dst, 16, 0, 0);
   };
-  auto issue_scales = [&](SPEC_LDS char* dst, int t) {
-    __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(reinterpret_cast<const char*>(S + t) + vs),
-                                     (SPEC_LDS void*)(dst + (BM + BN) * kStepBytes + wave * 256), 4, 0, 0);
+  auto issue_scales = [&](int t) {   // of steps t .. t + kScaleSteps - 1
+    if (t % kScaleSteps != 0) return;
+    const int g = min(t + sg, nk - 1);
+    SPEC_LDS char* dst = (SPEC_LDS char*)sxs + (t / kScaleSteps % 2 * BN * kScaleSteps + wave * 64) * 4;
+#pragma unroll
+    for (int u = 0; u < CS; ++u) {
+      const int r = min(sr + u * (NTHR / kScaleSteps), a.N - 1 - j0);
+      __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(S + (uint32_t)(r * nk + g)),
+                                       (SPEC_LDS void*)(dst + u * NTHR * 4), 4, 0, 0);
+    }
   };
   auto issue_whole = [&](SPEC_LDS char* dst, int t) {
     size_t o = (size_t)t * kStepBytes;
@@ -238,7 +248,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
     for (int u = 0; u < CA; ++u) dma(A + o, row_a(u), dst + (u * NW + wave) * 1024);
 #pragma unroll
     for (int u = 0; u < CB; ++u) dma(B + o, row_b(u), dst + BM * kStepBytes + (u * NW + wave) * 1024);
-    issue_scales(dst, t);
+    issue_scales(t);
   };
   auto issue = [&](int t) {
     SPEC_LDS char* dst = lds + (t % ST) * STAGE;
@@ -255,14 +265,14 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
       for (int u = 0; u < CB; ++u)
         *reinterpret_cast<SPEC_LDS v4u32*>(dst + BM * kStepBytes + (u * NW + wave) * 1024 + lane * 16) =
             lc < rem ? *reinterpret_cast<const v4u32*>(B + o + row_b(u)) : zero;
-      issue_scales(dst, t);
+      issue_scales(t);
     }
   };
 
   f32x4 acc[MT][NT] = {};
   const int ra = (wi * MT * 16 + l16) * kStepBytes + ((q ^ (lane & 7)) * 16);
   const int rb = (BM + wj * NT * 16 + l16) * kStepBytes + ((q ^ (lane & 7)) * 16);
-  const int rs = (BM + BN) * kStepBytes + (wj * NT * 16 + l16) * 4;
+  const int rs = (wj * NT * 16 + l16) * kScaleSteps;
   auto read = [&](const SPEC_LDS char* st, int at) {   // chunks q and q + 4
     return Codes{*reinterpret_cast<const SPEC_LDS v4u32*>(st + at), *reinterpret_cast<const SPEC_LDS v4u32*>(st + (at ^ 64))};
   };
@@ -272,10 +282,11 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
   f32x4 p[2][NT];
   auto read_a = [&](const SPEC_LDS char* st, int m) { ca[m] = read(st, ra + m * 16 * kStepBytes); };
   auto read_b = [&](const SPEC_LDS char* st, int n) { fb[n].set(read(st, rb + n * 16 * kStepBytes)); };
-  auto read_s = [&](const SPEC_LDS char* st, int t) {
+  auto read_s = [&](int t) {
     const float w = sws[wi * (BM / WM) / 128][t];
+    const float* x = sxs + t / kScaleSteps % 2 * BN * kScaleSteps + t % kScaleSteps + rs;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) s[n] = *reinterpret_cast<const SPEC_LDS float*>(st + rs + n * 64) * w;
+    for (int n = 0; n < NT; ++n) s[n] = x[n * 16 * kScaleSteps] * w;
   };
   auto add = [&](int m) {   // the sums of unit m
 #pragma unroll
@@ -306,12 +317,12 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
     const SPEC_LDS char* cur = lds + (t % ST) * STAGE;
 #pragma unroll
     for (int n = 0; n < NT; ++n) read_b(cur, n);
-    read_s(cur, t);
+    read_s(t);
     read_a(cur, 0);
     read_a(cur, 1);
   };
   // step 0
-  if (nk >= ST) wait_barrier<(ST - 1) * DMA>();
+  if (nk >= ST) wait_barrier<(ST - 1) * (CA + CB)>();
   else wait_barrier<0>();
   first(0);
   head(lds);
@@ -329,12 +340,12 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
     for (int n = 0; n < NT; ++n) read_b(cur, n);
     __builtin_amdgcn_sched_barrier(0);
     add(MT - 1);
-    read_s(cur, t);
+    read_s(t);
     head(cur);
   };
   int t = 1;
   for (; t + ST - 1 < full; ++t) {
-    wait_barrier<(ST - 2) * DMA>();
+    wait_barrier<(ST - 2) * (CA + CB)>();
     turn(lds + ((t + ST - 1) % ST) * STAGE, lds + (t % ST) * STAGE, t, true);
   }
   for (; t < nk; ++t) {

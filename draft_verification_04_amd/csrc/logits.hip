@@ -30,7 +30,6 @@ struct __attribute__((packed, aligned(2))) Any16 {
   v4u32 v;
 };
 
-#define SPEC_GLOBAL __attribute__((address_space(1)))
 #define SPEC_LDS __attribute__((address_space(3)))
 
 struct LogitArgs {
@@ -170,6 +169,24 @@ __global__ __launch_bounds__(KW * 64, 2) void logits_rows_kernel(LogitArgs a) {
   }
 }
 
+// 16 (or 4) bytes per lane from base + off to LDS at dst, a wave's lanes side by side.  The caller waits for it (vmcnt)
+// before the bytes are read: behind the builtin of this instruction the compiler would have the next LDS read wait for
+// all loads in flight, which left a step's loads no time (2048 rows x 151936, d = 4096: 1429 us, so 1228).
+template <int BYTES>
+__device__ __forceinline__ void load_lds(const void* base, uint32_t off, SPEC_LDS char* dst) {
+  static_assert(BYTES == 16 || BYTES == 4, "dwords");
+  const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)dst);
+  const uint64_t b = (uint64_t)base;   // in scalar registers, whichever unit it was computed in
+  const uint64_t sb = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32 |
+                      (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b);
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(sb)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(at), "v"(off), "s"(sb)
+                 : "memory", "m0");
+}
+
 // Waits until at most N of the wave's loads are in flight and its LDS accesses are done, then the workgroup barrier.
 template <int N>
 __device__ __forceinline__ void wait_barrier() {
@@ -182,11 +199,13 @@ __device__ __forceinline__ int xcd_tile(int bid, int total) {
   return x < rem ? x * (q + 1) + i : rem * (q + 1) + (x - rem) * q + i;
 }
 
-constexpr int kScaleSteps = 4;
+constexpr int kScaleSteps = 4;   // steps whose scales are loaded together
+constexpr int kPart = 2;         // of a thread's loads for a step, issued between two units
 
 // Many rows: tiles of BM tokens and BN rows, WM x WN waves.  A step is one block of k: 128 bytes of every row of the
 // tile, brought to LDS directly (16 bytes per lane, chunk c of row r at c ^ (r & 7), so that the 16 rows that an
-// operand read touches fall into different banks), ST - 1 steps ahead.
+// operand read touches fall into different banks), ST - 1 steps ahead, a few loads between two units (all of them at
+// once: 1221 us in place of 1153 on 2048 rows x 151936, d = 4096; later ones, one a unit: 1198).
 //
 // A wave goes through its MT operands of the vocabulary one after the other, each against the NT of the rows (a unit:
 // NT matrix instructions); while a unit runs, the unit before it is scaled and added and the operands of the next but
@@ -196,7 +215,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
   constexpr int NW = WM * WN, NTHR = NW * 64, MT = BM / WM / 16, NT = BN / WN / 16;
   constexpr int CA = BM * 8 / NTHR, CB = BN * 8 / NTHR, CS = BN * kScaleSteps / NTHR;
   constexpr int STAGE = (BM + BN) * kStepBytes;
-  static_assert(MT >= 4 && BM / WM <= 128 && CS >= 1 && ST <= kScaleSteps, "tile");
+  static_assert(MT >= 4 && BM / WM <= 128 && CS >= 1 && ST <= kScaleSteps && (CA + CB) <= kPart * MT, "tile");
   __shared__ __attribute__((aligned(128))) char lds_[ST * STAGE];
   __shared__ float sxs[2 * BN * kScaleSteps];
   __shared__ float sws[(BM + 127) / 128][SPEC_MAX_HEAD_WIDTH / 128];
@@ -206,13 +225,8 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
   // bands of up to 8 tiles of rows: the workgroups of an XCD share a few strips of either operand in its L2
   const int tile = xcd_tile((int)blockIdx.x, ti * tj), band = tile / (8 * ti), in = tile - band * 8 * ti;
   const int bw = min(8, tj - band * 8);
-  const int i0 = in / bw * BM, j0 = (band * 8 + in % bw) * BN;
+  const int i0 = __builtin_amdgcn_readfirstlane(in / bw * BM), j0 = __builtin_amdgcn_readfirstlane((band * 8 + in % bw) * BN);
   const int nk = a.groups, full = a.d / kStepBytes, rem = a.d % kStepBytes;
-
-  for (int k = tid; k < (BM + 127) / 128 * nk; k += NTHR) {
-    const int s = k / nk, g = k - s * nk, row = min(i0 / 128 + s, (a.V - 1) / 128);
-    sws[s][g] = a.sw[(size_t)row * nk + g];
-  }
 
   const int lr = lane >> 3, lc = ((lane & 7) ^ lr) * 16;
   const uint8_t* A = a.w + (size_t)i0 * a.d;
@@ -226,34 +240,35 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
   // the loads as much as the operands)
   const float* S = a.sx + (size_t)j0 * nk;
   const int sr = tid / kScaleSteps, sg = tid % kScaleSteps;
-  auto dma = [&](const void* src, uint32_t off, SPEC_LDS char* dst) {
-    __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(reinterpret_cast<const char*>(src) + off),
-                                     (SPEC_LDS void*)dst, 16, 0, 0);
-  };
+  auto stage = [&](int t) { return lds + (t % ST) * STAGE; };
+  auto scales_of = [&](int t) { return (SPEC_LDS char*)sxs + t / kScaleSteps % 2 * (BN * kScaleSteps * 4); };
   auto issue_scales = [&](int t) {   // of steps t .. t + kScaleSteps - 1
     if (t % kScaleSteps != 0) return;
     const int g = min(t + sg, nk - 1);
-    SPEC_LDS char* dst = (SPEC_LDS char*)sxs + (t / kScaleSteps % 2 * BN * kScaleSteps + wave * 64) * 4;
+    SPEC_LDS char* dst = scales_of(t) + wave * 256;
 #pragma unroll
     for (int u = 0; u < CS; ++u) {
       const int r = min(sr + u * (NTHR / kScaleSteps), a.N - 1 - j0);
-      __builtin_amdgcn_global_load_lds((const SPEC_GLOBAL void*)(S + (uint32_t)(r * nk + g)),
-                                       (SPEC_LDS void*)(dst + u * NTHR * 4), 4, 0, 0);
+      load_lds<4>(S, (uint32_t)(r * nk + g) * 4, dst + u * NTHR * 4);
     }
   };
-  auto issue_whole = [&](SPEC_LDS char* dst, int t) {
+  // part `c` of step t's loads: kPart of the thread's chunks
+  auto issue_part = [&](int t, int c) {
+    SPEC_LDS char* const dst = stage(t);
     size_t o = (size_t)t * kStepBytes;
     asm("" : "+s"(o));   // scalar base + 32-bit lane offset
 #pragma unroll
-    for (int u = 0; u < CA; ++u) dma(A + o, row_a(u), dst + (u * NW + wave) * 1024);
-#pragma unroll
-    for (int u = 0; u < CB; ++u) dma(B + o, row_b(u), dst + BM * kStepBytes + (u * NW + wave) * 1024);
-    issue_scales(t);
+    for (int u = c * kPart; u < min((c + 1) * kPart, CA + CB); ++u) {
+      if (u < CA) load_lds<16>(A + o, row_a(u), dst + (u * NW + wave) * 1024);
+      else load_lds<16>(B + o, row_b(u - CA), dst + BM * kStepBytes + ((u - CA) * NW + wave) * 1024);
+    }
   };
   auto issue = [&](int t) {
-    SPEC_LDS char* dst = lds + (t % ST) * STAGE;
+    SPEC_LDS char* const dst = stage(t);
     if (t < full) {
-      issue_whole(dst, t);
+#pragma unroll
+      for (int c = 0; c * kPart < CA + CB; ++c) issue_part(t, c);
+      issue_scales(t);
     } else if (t < nk) {   // rows that are no multiple of 128 bytes: zeros behind their end
       const v4u32 zero = {};
       const size_t o = (size_t)t * kStepBytes;
@@ -284,7 +299,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
   auto read_b = [&](const SPEC_LDS char* st, int n) { fb[n].set(read(st, rb + n * 16 * kStepBytes)); };
   auto read_s = [&](int t) {
     const float w = sws[wi * (BM / WM) / 128][t];
-    const float* x = sxs + t / kScaleSteps % 2 * BN * kScaleSteps + t % kScaleSteps + rs;
+    const SPEC_LDS float* x = reinterpret_cast<const SPEC_LDS float*>(scales_of(t)) + t % kScaleSteps + rs;
 #pragma unroll
     for (int n = 0; n < NT; ++n) s[n] = x[n * 16 * kScaleSteps] * w;
   };
@@ -303,36 +318,43 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
 
 #pragma unroll
   for (int t = 0; t < ST; ++t) issue(t);
+  for (int k = tid; k < (BM + 127) / 128 * nk; k += NTHR) {
+    const int s = k / nk, g = k - s * nk, row = min(i0 / 128 + s, (a.V - 1) / 128);
+    sws[s][g] = a.sw[(size_t)row * nk + g];
+  }
   // units 0 .. MT - 3 of a step whose first operands are there
-  auto head = [&](const SPEC_LDS char* cur) {
+  auto head = [&](const SPEC_LDS char* cur, int t, bool whole) {
 #pragma unroll
     for (int m = 0; m < MT - 2; ++m) {
-      if (m + 2 < MT) read_a(cur, m + 2);
+      if (whole) issue_part(t + ST - 1, m + 2);
+      read_a(cur, m + 2);
       multiply(m);
       if (m > 0) add(m - 1);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  auto first = [&](int t) {
-    const SPEC_LDS char* cur = lds + (t % ST) * STAGE;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) read_b(cur, n);
-    read_s(t);
-    read_a(cur, 0);
-    read_a(cur, 1);
-  };
   // step 0
   if (nk >= ST) wait_barrier<(ST - 1) * (CA + CB)>();
   else wait_barrier<0>();
-  first(0);
-  head(lds);
-  auto turn = [&](SPEC_LDS char* __restrict__ free, const SPEC_LDS char* __restrict__ cur, int t, bool whole) {
-    if (whole) issue_whole(free, t + ST - 1);
-    else issue(t + ST - 1);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) read_b(lds, n);
+  read_s(0);
+  read_a(lds, 0);
+  read_a(lds, 1);
+  head(lds, 0, false);
+  auto turn = [&](int t, bool whole) {
+    const SPEC_LDS char* const cur = stage(t);
+    if (whole) {   // step t + ST - 1, into the buffer of step t - 1, which every wave has read
+      issue_part(t + ST - 1, 0);
+      issue_scales(t + ST - 1);
+    } else {
+      issue(t + ST - 1);
+    }
     read_a(cur, 0);
     multiply(MT - 2);
     add(MT - 3);
     __builtin_amdgcn_sched_barrier(0);
+    if (whole) issue_part(t + ST - 1, 1);
     multiply(MT - 1);
     add(MT - 2);
     read_a(cur, 1);
@@ -341,16 +363,16 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
     __builtin_amdgcn_sched_barrier(0);
     add(MT - 1);
     read_s(t);
-    head(cur);
+    head(cur, t, whole);
   };
   int t = 1;
   for (; t + ST - 1 < full; ++t) {
     wait_barrier<(ST - 2) * (CA + CB)>();
-    turn(lds + ((t + ST - 1) % ST) * STAGE, lds + (t % ST) * STAGE, t, true);
+    turn(t, true);
   }
   for (; t < nk; ++t) {
     wait_barrier<0>();
-    turn(lds + ((t + ST - 1) % ST) * STAGE, lds + (t % ST) * STAGE, t, false);
+    turn(t, false);
   }
   multiply(MT - 2);
   add(MT - 3);

@@ -5,10 +5,14 @@
 //   z = z - frequency * count;  z = z - presence (count > 0);  z = z + bias;  z = -inf where the mask's bit is 0
 //
 // Nearly all of a row stays as it is: a history names a few thousand tokens of the vocabulary.  A workgroup takes a
-// request and a slice of the vocabulary: it counts the slice's tokens of the history in LDS (a word per token; the
-// first to name a token puts it on a list), and then goes over the list for every row of the block.  In place the
-// rest of the row is touched only where a mask forbids it; out of place it is copied.  The rows of a block share
-// one count, the draft tokens before a row are compared with the listed token one by one.
+// request and a slice of the vocabulary.  It counts the slice's tokens of the history in LDS (a word per token; the
+// first to count a token puts it on a list), and then goes through the block's rows, which share one count; the draft
+// tokens before a row are compared with the listed token one by one.
+//   Out of place, under a mask, or where much may be listed: the slice of a row goes through LDS, where
+//   lanes take the listed tokens (adjusted in the registers that carry the rows, a lane here and there of every wave,
+//   it took as long as the copy itself).  Masks are applied on the way out.  In place, pieces without a count are
+//   written only where the mask forbids a value, and read only where it forbids some.
+//   In place without a mask and with few tokens: lanes take pairs of listed token and row in memory.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -23,9 +27,8 @@
 namespace spec {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kSlice = 8192;                 // tokens of the vocabulary per workgroup (at most 2^16)
-constexpr uint32_t kInPrompt = 1u << 30, kListed = 1u << 31, kCount = kInPrompt - 1;
+constexpr int kSlice = 4096, kLongHistory = 8192;
+constexpr uint32_t kInPrompt = 1u << 30, kDrafted = 1u << 31, kBiased = 1u << 29, kCount = kBiased - 1;
 
 struct AdjustArgs {
   const char* logits;   // [B, R, V]
@@ -47,12 +50,11 @@ struct AdjustArgs {
   int R, V, gamma, H, bias_count, masks, words;
 };
 
-// The row's mask bits of tokens v .. v + 31 (0 past the words).
-__device__ __forceinline__ uint32_t mask_bits(const uint32_t* m, int words, int v) {
-  const int w = v >> 5, s = v & 31;
-  const uint32_t lo = m[w], hi = w + 1 < words ? m[w + 1] : 0u;
-  return (uint32_t)((((uint64_t)hi << 32) | lo) >> s);
-}
+// 16 bytes of a row; rows start on no boundary where V is odd.
+template <int ALIGN>
+struct __attribute__((packed, aligned(ALIGN))) Piece {
+  v4u32 v;
+};
 
 template <bool BF16>
 __device__ __forceinline__ void store_elem(char* row, int64_t v, float z) {
@@ -60,19 +62,23 @@ __device__ __forceinline__ void store_elem(char* row, int64_t v, float z) {
   else reinterpret_cast<float*>(row)[v] = z;
 }
 
-// BIAS: the slots of the biases lie behind the counts.
-template <bool BF16, bool BIAS, bool COPY>
-__global__ __launch_bounds__(kThreads) void adjust_kernel(AdjustArgs a) {
-  constexpr int ES = BF16 ? 2 : 4, VE = 16 / ES;
-  constexpr uint32_t kNegInf = BF16 ? 0xff80ff80u : 0xff800000u;
-  __shared__ uint32_t count[kSlice];
-  __shared__ uint32_t bias_at[BIAS ? kSlice : 1];   // entry of the list + 1 (the last one of a token named twice)
-  __shared__ uint16_t list[kSlice];
+// S tokens of the vocabulary and T threads per workgroup.
+enum { kCopy = 0, kPlace = 1, kFew = 2 };   // out of place; in place; in place without a mask, few tokens
+
+template <bool BF16, bool BIAS, int MODE, int S, int T, int U>
+__global__ __launch_bounds__(T) void adjust_kernel(AdjustArgs a) {
+  constexpr bool COPY = MODE == kCopy;
+  constexpr int ES = BF16 ? 2 : 4, VE = 16 / ES, NV = S / VE / T;   // pieces of a row per lane; U rows at a time
+  static_assert(S % (VE * T) == 0 && S <= 65536, "slice");
+  __shared__ __attribute__((aligned(16))) uint32_t count[S];
+  __shared__ __attribute__((aligned(16))) uint32_t bias_at[BIAS ? S : 4];   // entry of the list + 1 (the last one of a token named twice)
+  __shared__ __attribute__((aligned(16))) char rows[MODE == kFew ? 1 : U][MODE == kFew ? 16 : S * ES];
+  __shared__ uint16_t list[S];
   __shared__ int32_t drafts[SPEC_MAX_GAMMA];
   __shared__ int listed, bad;
-  const int tid = threadIdx.x, V = a.V, R = a.R, slices = (V + kSlice - 1) / kSlice;
+  const int tid = threadIdx.x, V = a.V, R = a.R, slices = (V + S - 1) / S;
   const int b = (int)(blockIdx.x / (unsigned)slices), slice = (int)(blockIdx.x % (unsigned)slices);
-  const int v0 = slice * kSlice, n = min(kSlice, V - v0);
+  const int v0 = slice * S, n = min(S, V - v0);
 
   // the request's own numbers; every workgroup of the request comes to the same verdict
   int st = 0;
@@ -98,37 +104,55 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(AdjustArgs a) {
   const int mi = a.mask ? (a.mask_index ? a.mask_index[b] : b) : -1;
   if (mi < -1 || mi >= a.masks) st |= SPEC_REQ_BAD_MASK;
 
-  for (int i = tid; i < n; i += kThreads) {
-    count[i] = 0;
-    if constexpr (BIAS) bias_at[i] = 0;
+  for (int i = tid; i < S / 4; i += T) {
+    reinterpret_cast<v4u32*>(count)[i] = v4u32{};
+    if constexpr (BIAS) reinterpret_cast<v4u32*>(bias_at)[i] = v4u32{};
   }
   if (tid == 0) listed = bad = 0;
   const int need = penal ? min(live - 1, a.gamma) : 0;   // draft tokens that precede a live row
   if (tid < need) drafts[tid] = a.draft_tokens[(size_t)b * a.gamma + tid];
   __syncthreads();
   bool off = false;
-  auto note = [&](int i, uint32_t old) {
+  auto note = [&](unsigned i, uint32_t old) {
     if (old == 0) list[atomicAdd(&listed, 1)] = (uint16_t)i;
   };
   if (penal && live > 0) {
     const int32_t* h = a.history + (size_t)b * a.H;
-    for (int i = tid; i < hl; i += kThreads) {
-      const int t = h[i], at = t - v0;
-      off |= t < -1 || t >= V;
-      if (at >= 0 && at < n) note(at, i < pl ? atomicOr(&count[at], kInPrompt) : atomicAdd(&count[at], 1u));
+    // four tokens a load, F loads in flight per thread
+    constexpr int F = 4;
+    const int quads = hl >> 2;
+    uint32_t most = 0;   // of t + 1: -1 is a hole
+    auto count_in = [&](int t, int i) {
+      const unsigned at = (unsigned)t - (unsigned)v0;
+      most = max(most, (unsigned)t + 1u);
+      if (at < (unsigned)n) note(at, i < pl ? atomicOr(&count[at], kInPrompt) : atomicAdd(&count[at], 1u));
+    };
+    for (int i0 = tid; i0 < quads; i0 += F * T) {
+      v4u32 t[F];
+#pragma unroll
+      for (int u = 0; u < F; ++u) {
+        t[u] = v4u32{~0u, ~0u, ~0u, ~0u};
+        if (i0 + u * T < quads) t[u] = reinterpret_cast<const Piece<4>*>(h + 4 * (i0 + u * T))->v;
+      }
+#pragma unroll
+      for (int u = 0; u < F; ++u)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) count_in((int)t[u][x], 4 * (i0 + u * T) + x);
     }
+    if (tid < (hl & 3)) count_in(h[4 * quads + tid], 4 * quads + tid);
+    off |= most > (unsigned)V;
     if (tid < need) {
-      const int t = drafts[tid], at = t - v0;
-      off |= t < 0 || t >= V;
-      if (at >= 0 && at < n) note(at, atomicOr(&count[at], kListed));
+      const unsigned t = (unsigned)drafts[tid], at = t - (unsigned)v0;
+      off |= t >= (unsigned)V;
+      if (at < (unsigned)n) note(at, atomicOr(&count[at], kDrafted));
     }
   }
   if constexpr (BIAS) {
-    for (int i = tid; i < bn && live > 0; i += kThreads) {
-      const int t = a.bias_tokens[bo + i], at = t - v0;
-      off |= t < 0 || t >= V;
-      if (at >= 0 && at < n) {
-        note(at, atomicOr(&count[at], kListed));
+    for (int i = tid; i < bn && live > 0; i += T) {
+      const unsigned t = (unsigned)a.bias_tokens[bo + i], at = t - (unsigned)v0;
+      off |= t >= (unsigned)V;
+      if (at < (unsigned)n) {
+        note(at, atomicOr(&count[at], kBiased));
         atomicMax(&bias_at[at], (uint32_t)i + 1);
       }
     }
@@ -139,86 +163,191 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(AdjustArgs a) {
   if (slice == 0 && tid == 0 && a.status) a.status[b] = st;
   if (st) return;
 
+  const int E = listed;
   const uint32_t* mask = mi >= 0 ? a.mask + (size_t)mi * R * a.words : nullptr;
-  if (COPY || mask) {
-    for (int r = 0; r < live; ++r) {
-      const size_t row = ((size_t)b * R + r) * V;
-      const char* src = a.logits + row * ES;
-      char* dst = a.out + row * ES;
-      const uint32_t* m = mask ? mask + (size_t)r * a.words : nullptr;
-      // vectors that lie within the slice; up to VE - 1 values before and after them
-      const int head = min((int)((0 - (row + v0)) & (VE - 1)), n), nv = (n - head) / VE, rest = n - head - nv * VE;
-      for (int i = tid; i < nv; i += kThreads) {
-        const int v = v0 + head + i * VE;
-        const uint32_t on = m ? mask_bits(m, a.words, v) & ((1u << VE) - 1) : (1u << VE) - 1;
-        if (!COPY && on == (1u << VE) - 1) continue;
-        v4u32 z = {};
-        if (on) z = __builtin_nontemporal_load(reinterpret_cast<const v4u32*>(src + (size_t)v * ES));
+  const size_t row0 = (size_t)b * R * V + v0;
+  // a listed token: what is the same for every row
+  struct Token {
+    int i, c;
+    bool prompt, drafted, biased;
+    float bias;
+  };
+  auto token = [&](int e) {
+    Token t;
+    t.i = list[e];
+    const uint32_t w = count[t.i];
+    t.c = (int)(w & kCount);
+    t.prompt = w & kInPrompt;
+    t.drafted = w & kDrafted;
+    t.biased = BIAS && (w & kBiased);
+    t.bias = 0.f;
+    if constexpr (BIAS)
+      if (t.biased) t.bias = a.bias_values[bo + (int)bias_at[t.i] - 1];
+    return t;
+  };
+  auto adjusted = [&](float z, const Token& t, int r) {
+    int c = t.c;
+    if (t.drafted)
+      for (int k = 0; k < min(r, need); ++k) c += drafts[k] == v0 + t.i;
+    if (c > 0 || t.prompt) z = z > 0.f ? z / rep : z * rep;
+    if (c > 0) {
+      z = z - freq * (float)c;
+      z = z - pres;
+    }
+    if (t.biased) z = z + t.bias;
+    return z;
+  };
+
+  if constexpr (MODE == kFew) {
+    const unsigned pairs = (unsigned)E * (unsigned)live;
+    for (unsigned p0 = tid; p0 < pairs; p0 += U * T) {
+      float z[U];
+      Token t[U];
+      int r[U];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if constexpr (BF16) {
-            const uint32_t p = on >> (2 * x) & 3u, keep = (p & 1u ? 0xffffu : 0u) | (p & 2u ? 0xffff0000u : 0u);
-            z[x] = (z[x] & keep) | (kNegInf & ~keep);
-          } else {
-            z[x] = on >> x & 1u ? z[x] : kNegInf;
+      for (int u = 0; u < U; ++u) {
+        const unsigned p = min(p0 + u * T, pairs - 1);
+        r[u] = (int)(p / (unsigned)E);
+        t[u] = token((int)(p % (unsigned)E));
+        z[u] = load_elem<BF16>(a.logits, (int64_t)(row0 + (size_t)r[u] * V + t[u].i));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (p0 + u * T < pairs) store_elem<BF16>(a.out, (int64_t)(row0 + (size_t)r[u] * V + t[u].i), adjusted(z[u], t[u], r[u]));
+    }
+  } else {
+
+    constexpr uint32_t kAll = (1u << VE) - 1;
+    uint32_t some[NV];   // in place: a lane's values with a count
+#pragma unroll
+    for (int q = 0; q < NV; ++q) {
+      some[q] = 0;
+      if (!COPY)
+#pragma unroll
+        for (int x = 0; x < VE; ++x) some[q] |= (count[(tid + q * T) * VE + x] ? 1u : 0u) << x;
+    }
+    Token mine{};   // the lane's first listed token
+    if (tid < E) mine = token(tid);
+    for (int r0 = 0; r0 < live; r0 += U) {
+      v4u32 z[U][NV];
+      uint32_t on[U][NV];   // allowed values of the piece (0 where there is none)
+      bool move[U][NV];     // in place only what changes is read: a value with a count, or one beside a forbidden one
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int q = 0; q < NV; ++q) {
+          const int i = (tid + q * T) * VE, left = r0 + u < live ? n - i : 0;
+          on[u][q] = left >= VE ? kAll : left > 0 ? (1u << left) - 1 : 0u;
+          if (mask && left > 0) on[u][q] &= mask[(size_t)(r0 + u) * a.words + ((v0 + i) >> 5)] >> ((v0 + i) & 31);
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int q = 0; q < NV; ++q) {
+          const int i = (tid + q * T) * VE;
+          const uint32_t whole = i + VE <= n ? kAll : (1u << max(n - i, 0)) - 1;
+          move[u][q] = COPY ? on[u][q] != 0 : (on[u][q] & some[q]) != 0 || (on[u][q] != 0 && on[u][q] != whole);
+          if (!move[u][q]) continue;
+          const size_t at = row0 + (size_t)(r0 + u) * V + i;
+          if (i + VE <= n) {
+            z[u][q] = __builtin_nontemporal_load(&reinterpret_cast<const Piece<ES>*>(a.logits + at * ES)->v);
+          } else {   // the row's last values
+            z[u][q] = v4u32{};
+            for (int x = 0; i + x < n; ++x) {
+              const uint32_t h = BF16 ? reinterpret_cast<const uint16_t*>(a.logits)[at + x] : reinterpret_cast<const uint32_t*>(a.logits)[at + x];
+              if constexpr (BF16) {
+                if (x < 2) z[u][q].x |= h << (16 * x);
+                else if (x < 4) z[u][q].y |= h << (16 * (x - 2));
+                else if (x < 6) z[u][q].z |= h << (16 * (x - 4));
+                else z[u][q].w |= h << (16 * (x - 6));
+              } else {
+                if (x == 0) z[u][q].x = h;
+                else if (x == 1) z[u][q].y = h;
+                else z[u][q].z = h;
+              }
+            }
           }
         }
-        *reinterpret_cast<v4u32*>(dst + (size_t)v * ES) = z;
-      }
-      if (tid < head + rest) {
-        const int v = v0 + (tid < head ? tid : tid + nv * VE);
-        const bool on = !m || (m[v >> 5] >> (v & 31) & 1u);
-        if (!on) store_elem<BF16>(dst, v, -INFINITY);
-        else if (COPY) store_elem<BF16>(dst, v, load_elem<BF16>(src, v));
-      }
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the copy is written before values of it are written again
-    __syncthreads();
-  }
-  const unsigned E = (unsigned)listed, pairs = E * (unsigned)live;
-  constexpr int U = 4;   // values in flight per thread
-  for (unsigned p0 = tid; p0 < pairs; p0 += U * kThreads) {
-    float z[U];
-    size_t at[U];
-    bool on[U];
-    unsigned e[U];
-    int r[U];
+      if (E > 0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const unsigned p = p0 + u * kThreads;
-      on[u] = p < pairs;
-      r[u] = on[u] ? (int)(p / E) : 0;
-      e[u] = on[u] ? list[p - (unsigned)r[u] * E] : 0u;
-      const int v = v0 + (int)e[u];
-      if (mask && on[u]) on[u] = mask[(size_t)r[u] * a.words + (v >> 5)] >> (v & 31) & 1u;
-      at[u] = ((size_t)b * R + r[u]) * V + v;
-      z[u] = on[u] ? load_elem<BF16>(a.logits, (int64_t)at[u]) : 0.f;
-    }
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (!on[u]) continue;
-      const uint32_t word = count[e[u]];
-      int c = (int)(word & kCount);
-      const int v = v0 + (int)e[u], before = min(r[u], need);
-      for (int k = 0; k < before; ++k) c += drafts[k] == v;
-      float x = z[u];
-      if (c > 0 || (word & kInPrompt)) x = x > 0.f ? x / rep : x * rep;
-      x = x - freq * (float)c;
-      if (c > 0) x = x - pres;
-      if constexpr (BIAS) {
-        const uint32_t k = bias_at[e[u]];
-        if (k) x = x + a.bias_values[bo + (int)k - 1];
+          for (int q = 0; q < NV; ++q)
+            if (move[u][q]) *reinterpret_cast<v4u32*>(&rows[u][(tid + q * T) * 16]) = z[u][q];
+        __syncthreads();
+        for (int e = tid; e < E; e += T) {
+          const Token t = e == tid ? mine : token(e);
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (r0 + u < live) store_elem<BF16>(rows[u], t.i, adjusted(load_elem<BF16>(rows[u], t.i), t, r0 + u));
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int q = 0; q < NV; ++q)
+            if (move[u][q]) z[u][q] = *reinterpret_cast<const v4u32*>(&rows[u][(tid + q * T) * 16]);
       }
-      store_elem<BF16>(a.out, (int64_t)at[u], x);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int q = 0; q < NV; ++q) {
+          const int i = (tid + q * T) * VE;
+          if (r0 + u >= live || i >= n || (!COPY && !move[u][q] && on[u][q] != 0)) continue;
+          const size_t at = row0 + (size_t)(r0 + u) * V + i;
+          v4u32 y = move[u][q] ? z[u][q] : v4u32{};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if constexpr (BF16) {
+              const uint32_t p = on[u][q] >> (2 * x) & 3u, keep = (p & 1u ? 0xffffu : 0u) | (p & 2u ? 0xffff0000u : 0u);
+              y[x] = (y[x] & keep) | (0xff80ff80u & ~keep);
+            } else {
+              y[x] = on[u][q] >> x & 1u ? y[x] : 0xff800000u;
+            }
+          }
+          if (i + VE <= n) {
+            __builtin_nontemporal_store(y, &reinterpret_cast<Piece<ES>*>(a.out + at * ES)->v);
+          } else {
+#pragma unroll
+            for (int x = 0; x < VE; ++x) {
+              if (i + x >= n) break;
+              if constexpr (BF16) reinterpret_cast<uint16_t*>(a.out)[at + x] = (uint16_t)(y[x / 2] >> (x & 1 ? 16 : 0));
+              else reinterpret_cast<uint32_t*>(a.out)[at + x] = y[x];
+            }
+          }
+        }
     }
   }
 }
 
+template <bool BF16, bool BIAS, int MODE, int S, int T, int U>
+void launch(const AdjustArgs& a, int B, hipStream_t s) {
+  const dim3 grid((unsigned)ceil_div(a.V, S) * (unsigned)B);
+  hipLaunchKernelGGL((adjust_kernel<BF16, BIAS, MODE, S, T, U>), grid, dim3(T), 0, s, a);
+}
+
+// Slices of 4096 tokens, one row of it in LDS at a time (two: 98 in place of 91 us out of place on 64 blocks of 17 rows
+// of 151936 bf16, half of them live; slices of 2048: 100, of 8192: 109): 24 waves a CU or more.  Every slice's workgroup reads the
+// whole history, and from some 8000 tokens on half as many slices are faster, where their LDS leaves two workgroups
+// to a CU (96 x 8 rows of 129280 after 30011 tokens: 120 -> 108 us; after 1000: 74 -> 77).
+// In place, listed tokens cost 30 ps a row where they lie in memory, and a row's slice through LDS 1 ps a token: where
+// the history can name a thirtieth of the vocabulary the row goes through LDS.
 template <bool BF16, bool BIAS>
 void run_adjust(const AdjustArgs& a, int B, hipStream_t s) {
-  const dim3 grid((unsigned)ceil_div(a.V, kSlice) * (unsigned)B);
-  if (a.logits == a.out) hipLaunchKernelGGL((adjust_kernel<BF16, BIAS, false>), grid, dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((adjust_kernel<BF16, BIAS, true>), grid, dim3(kThreads), 0, s, a);
+  const bool copy = a.logits != a.out;
+  if (!copy && !a.mask && a.H <= a.V / 32) {
+    launch<BF16, BIAS, kFew, kSlice, 512, 4>(a, B, s);
+    return;
+  }
+  if constexpr (BF16 && !BIAS) {
+    if (a.H > kLongHistory) {
+      if (copy) launch<BF16, BIAS, kCopy, 2 * kSlice, 1024, 1>(a, B, s);
+      else launch<BF16, BIAS, kPlace, 2 * kSlice, 1024, 1>(a, B, s);
+      return;
+    }
+  }
+  if (copy) launch<BF16, BIAS, kCopy, kSlice, 512, 1>(a, B, s);
+  else launch<BF16, BIAS, kPlace, kSlice, 512, 1>(a, B, s);
 }
 
 }  // namespace
@@ -252,7 +381,7 @@ extern "C" int32_t spec_adjust_logits(int32_t B, int32_t R, int32_t V, int32_t d
     if (overlap(logits_out, bytes, p, m) || overlap(status, per, p, m)) return SPEC_ERR_INVALID_ARG;
   if (overlap(status, per, logits_out, bytes) || overlap(status, per, logits, bytes)) return SPEC_ERR_INVALID_ARG;
   // a launch's work-items are counted in 32 bits
-  if ((long long)ceil_div(V, kSlice) * B * kThreads > 0xffffffffll) return SPEC_ERR_UNSUPPORTED;
+  if ((long long)ceil_div(V, kSlice) * B * 512 > 0xffffffffll) return SPEC_ERR_UNSUPPORTED;
   const AdjustArgs a{reinterpret_cast<const char*>(logits), reinterpret_cast<char*>(logits_out), draft_tokens, lengths,
                      history, history_len, prompt_len, repetition, frequency, presence, bias_offsets, bias_tokens,
                      bias_values, mask, mask_index, status, R, V, gamma, H, bias_count, masks, (int)words};

@@ -408,7 +408,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
       const v4u32 v = *reinterpret_cast<const SPEC_LDS v4u32*>(mine + row * PITCH + c * ES);
       char* dst = reinterpret_cast<char*>(a.out) + ((size_t)j * a.V + i) * ES;
       if (j < a.N && i + VE <= a.V) {
-        reinterpret_cast<Any16*>(dst)->v = v;
+        __builtin_nontemporal_store(v, &reinterpret_cast<Any16*>(dst)->v);   // 2048 x 151936, d = 512: 248 -> 209 us
       } else if (j < a.N) {
 #pragma unroll
         for (int x = 0; x < VE; ++x)

@@ -172,8 +172,11 @@ def test_a_token_listed_twice(sv):
 
 
 def test_long_histories(sv):
-    z, toks, L, kw, g = _inputs(5, 3, 3, 4, 40000, 120001, "bf16")
-    _check(sv, z, toks, L, **kw)
+    for dtype, V in (("bf16", 40000), ("bf16", 16385), ("f32", 9001)):
+        print(f"long histories {dtype} {V}", flush=True)
+        z, toks, L, kw, g = _inputs(5, 3, 3, 4, V, 120001, dtype)
+        _check(sv, z, toks, L, **kw)
+        _check(sv, z, toks, L, **kw, mask=_mask(g, 3, 4, V, [0.5, 0.01, 0.99]))
 
 
 def test_status(sv):

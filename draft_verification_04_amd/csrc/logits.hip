@@ -15,9 +15,9 @@
 #include <stdint.h>
 
 #include "common.hpp"
+#include "logits_plan.hpp"
 #include "rowseg.hpp"
 #include "spec_verify.h"
-#include "xent_plan.hpp"
 
 namespace spec {
 namespace {
@@ -88,98 +88,20 @@ __device__ __forceinline__ f32x4 product(const Frag<true>& a, const Frag<true>& 
   return c;
 }
 
-template <bool F32>
-__device__ __forceinline__ void put(void* out, size_t at, float v) {
-  if constexpr (F32) reinterpret_cast<float*>(out)[at] = v;
-  else reinterpret_cast<__bf16*>(out)[at] = (__bf16)v;
-}
-
-// Few rows: a workgroup takes 64 tokens of the vocabulary and 16 NT rows, its waves every KW-th block of k, straight
-// from memory into registers; their sums are added in wave order.
-template <bool F32, int NT, int KW>
-__global__ __launch_bounds__(KW * 64, 2) void logits_rows_kernel(LogitArgs a) {
-  constexpr int MT = 4, BM = 16 * MT, BN = 16 * NT;
-  __shared__ float sh[KW - 1][BN][BM + 4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int l16 = lane & 15, q = lane >> 4;
-  const int i0 = blockIdx.x * BM, j0 = blockIdx.y * BN;
-  const uint8_t* wp[MT];
-  const uint8_t* xp[NT];
-  const float* sp[NT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) wp[m] = a.w + (size_t)min(i0 + m * 16 + l16, a.V - 1) * a.d + q * 16;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int j = min(j0 + n * 16 + l16, a.N - 1);
-    xp[n] = a.x + (size_t)j * a.d + q * 16;
-    sp[n] = a.sx + (size_t)j * a.groups;
-  }
-  const float* sw = a.sw + (size_t)(i0 >> 7) * a.groups;
-  f32x4 acc[MT][NT] = {};
-  for (int g = wave; g < a.groups; g += KW) {
-    const int k = g * 128, left = a.d - k - q * 16;   // bytes from the lane's first chunk to the row's end
-    const v4u32 zero = {};
-    auto fetch = [&](const uint8_t* p) {
-      return Codes{left > 0 ? *reinterpret_cast<const v4u32*>(p + k) : zero,
-                   left > 64 ? *reinterpret_cast<const v4u32*>(p + k + 64) : zero};
-    };
-    Codes ca[MT], cb[NT];
-    float s[NT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) ca[m] = fetch(wp[m]);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      cb[n] = fetch(xp[n]);
-      s[n] = sp[n][g] * sw[g];
-    }
-    Frag<F32> fa[MT], fb[NT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) fa[m].set(ca[m]);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) fb[n].set(cb[n]);
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const f32x4 p = product(fa[m], fb[n]);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) acc[m][n][x] = fmaf(p[x], s[n], acc[m][n][x]);
-      }
-  }
-  // acc[m][n][x]: token i0 + 16 m + 4 q + x of row j0 + 16 n + l16
-  if (wave > 0)
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(&sh[wave - 1][n * 16 + l16][m * 16 + q * 4]) = acc[m][n];
-  __syncthreads();
-  if (wave > 0) return;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int j = j0 + n * 16 + l16;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int w = 0; w < KW - 1; ++w) acc[m][n] += *reinterpret_cast<const f32x4*>(&sh[w][n * 16 + l16][m * 16 + q * 4]);
-      const int i = i0 + m * 16 + q * 4;
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (j < a.N && i + x < a.V) put<F32>(a.out, (size_t)j * a.V + i + x, acc[m][n][x]);
-    }
-  }
-}
-
 // 16 (or 4) bytes per lane from base + off to LDS at dst, a wave's lanes side by side.  The caller waits for it (vmcnt)
 // before the bytes are read: behind the builtin of this instruction the compiler would have the next LDS read wait for
 // all loads in flight, which left a step's loads no time (2048 rows x 151936, d = 4096: 1429 us, so 1228).
-template <int BYTES>
+template <int BYTES, bool ONCE = false>
 __device__ __forceinline__ void load_lds(const void* base, uint32_t off, SPEC_LDS char* dst) {
   static_assert(BYTES == 16 || BYTES == 4, "dwords");
   const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)dst);
   const uint64_t b = (uint64_t)base;   // in scalar registers, whichever unit it was computed in
   const uint64_t sb = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32 |
                       (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b);
-  if constexpr (BYTES == 16)
+  if constexpr (BYTES == 16 && ONCE)   // past the caches' ordinary replacement: read by no other workgroup
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(at), "v"(off), "s"(sb)
+                 : "memory", "m0");
+  else if constexpr (BYTES == 16)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(sb)
                  : "memory", "m0");
   else
@@ -202,7 +124,7 @@ __device__ __forceinline__ int xcd_tile(int bid, int total) {
 constexpr int kScaleSteps = 4;   // steps whose scales are loaded together
 constexpr int kPart = 2;         // of a thread's loads for a step, issued between two units
 
-// Many rows: tiles of BM tokens and BN rows, WM x WN waves.  A step is one block of k: 128 bytes of every row of the
+// Tiles of BM tokens and BN rows, WM x WN waves.  A step is one block of k: 128 bytes of every row of the
 // tile, brought to LDS directly (16 bytes per lane, chunk c of row r at c ^ (r & 7), so that the 16 rows that an
 // operand read touches fall into different banks), ST - 1 steps ahead, a few loads between two units (all of them at
 // once: 1221 us in place of 1153 on 2048 rows x 151936, d = 4096; later ones, one a unit: 1198).
@@ -210,15 +132,18 @@ constexpr int kPart = 2;         // of a thread's loads for a step, issued betwe
 // A wave goes through its MT operands of the vocabulary one after the other, each against the NT of the rows (a unit:
 // NT matrix instructions); while a unit runs, the unit before it is scaled and added and the operands of the next but
 // one are read from LDS.  The last two units of a step run behind the barrier, with the first reads of the next step.
-template <bool F32, int BM, int BN, int WM, int WN, int ST>
+template <bool F32, int BM, int BN, int WM, int WN, int ST, bool ONCE>
 __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs a, int ti, int tj) {
   constexpr int NW = WM * WN, NTHR = NW * 64, MT = BM / WM / 16, NT = BN / WN / 16;
-  constexpr int CA = BM * 8 / NTHR, CB = BN * 8 / NTHR, CS = BN * kScaleSteps / NTHR;
+  constexpr int CA = BM * 8 / NTHR, CB = BN * 8 / NTHR;
+  constexpr int SL = BN * kScaleSteps / 64, CS = (SL + NW - 1) / NW;   // loads of scales, and a wave's
   constexpr int STAGE = (BM + BN) * kStepBytes;
-  static_assert(MT >= 4 && BM / WM <= 128 && CS >= 1 && ST <= kScaleSteps && (CA + CB) <= kPart * MT, "tile");
+  static_assert(MT >= 4 && CB >= 1 && BM / WM <= 128 && SL >= 1 && (SL % NW == 0 || SL < NW) && ST <= kScaleSteps &&
+                    CA + CB <= kPart * MT, "tile");
   __shared__ __attribute__((aligned(128))) char lds_[ST * STAGE];
   __shared__ float sxs[2 * BN * kScaleSteps];
-  __shared__ float sws[(BM + 127) / 128][SPEC_MAX_HEAD_WIDTH / 128];
+  constexpr int WB = (BM + 127) / 128;   // blocks of the weight's scales that the tile lies in
+  __shared__ float sws[WB * SPEC_MAX_HEAD_WIDTH / 128];
   SPEC_LDS char* const lds = (SPEC_LDS char*)lds_;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wi = wave % WM, wj = wave / WM, l16 = lane & 15, q = lane >> 4;
@@ -243,7 +168,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
   auto stage = [&](int t) { return lds + (t % ST) * STAGE; };
   auto scales_of = [&](int t) { return (SPEC_LDS char*)sxs + t / kScaleSteps % 2 * (BN * kScaleSteps * 4); };
   auto issue_scales = [&](int t) {   // of steps t .. t + kScaleSteps - 1
-    if (t % kScaleSteps != 0) return;
+    if (t % kScaleSteps != 0 || (SL < NW && wave >= SL)) return;
     const int g = min(t + sg, nk - 1);
     SPEC_LDS char* dst = scales_of(t) + wave * 256;
 #pragma unroll
@@ -259,7 +184,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
     asm("" : "+s"(o));   // scalar base + 32-bit lane offset
 #pragma unroll
     for (int u = c * kPart; u < min((c + 1) * kPart, CA + CB); ++u) {
-      if (u < CA) load_lds<16>(A + o, row_a(u), dst + (u * NW + wave) * 1024);
+      if (u < CA) load_lds<16, ONCE>(A + o, row_a(u), dst + (u * NW + wave) * 1024);
       else load_lds<16>(B + o, row_b(u - CA), dst + BM * kStepBytes + ((u - CA) * NW + wave) * 1024);
     }
   };
@@ -298,7 +223,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
   auto read_a = [&](const SPEC_LDS char* st, int m) { ca[m] = read(st, ra + m * 16 * kStepBytes); };
   auto read_b = [&](const SPEC_LDS char* st, int n) { fb[n].set(read(st, rb + n * 16 * kStepBytes)); };
   auto read_s = [&](int t) {
-    const float w = sws[wi * (BM / WM) / 128][t];
+    const float w = sws[wi * (BM / WM) / 128 * nk + t];
     const SPEC_LDS float* x = reinterpret_cast<const SPEC_LDS float*>(scales_of(t)) + t % kScaleSteps + rs;
 #pragma unroll
     for (int n = 0; n < NT; ++n) s[n] = x[n * 16 * kScaleSteps] * w;
@@ -316,12 +241,12 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
     for (int n = 0; n < NT; ++n) p[m & 1][n] = product(fa, fb[n]);
   };
 
+  // the weight's scales of the tile, side by side in memory as in LDS
+  const int rest = ((a.V + 127) / 128 - i0 / 128) * nk - 1;
+  for (int k = wave * 64; k < WB * nk; k += NTHR)
+    load_lds<4>(a.sw + (size_t)(i0 / 128) * nk, (uint32_t)min(k + lane, rest) * 4, (SPEC_LDS char*)sws + k * 4);
 #pragma unroll
   for (int t = 0; t < ST; ++t) issue(t);
-  for (int k = tid; k < (BM + 127) / 128 * nk; k += NTHR) {
-    const int s = k / nk, g = k - s * nk, row = min(i0 / 128 + s, (a.V - 1) / 128);
-    sws[s][g] = a.sw[(size_t)row * nk + g];
-  }
   // units 0 .. MT - 3 of a step whose first operands are there
   auto head = [&](const SPEC_LDS char* cur, int t, bool whole) {
 #pragma unroll
@@ -421,23 +346,25 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
   }
 }
 
+template <bool F32, int BM, int BN, int WM, int WN, int ST, bool ONCE>
+void launch(const LogitArgs& a, hipStream_t s) {
+  const int ti = ceil_div(a.V, BM), tj = ceil_div(a.N, BN);
+  hipLaunchKernelGGL((logits_tile_kernel<F32, BM, BN, WM, WN, ST, ONCE>), dim3((unsigned)ti * (unsigned)tj),
+                     dim3(WM * WN * 64), 0, s, a, ti, tj);
+}
+
 template <bool F32>
 void run_logits(const LogitArgs& a, hipStream_t s) {
-  const unsigned gx = (unsigned)ceil_div(a.V, 64);
-  if (a.N <= 16) {
-    hipLaunchKernelGGL((logits_rows_kernel<F32, 1, 4>), dim3(gx, 1), dim3(256), 0, s, a);
-  } else if (a.N <= 32) {
-    hipLaunchKernelGGL((logits_rows_kernel<F32, 2, 4>), dim3(gx, 1), dim3(256), 0, s, a);
-  } else if (a.N <= 64) {
-    hipLaunchKernelGGL((logits_rows_kernel<F32, 4, 4>), dim3(gx, 1), dim3(256), 0, s, a);
-  } else {
-    constexpr int BM = F32 ? 128 : 256, BN = F32 ? 128 : 256;
-    const int ti = ceil_div(a.V, BM), tj = ceil_div(a.N, BN);
-    if constexpr (F32)
-      hipLaunchKernelGGL((logits_tile_kernel<true, 128, 128, 2, 2, 2>), dim3((unsigned)(ti * tj)), dim3(256), 0, s, a, ti, tj);
-    else
-      hipLaunchKernelGGL((logits_tile_kernel<false, 256, 256, 2, 4, 2>), dim3((unsigned)(ti * tj)), dim3(512), 0, s, a, ti, tj);
+  const int t = pick_logit_tile(F32, a.N, a.V, a.d);
+  if constexpr (!F32) {
+    if (t == kL256x256) return launch<false, 256, 256, 2, 4, 2, false>(a, s);
+    if (t == kL256x128) return launch<false, 256, 128, 4, 2, 3, false>(a, s);
   }
+  if (t == kL128x128) launch<F32, 128, 128, 2, 2, 2, false>(a, s);
+  else if (t == kL128x64) launch<F32, 128, 64, 2, 2, 3, true>(a, s);
+  else if (t == kL128x32) launch<F32, 128, 32, 2, 2, 3, true>(a, s);
+  else if (t == kL64x64) launch<F32, 64, 64, 1, 4, 4, false>(a, s);
+  else launch<F32, 64, 32, 1, 2, 4, false>(a, s);
 }
 
 }  // namespace
@@ -459,7 +386,7 @@ extern "C" int32_t spec_head_logits(int32_t N, int32_t V, int32_t d, int32_t dty
       overlap(logits_out, out, weight_scales, ceil_div(V, 128) * groups * sizeof(float)))
     return SPEC_ERR_INVALID_ARG;
   // the dispatch packet counts a launch's work-items in 32 bits
-  if ((long long)ceil_div(V, 64) * ceil_div(N, 64) * 256 > 0xffffffffll) return SPEC_ERR_UNSUPPORTED;
+  if ((long long)ceil_div(V, 64) * ceil_div(N, 32) * 128 > 0xffffffffll) return SPEC_ERR_UNSUPPORTED;
   const LogitArgs a{codes, scales, weight_codes, weight_scales, logits_out, N, V, d, (int)groups};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (dtype == SPEC_BF16) run_logits<false>(a, s);

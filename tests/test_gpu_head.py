@@ -28,6 +28,7 @@ import torch
 pytestmark = pytest.mark.gpu
 
 import oracle
+from logits_plans import PLANS
 
 DEV = "cuda:0"
 U = 2.0 ** -24 * (1 + 2.0 ** -10)
@@ -283,9 +284,17 @@ def test_logits(sv, shape, dtype):
     _check_logits(sv, *_as_codes(y, 1), *_as_codes(w, 128), DT[dtype])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", list(PLANS))
+def test_logits_of_every_tile(sv, shape, dtype):
+    print(f"tile {PLANS[shape]} {shape} {dtype}", flush=True)
+    y, w = _logit_inputs(sum(shape) + 1, *shape)
+    _check_logits(sv, *_as_codes(y, 1), *_as_codes(w, 128), DT[dtype])
+
+
 def test_logits_write_their_rows_alone(sv):
     """Odd rows of an odd vocabulary in the middle of a buffer: nothing around them is written."""
-    for N, V, d in ((5, 1003, 144), (70, 333, 272), (300, 1001, 128), (520, 777, 400)):
+    for N, V, d in ((5, 1003, 144), (70, 333, 272), (300, 20011, 128), (520, 40003, 400), (200, 9001, 272), (50, 40001, 144)):
         for dt in (torch.bfloat16, torch.float32):
             print(f"rows {N} {V} {d} {dt}", flush=True)
             y, w = _logit_inputs(3, N, V, d)

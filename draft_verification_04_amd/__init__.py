@@ -1059,33 +1059,49 @@ def _blocks(n):
     return -(-n // 128)
 
 
+def _ready(device, *wanted):
+    """Whether every (tensor, dtype, shape) that is there is a contiguous tensor of the kind on `device`.  The calls'
+    checks at once, a third of their time; where it says no, the single checks find out what is wrong."""
+    for t, dtype, shape in wanted:
+        if t is not None and not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
+                                  t.device == device and t.is_contiguous()):
+            return False
+    return True
+
+
+def _at(t):
+    """A device address as ctypes takes it."""
+    return None if t is None else t.data_ptr()
+
+
 def head_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
               quantize: bool = False, out: Optional[dict] = None, stream=None) -> dict:
     """spec_head_norm: h = x + residual and its root-mean-square norm, y = h / sqrt(mean(h^2) + eps) * weight.
 
     x and residual [N, d], weight [d] (all float32 or all bfloat16).  Returns dict(y [N, d], h [N, d] (x itself
     without a residual), rstd [N] float32); quantize (d a multiple of 16) gives codes [N, d] float8_e4m3fn and
-    scales [N, ceil(d / 128)] float32 in place of y.  `out` may hold x or the residual as its h or y.
+    scales [N, ceil(d / 128)] float32 in place of y and rstd.  `out` may hold x or the residual as its h or y (and
+    an rstd beside codes).
 
     No autograd graph is built: the gradients are head_norm_backward's.
     """
     lib = load_library()
     N, d = _rows(x, "x")
-    _vec(weight, "weight", d)
-    _shape(residual, "residual", (N, d))
-    _dev(x, "x", _FLOATS, 2)
-    _dev(weight, "weight", x.dtype, 1)
-    _dev(residual, "residual", x.dtype, 2)
-    dev = x.device
-    _on(dev, weight=weight, residual=residual)
+    dev, dt = x.device, x.dtype
+    if not (dt in _FLOATS and x.is_cuda and _ready(dev, (x, dt, (N, d)), (weight, dt, (d,)), (residual, dt, (N, d)))):
+        _vec(weight, "weight", d)
+        _shape(residual, "residual", (N, d))
+        _dev(x, "x", _FLOATS, 2)
+        _dev(weight, "weight", dt, 1)
+        _dev(residual, "residual", dt, 2)
+        _on(dev, weight=weight, residual=residual)
     mine = []
     if out is None:
-        out = dict(rstd=torch.empty(N, dtype=torch.float32, device=dev))
-        if quantize:
-            out["codes"] = torch.empty((N, d), dtype=_E4M3, device=dev)
-            out["scales"] = torch.empty((N, _blocks(d)), dtype=torch.float32, device=dev)
+        if quantize:   # for serving: nothing is kept for a gradient
+            out = dict(codes=torch.empty((N, d), dtype=_E4M3, device=dev),
+                       scales=torch.empty((N, _blocks(d)), dtype=torch.float32, device=dev))
         else:
-            out["y"] = torch.empty_like(x)
+            out = dict(y=torch.empty_like(x), rstd=torch.empty(N, dtype=torch.float32, device=dev))
         if residual is not None:
             out["h"] = torch.empty_like(x)
         mine.extend(out.values())
@@ -1094,8 +1110,8 @@ def head_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Te
                              scales=((N, _blocks(d)), torch.float32, quantize),
                              h=((N, d), x.dtype, residual is not None), rstd=((N,), torch.float32, False)), dev)
     code = _launch_on(dev, stream, mine, lambda sp: lib.spec_head_norm(
-        N, d, _logit_dtype(x), _ptr(x), _ptr(residual), _ptr(weight), float(eps), _ptr(out.get("h")),
-        _ptr(out.get("y")), _ptr(out.get("codes")), _ptr(out.get("scales")), _ptr(out.get("rstd")), sp))
+        N, d, _logit_dtype(x), _at(x), _at(residual), _at(weight), float(eps), _at(out.get("h")),
+        _at(out.get("y")), _at(out.get("codes")), _at(out.get("scales")), _at(out.get("rstd")), sp))
     _check("spec_head_norm", code)
     if residual is None and "h" not in out:
         out = dict(out, h=x)
@@ -1113,17 +1129,20 @@ def head_norm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Tens
     """
     lib = load_library()
     N, d = _rows(grad_y, "grad_y")
-    _shape(h, "h", (N, d))
-    _vec(weight, "weight", d)
-    _vec(rstd, "rstd", N)
-    _shape(grad_h, "grad_h", (N, d))
-    _dev(grad_y, "grad_y", _FLOATS, 2)
-    _dev(h, "h", grad_y.dtype, 2)
-    _dev(weight, "weight", grad_y.dtype, 1)
-    _dev(rstd, "rstd", torch.float32, 1)
-    _dev(grad_h, "grad_h", grad_y.dtype, 2)
-    dev = grad_y.device
-    _on(dev, h=h, weight=weight, rstd=rstd, grad_h=grad_h)
+    dev, dt = grad_y.device, grad_y.dtype
+    if not (dt in _FLOATS and grad_y.is_cuda and
+            _ready(dev, (grad_y, dt, (N, d)), (h, dt, (N, d)), (weight, dt, (d,)), (rstd, torch.float32, (N,)),
+                   (grad_h, dt, (N, d))) and h is not None and weight is not None and rstd is not None):
+        _shape(h, "h", (N, d))
+        _vec(weight, "weight", d)
+        _vec(rstd, "rstd", N)
+        _shape(grad_h, "grad_h", (N, d))
+        _dev(grad_y, "grad_y", _FLOATS, 2)
+        _dev(h, "h", dt, 2)
+        _dev(weight, "weight", dt, 1)
+        _dev(rstd, "rstd", torch.float32, 1)
+        _dev(grad_h, "grad_h", dt, 2)
+        _on(dev, h=h, weight=weight, rstd=rstd, grad_h=grad_h)
     mine = []
     if out is None:
         out = dict(grad_x=torch.empty_like(grad_y))
@@ -1136,8 +1155,8 @@ def head_norm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Tens
     if out.get("grad_weight") is not None:
         ws = _device_workspace(int(lib.spec_head_norm_backward_workspace_size(N, d)), dev, workspace, mine)
     code = _launch_on(dev, stream, mine, lambda sp: lib.spec_head_norm_backward(
-        N, d, _logit_dtype(grad_y), _ptr(grad_y), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(grad_h),
-        _ptr(out["grad_x"]), _ptr(out.get("grad_weight")), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+        N, d, _logit_dtype(grad_y), _at(grad_y), _at(h), _at(weight), _at(rstd), _at(grad_h),
+        _at(out["grad_x"]), _at(out.get("grad_weight")), _at(ws), 0 if ws is None else ws.numel() * ws.element_size(),
         sp))
     _check("spec_head_norm_backward", code)
     return out
@@ -1181,24 +1200,27 @@ def head_logits(codes: torch.Tensor, scales: torch.Tensor, weight_codes: torch.T
         raise ValueError("weight_codes must be [V, d] with the codes' d")
     V = weight_codes.shape[0]
     _int32(V=V)
-    _shape(scales, "scales", (N, _blocks(d)))
-    _shape(weight_scales, "weight_scales", (_blocks(V), _blocks(d)))
-    _shape(out, "out", (N, V))
+    G, dev, f32 = _blocks(d), codes.device, torch.float32
     if dtype not in _FLOATS:
         raise TypeError(f"logits are float32 or bfloat16, got {dtype}")
-    _dev(codes, "codes", _E4M3, 2)
-    _dev(weight_codes, "weight_codes", _E4M3, 2)
-    _dev(scales, "scales", torch.float32, 2)
-    _dev(weight_scales, "weight_scales", torch.float32, 2)
-    _dev(out, "out", _FLOATS, 2)
-    dev = codes.device
-    _on(dev, scales=scales, weight_codes=weight_codes, weight_scales=weight_scales, out=out)
+    if not (codes.is_cuda and scales is not None and weight_scales is not None and
+            _ready(dev, (codes, _E4M3, (N, d)), (scales, f32, (N, G)), (weight_codes, _E4M3, (V, d)),
+                   (weight_scales, f32, (_blocks(V), G)), (out, torch.bfloat16, (N, V)))):
+        _shape(scales, "scales", (N, G))
+        _shape(weight_scales, "weight_scales", (_blocks(V), G))
+        _shape(out, "out", (N, V))
+        _dev(codes, "codes", _E4M3, 2)
+        _dev(weight_codes, "weight_codes", _E4M3, 2)
+        _dev(scales, "scales", f32, 2)
+        _dev(weight_scales, "weight_scales", f32, 2)
+        _dev(out, "out", _FLOATS, 2)
+        _on(dev, scales=scales, weight_codes=weight_codes, weight_scales=weight_scales, out=out)
     mine = []
     if out is None:
         out = torch.empty((N, V), dtype=dtype, device=dev)
         mine.append(out)
     code = _launch_on(dev, stream, mine, lambda sp: lib.spec_head_logits(
-        N, V, d, _logit_dtype(out), _ptr(codes), _ptr(scales), _ptr(weight_codes), _ptr(weight_scales), _ptr(out), sp))
+        N, V, d, _logit_dtype(out), _at(codes), _at(scales), _at(weight_codes), _at(weight_scales), _at(out), sp))
     _check("spec_head_logits", code)
     return out
 
@@ -1241,41 +1263,45 @@ def adjust_logits(logits: torch.Tensor, draft_tokens: Optional[torch.Tensor] = N
         raise ValueError("history_len and prompt_len need a history")
     if history is not None and H == 0:   # of no tokens: the lengths can only be 0
         history = history_len = prompt_len = None
-    for name, t in (("lengths", lengths), ("history_len", history_len), ("prompt_len", prompt_len),
-                    ("repetition", repetition), ("frequency", frequency), ("presence", presence),
-                    ("mask_index", mask_index), ("status", status)):
-        _vec(t, name, B)
     offsets, tokens, values = bias if bias is not None else (None, None, None)
-    nb = 0
-    if bias is not None:
-        _vec(offsets, "bias offsets", B + 1)
-        nb = tokens.numel() if isinstance(tokens, torch.Tensor) else -1
-        _vec(tokens, "bias tokens", nb)
-        _vec(values, "bias values", nb)
+    nb = 0 if bias is None else tokens.numel() if isinstance(tokens, torch.Tensor) else -1
+    words = -(-V // 32)
     M = 0
     if mask is not None:
-        if not isinstance(mask, torch.Tensor) or mask.dim() != 3 or tuple(mask.shape[1:]) != (R, -(-V // 32)):
-            raise ValueError(f"mask must be [M, {R}, {-(-V // 32)}]")
+        if not isinstance(mask, torch.Tensor) or mask.dim() != 3 or tuple(mask.shape[1:]) != (R, words):
+            raise ValueError(f"mask must be [M, {R}, {words}]")
         M = mask.shape[0]
     elif mask_index is not None:
         raise ValueError("mask_index needs a mask")
-    _shape(out, "out", (B, R, V))
     _int32(B=B, R=R, V=V, H=H, nb=nb, M=M)
-    _dev(logits, "logits", _FLOATS, 3)
-    i32 = dict(draft_tokens=draft_tokens, lengths=lengths, history=history, history_len=history_len,
-               prompt_len=prompt_len, mask_index=mask_index, status=status)
-    f32 = dict(repetition=repetition, frequency=frequency, presence=presence)
-    if bias is not None:
-        i32.update(bias_offsets=offsets, bias_tokens=tokens)
-        f32.update(bias_values=values)
-    for name, t in i32.items():
-        _dev(t, name, torch.int32)
-    for name, t in f32.items():
-        _dev(t, name, torch.float32)
-    _dev(mask, "mask", (torch.int32, torch.uint32) if hasattr(torch, "uint32") else torch.int32)
-    _dev(out, "out", logits.dtype)
-    dev = logits.device
-    _on(dev, mask=mask, out=out, **i32, **f32)
+    dev, i32, f32, each = logits.device, torch.int32, torch.float32, (B,)
+    if not (logits.dtype in _FLOATS and logits.is_cuda and (bias is None or (offsets is not None and values is not None)) and
+            _ready(dev, (logits, logits.dtype, (B, R, V)), (draft_tokens, i32, (B, G)), (lengths, i32, each),
+                   (history, i32, (B, H)), (history_len, i32, each), (prompt_len, i32, each), (repetition, f32, each),
+                   (frequency, f32, each), (presence, f32, each), (offsets, i32, (B + 1,)), (tokens, i32, (nb,)),
+                   (values, f32, (nb,)), (mask, i32, (M, R, words)), (mask_index, i32, each),
+                   (out, logits.dtype, (B, R, V)), (status, i32, each))):
+        for name, t in (("lengths", lengths), ("history_len", history_len), ("prompt_len", prompt_len),
+                        ("repetition", repetition), ("frequency", frequency), ("presence", presence),
+                        ("mask_index", mask_index), ("status", status)):
+            _vec(t, name, B)
+        if bias is not None:
+            for name, t, n in (("bias offsets", offsets, B + 1), ("bias tokens", tokens, nb), ("bias values", values, nb)):
+                if t is None:
+                    raise ValueError(f"{name} are missing")
+                _vec(t, name, n)
+        _shape(out, "out", (B, R, V))
+        _dev(logits, "logits", _FLOATS, 3)
+        ints = dict(draft_tokens=draft_tokens, lengths=lengths, history=history, history_len=history_len,
+                    prompt_len=prompt_len, bias_offsets=offsets, bias_tokens=tokens, mask_index=mask_index, status=status)
+        floats = dict(repetition=repetition, frequency=frequency, presence=presence, bias_values=values)
+        for name, t in ints.items():
+            _dev(t, name, i32)
+        for name, t in floats.items():
+            _dev(t, name, f32)
+        _dev(mask, "mask", (i32, torch.uint32) if hasattr(torch, "uint32") else i32)
+        _dev(out, "out", logits.dtype)
+        _on(dev, mask=mask, out=out, **ints, **floats)
     if in_place and out is not None:
         raise ValueError("pass out or in_place, not both")
     mine = []
@@ -1291,8 +1317,8 @@ def adjust_logits(logits: torch.Tensor, draft_tokens: Optional[torch.Tensor] = N
     if nb == 0 and bias is not None:
         tokens, values = offsets, offsets
     code = _launch_on(dev, stream, mine, lambda sp: lib.spec_adjust_logits(
-        B, R, V, _logit_dtype(logits), _ptr(logits), G, _ptr(draft_tokens) if G else None, _ptr(lengths), _ptr(history), H,
-        _ptr(history_len), _ptr(prompt_len), _ptr(repetition), _ptr(frequency), _ptr(presence), _ptr(offsets),
-        _ptr(tokens), _ptr(values), nb, _ptr(mask), M, _ptr(mask_index), _ptr(out), _ptr(status), sp))
+        B, R, V, _logit_dtype(logits), logits.data_ptr(), G, _at(draft_tokens) if G else None, _at(lengths), _at(history),
+        H, _at(history_len), _at(prompt_len), _at(repetition), _at(frequency), _at(presence), _at(offsets), _at(tokens),
+        _at(values), nb, _at(mask), M, _at(mask_index), _at(out), _at(status), sp))
     _check("spec_adjust_logits", code)
     return dict(logits=out, status=status)

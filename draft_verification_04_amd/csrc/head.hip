@@ -8,7 +8,9 @@
 //
 // All of them are bound by memory: a row is read once into registers (16 values a thread at most, 8 of them in a
 // row), and everything else is done there.  16 lanes hold 128 values, one group of the scales: its amax is a
-// reduction within a DPP row.
+// reduction within a DPP row.  A team of T threads takes a row; a workgroup has 256 threads or one team.
+// MI355X, bf16 with a residual: 4352 x 4096 to 8 bits 23-25 us (5.0-5.4 TB/s; a large copy runs at 4.8); 8192 x 4096
+// forward 50 us and backward 51 + 5 (5.3 TB/s); weight of 151936 x 4096 to 8 bits 317-322 us (5.8 TB/s).
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -40,7 +42,7 @@ struct NormArgs {
   uint8_t* codes;   // [N, d]
   float* scales;    // [N, groups]
   float* rstd;
-  int d, groups;
+  int N, d, groups;
   float eps;
 };
 
@@ -55,32 +57,40 @@ struct BackArgs {
   int N, d;
 };
 
+// 16 bytes at an address of that alignment: rows that are no multiple of 16 bytes start anywhere.
+template <int ALIGN>
+struct __attribute__((packed, aligned(ALIGN))) Piece {
+  v4u32 v;
+};
+
 // 8 consecutive values of a row from index c; zeros past d.  VEC: the rows are multiples of 16 bytes.
 template <bool BF16, bool VEC>
 __device__ __forceinline__ void load8(const void* p, size_t row, int c, int d, float (&v)[8]) {
+  constexpr int ES = BF16 ? 2 : 4;
+  const char* src = reinterpret_cast<const char*>(p) + (row + c) * ES;
 #pragma unroll
   for (int x = 0; x < 8; ++x) v[x] = 0.f;
-  if constexpr (VEC && BF16) {
-    if (c < d) {
-      const v4u32 t = *reinterpret_cast<const v4u32*>(reinterpret_cast<const uint16_t*>(p) + row + c);
+  if (c + 8 <= d || (VEC && !BF16 && c + 4 <= d)) {
+    const v4u32 t = reinterpret_cast<const Piece<VEC ? 16 : ES>*>(src)->v;
+    if constexpr (BF16) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         v[2 * x] = bf16_lo(t[x]);
         v[2 * x + 1] = bf16_hi(t[x]);
       }
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[x] = __uint_as_float(t[x]);
+      if (!VEC || c + 8 <= d) {
+        const v4u32 u = reinterpret_cast<const Piece<VEC ? 16 : ES>*>(src + 16)->v;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[4 + x] = __uint_as_float(u[x]);
+      }
     }
-  } else if constexpr (VEC) {
+  } else if (!VEC) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      if (c + 4 * q >= d) break;
-      const v4u32 t = *reinterpret_cast<const v4u32*>(reinterpret_cast<const float*>(p) + row + c + 4 * q);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) v[4 * q + x] = __uint_as_float(t[x]);
-    }
-  } else {
-#pragma unroll
-    for (int x = 0; x < 8; ++x)
-      if (c + x < d) v[x] = load_elem<BF16>(p, (int64_t)(row + c + x));
+    for (int x = 0; x < 7; ++x)
+      if (c + x < d) v[x] = load_elem<BF16>(src, x);
   }
 }
 
@@ -88,56 +98,68 @@ __device__ __forceinline__ uint32_t bf16_bits(float x) { return __builtin_bit_ca
 
 template <bool BF16, bool VEC>
 __device__ __forceinline__ void store8(void* p, size_t row, int c, int d, const float (&v)[8]) {
-  if constexpr (VEC && BF16) {
-    if (c < d) {
-      v4u32 t;
+  constexpr int ES = BF16 ? 2 : 4;
+  char* dst = reinterpret_cast<char*>(p) + (row + c) * ES;
+  if (c + 8 <= d || (VEC && !BF16 && c + 4 <= d)) {
+    v4u32 t;
+    if constexpr (BF16) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) t[x] = bf16_bits(v[2 * x]) | bf16_bits(v[2 * x + 1]) << 16;
-      *reinterpret_cast<v4u32*>(reinterpret_cast<uint16_t*>(p) + row + c) = t;
-    }
-  } else if constexpr (VEC) {
+      reinterpret_cast<Piece<VEC ? 16 : ES>*>(dst)->v = t;
+    } else {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      if (c + 4 * q >= d) break;
-      *reinterpret_cast<v4u32*>(reinterpret_cast<float*>(p) + row + c + 4 * q) =
-          v4u32{__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
-                __float_as_uint(v[4 * q + 3])};
-    }
-  } else {
+      for (int x = 0; x < 4; ++x) t[x] = __float_as_uint(v[x]);
+      reinterpret_cast<Piece<VEC ? 16 : ES>*>(dst)->v = t;
+      if (!VEC || c + 8 <= d) {
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
+        for (int x = 0; x < 4; ++x) t[x] = __float_as_uint(v[4 + x]);
+        reinterpret_cast<Piece<VEC ? 16 : ES>*>(dst + 16)->v = t;
+      }
+    }
+  } else if (!VEC) {
+#pragma unroll
+    for (int x = 0; x < 7; ++x) {
       if (c + x >= d) break;
-      if constexpr (BF16) reinterpret_cast<uint16_t*>(p)[row + c + x] = (uint16_t)bf16_bits(v[x]);
-      else reinterpret_cast<float*>(p)[row + c + x] = v[x];
+      if constexpr (BF16) reinterpret_cast<uint16_t*>(dst)[x] = (uint16_t)bf16_bits(v[x]);
+      else reinterpret_cast<float*>(dst)[x] = v[x];
     }
   }
 }
 
-// Sum over the workgroup, in wave order; `sh` holds a word per wave and is free until the next but one call
-// where the callers alternate between two.
+constexpr int kWorkgroup = 256;   // threads, where a team has fewer
+constexpr int teams(int T) { return T < kWorkgroup ? kWorkgroup / T : 1; }
+
+// Sum over the thread's team, in wave order; `sh` holds a word per wave of the workgroup and is free until the next but
+// one call where the callers alternate between two.
 template <int T>
-__device__ __forceinline__ float block_sum(float x, float* sh) {
+__device__ __forceinline__ float team_sum(float x, float* sh) {
   x = wave_reduce(x, [](float a, float b) { return a + b; });
   if constexpr (T == SPEC_WAVE) return x;
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
+  constexpr int NW = T / SPEC_WAVE;
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) sh[wave] = x;
   __syncthreads();
+  sh += wave / NW * NW;
   float s = sh[0];
 #pragma unroll
-  for (int w = 1; w < T / SPEC_WAVE; ++w) s += sh[w];
+  for (int w = 1; w < NW; ++w) s += sh[w];
   return s;
 }
 
 // Largest magnitude as its bits: NaN above infinity above every finite value.
 template <int T>
-__device__ __forceinline__ uint32_t block_amax(uint32_t x, float* sh) {
+__device__ __forceinline__ uint32_t team_amax(uint32_t x, float* sh) {
   x = wave_reduce(x, [](uint32_t a, uint32_t b) { return max(a, b); });
   if constexpr (T == SPEC_WAVE) return x;
+  constexpr int NW = T / SPEC_WAVE;
+  const int wave = threadIdx.x >> 6;
   uint32_t* s = reinterpret_cast<uint32_t*>(sh);
-  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
+  if ((threadIdx.x & 63) == 0) s[wave] = x;
   __syncthreads();
+  s += wave / NW * NW;
   uint32_t m = s[0];
 #pragma unroll
-  for (int w = 1; w < T / SPEC_WAVE; ++w) m = max(m, s[w]);
+  for (int w = 1; w < NW; ++w) m = max(m, s[w]);
   return m;
 }
 
@@ -150,10 +172,11 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 }
 
 template <bool BF16, bool VEC, bool Q8, int T, int K>
-__global__ __launch_bounds__(T) void norm_kernel(NormArgs a) {
-  __shared__ float sh[2][T / SPEC_WAVE];
-  const int tid = threadIdx.x, d = a.d;
-  const size_t row = (size_t)blockIdx.x * d;
+__global__ __launch_bounds__(T * teams(T)) void norm_kernel(NormArgs a) {
+  __shared__ float sh[4][T * teams(T) / SPEC_WAVE];
+  const int tid = threadIdx.x % T, d = a.d, n = (int)blockIdx.x * teams(T) + threadIdx.x / T;
+  const bool live = n < a.N;   // past the last row: its values again, nothing stored
+  const size_t row = (size_t)min(n, a.N - 1) * d;
   float v[K][8], w[K][8];
 #pragma unroll
   for (int k = 0; k < K; ++k) load8<BF16, VEC>(a.x, row, (k * T + tid) * 8, d, v[k]);
@@ -169,7 +192,7 @@ __global__ __launch_bounds__(T) void norm_kernel(NormArgs a) {
 #pragma unroll
   for (int k = 0; k < K; ++k) load8<BF16, VEC>(a.w, 0, (k * T + tid) * 8, d, w[k]);
   // the norm is taken of the sum in fp32; only what is stored of it is rounded
-  if (a.h)
+  if (a.h && live)
 #pragma unroll
     for (int k = 0; k < K; ++k) store8<BF16, VEC>(a.h, row, (k * T + tid) * 8, d, v[k]);
   float ss = 0.f;
@@ -177,34 +200,37 @@ __global__ __launch_bounds__(T) void norm_kernel(NormArgs a) {
   for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int x = 0; x < 8; ++x) ss += v[k][x] * v[k][x];
-  ss = block_sum<T>(ss, sh[0]);
+  ss = team_sum<T>(ss, sh[0]);
   float rs = 1.f / sqrtf(ss / (float)d + a.eps), rstd = rs;
-  if (!(ss >= 0x1p-90f && ss <= 0x1p120f)) {
+  bool off = !(ss >= 0x1p-90f && ss <= 0x1p120f);
+  if (T == SPEC_WAVE ? off : __syncthreads_or(off)) {
     // the squares left fp32's range (or nearly): taken again of the row scaled by a power of two
     uint32_t m = 0;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int x = 0; x < 8; ++x) m = max(m, magnitude(v[k][x]));
-    m = block_amax<T>(m, sh[1]);
-    if (m != 0 && m < 0x7f800000u) {
-      const int e = ilogbf(__uint_as_float(m));
-      ss = 0.f;
+    m = team_amax<T>(m, sh[1]);
+    off = off && m != 0 && m < 0x7f800000u;
+    const int e = off ? ilogbf(__uint_as_float(m)) : 0;
+    float sq = 0.f;
 #pragma unroll
-      for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          v[k][x] = ldexpf(v[k][x], -e);
-          ss += v[k][x] * v[k][x];
-        }
-      __syncthreads();   // sh[0] and sh[1] are read
-      ss = block_sum<T>(ss, sh[0]);
-      const double r = 1.0 / sqrt(ldexp((double)ss / d, 2 * e) + (double)a.eps);
+      for (int x = 0; x < 8; ++x) {
+        const float y = ldexpf(v[k][x], -e);
+        sq += y * y;
+        if (off) v[k][x] = y;
+      }
+    sq = team_sum<T>(sq, sh[2]);
+    if (off) {
+      const double r = 1.0 / sqrt(ldexp((double)sq / d, 2 * e) + (double)a.eps);
       rs = (float)ldexp(r, e);
       rstd = (float)r;
     }
   }
-  if (a.rstd && tid == 0) a.rstd[blockIdx.x] = rstd;
+  if (!live) return;
+  if (a.rstd && tid == 0) a.rstd[n] = rstd;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c = (k * T + tid) * 8;
@@ -228,30 +254,35 @@ __global__ __launch_bounds__(T) void norm_kernel(NormArgs a) {
         q.x = codes4(v[k][0] * r, v[k][1] * r, v[k][2] * r, v[k][3] * r);
         q.y = codes4(v[k][4] * r, v[k][5] * r, v[k][6] * r, v[k][7] * r);
         *reinterpret_cast<v2u32*>(a.codes + row + c) = q;
-        if ((tid & 15) == 0) a.scales[(size_t)blockIdx.x * a.groups + (c >> 7)] = amax / kCodeMax;
+        if ((tid & 15) == 0) a.scales[(size_t)n * a.groups + (c >> 7)] = amax / kCodeMax;
       }
     }
   }
 }
 
-// Rows blockIdx.x, blockIdx.x + gridDim.x, ...; the weight and its gradient's share stay in registers.
+// Every gridDim.x-th group of a row per team; the weight and its gradient's share stay in registers, and the teams'
+// shares are added at the end.
 template <bool BF16, bool VEC, int T, int K>
-__global__ __launch_bounds__(T) void norm_backward_kernel(BackArgs a) {
-  __shared__ float sh[2][T / SPEC_WAVE];
-  const int tid = threadIdx.x, d = a.d;
+__global__ __launch_bounds__(T * teams(T)) void norm_backward_kernel(BackArgs a) {
+  constexpr int TEAMS = teams(T);
+  __shared__ float sh[2][T * TEAMS / SPEC_WAVE];
+  __shared__ float share[TEAMS > 1 ? TEAMS - 1 : 1][TEAMS > 1 ? 8 * K * T : 1];
+  const int tid = threadIdx.x % T, team = threadIdx.x / T, d = a.d;
   float w[K][8], dw[K][8] = {};
 #pragma unroll
   for (int k = 0; k < K; ++k) load8<BF16, VEC>(a.w, 0, (k * T + tid) * 8, d, w[k]);
   int turn = 0;
-  for (int n = blockIdx.x; n < a.N; n += gridDim.x, turn ^= 1) {
-    const size_t row = (size_t)n * d;
-    const float rstd = a.rstd[n];
+  for (int n0 = (int)blockIdx.x * TEAMS; n0 < a.N; n0 += (int)gridDim.x * TEAMS, turn ^= 1) {
+    const int n = n0 + team;
+    const bool live = n < a.N;
+    const size_t row = (size_t)min(n, a.N - 1) * d;
+    const float rstd = a.rstd[min(n, a.N - 1)];
     float gy[K][8], xh[K][8], gh[K][8];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       load8<BF16, VEC>(a.grad_y, row, (k * T + tid) * 8, d, gy[k]);
       load8<BF16, VEC>(a.h, row, (k * T + tid) * 8, d, xh[k]);
-      // single values take an address each: behind the sum, or the registers do not do
+      // unaligned: behind the sum, or the registers do not do
       if (VEC && a.grad_h) load8<BF16, VEC>(a.grad_h, row, (k * T + tid) * 8, d, gh[k]);
     }
     float dot = 0.f;
@@ -260,11 +291,12 @@ __global__ __launch_bounds__(T) void norm_backward_kernel(BackArgs a) {
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
         xh[k][x] *= rstd;
-        dw[k][x] += gy[k][x] * xh[k][x];
+        if (TEAMS == 1 || live) dw[k][x] += gy[k][x] * xh[k][x];
         gy[k][x] *= w[k][x];
         dot += gy[k][x] * xh[k][x];
       }
-    dot = block_sum<T>(dot, sh[turn]) / (float)d;
+    dot = team_sum<T>(dot, sh[turn]) / (float)d;
+    if (TEAMS > 1 && !live) continue;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (!VEC && a.grad_h) load8<BF16, VEC>(a.grad_h, row, (k * T + tid) * 8, d, gh[k]);
@@ -276,9 +308,24 @@ __global__ __launch_bounds__(T) void norm_backward_kernel(BackArgs a) {
       store8<BF16, VEC>(a.grad_x, row, (k * T + tid) * 8, d, gy[k]);
     }
   }
-  if (a.part)
+  if (!a.part) return;
+  if constexpr (TEAMS > 1) {
+    if (team > 0)
 #pragma unroll
-    for (int k = 0; k < K; ++k) store8<false, VEC>(a.part, (size_t)blockIdx.x * d, (k * T + tid) * 8, d, dw[k]);
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) share[team - 1][(k * 8 + x) * T + tid] = dw[k][x];
+    __syncthreads();
+    if (team > 0) return;
+#pragma unroll
+    for (int q = 0; q < TEAMS - 1; ++q)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) dw[k][x] += share[q][(k * 8 + x) * T + tid];
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) store8<false, VEC>(a.part, (size_t)blockIdx.x * d, (k * T + tid) * 8, d, dw[k]);
 }
 
 // grad_w: the workgroups' shares in order, in fp64, rounded once.
@@ -315,7 +362,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const void* w, int V, int
   for (int u = 0; u < 8; ++u)
 #pragma unroll
     for (int x = 0; x < 8; ++x) m = max(m, magnitude(v[u][x]));
-  const float amax = __uint_as_float(block_amax<256>(m, sh));
+  const float amax = __uint_as_float(team_amax<256>(m, sh));
   // w 448 / amax to the nearest fp32 (a quotient of two bf16 values often lies halfway between two codes, where the
   // last bit decides): both scaled to amax in [1, 2), one correction of the product with the reciprocal
   const int e = ilogbf(amax);
@@ -366,7 +413,11 @@ bool norm_ok(int N, int d, int dtype) {
 
 bool vector_rows(int d, int dtype) { return d * (dtype == SPEC_BF16 ? 2 : 4) % 16 == 0; }
 
-int back_groups(int N) { return N < kBackGroups ? N : kBackGroups; }
+// Workgroups of the backward kernel: what its rows need, at most kBackGroups (512: 8192 x 4096 bf16 54 us, 1024: 51).
+int back_groups(int N, int d) {
+  const int rows = d <= 1024 ? teams(64) : d <= 2048 ? teams(128) : 1, groups = ceil_div(N, rows);
+  return groups < kBackGroups ? groups : kBackGroups;
+}
 
 int32_t launched() { return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ERR_HIP; }
 
@@ -398,21 +449,23 @@ extern "C" int32_t spec_head_norm(int32_t N, int32_t d, int32_t dtype, const voi
   for (int i = 0; i < 5; ++i)
     for (int j = 0; j < i; ++j)
       if (overlap(outs[i].first, outs[i].second, outs[j].first, outs[j].second)) return SPEC_ERR_INVALID_ARG;
-  const NormArgs a{x, residual, weight, h_out, y_out, codes_out, scales_out, rstd_out, d, (int)groups, eps};
+  const NormArgs a{x, residual, weight, h_out, y_out, codes_out, scales_out, rstd_out, N, d, (int)groups, eps};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   with_shape(d, [&](auto T, auto K) {
     with_type(dtype, vector_rows(d, dtype), [&](auto BF, auto VEC) {
+      constexpr int rows = teams(T());
+      const dim3 grid(ceil_div(N, rows)), block(T() * rows);
       if (!codes_out)
-        hipLaunchKernelGGL((norm_kernel<BF(), VEC(), false, T(), K()>), dim3(N), dim3(T()), 0, s, a);
+        hipLaunchKernelGGL((norm_kernel<BF(), VEC(), false, T(), K()>), grid, block, 0, s, a);
       else if constexpr (VEC())   // multiples of 16 values
-        hipLaunchKernelGGL((norm_kernel<BF(), true, true, T(), K()>), dim3(N), dim3(T()), 0, s, a);
+        hipLaunchKernelGGL((norm_kernel<BF(), true, true, T(), K()>), grid, block, 0, s, a);
     });
   });
   return launched();
 }
 
 extern "C" size_t spec_head_norm_backward_workspace_size(int32_t N, int32_t d) {
-  return norm_ok(N, d, SPEC_F32) ? round256((size_t)back_groups(N) * round_to(d, 4) * sizeof(float)) : 0;
+  return norm_ok(N, d, SPEC_F32) ? round256((size_t)back_groups(N, d) * round_to(d, 4) * sizeof(float)) : 0;
 }
 
 extern "C" int32_t spec_head_norm_backward(int32_t N, int32_t d, int32_t dtype, const void* grad_y, const void* h,
@@ -433,13 +486,13 @@ extern "C" int32_t spec_head_norm_backward(int32_t N, int32_t d, int32_t dtype, 
   for (auto [p, m] : {std::pair<const void*, size_t>{grad_y, bytes}, {h, bytes}, {grad_h, bytes}, {weight, wbytes},
                       {rstd, N * sizeof(float)}})
     if (overlap(grad_weight, wbytes, p, m)) return SPEC_ERR_INVALID_ARG;
-  const int P = back_groups(N);
+  const int P = back_groups(N, d);
   const BackArgs a{grad_y, h, weight, rstd, grad_h, grad_x, grad_weight ? reinterpret_cast<float*>(workspace) : nullptr,
                    N, d};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   with_shape(d, [&](auto T, auto K) {
     with_type(dtype, vector_rows(d, dtype), [&](auto BF, auto VEC) {
-      hipLaunchKernelGGL((norm_backward_kernel<BF(), VEC(), T(), K()>), dim3(P), dim3(T()), 0, s, a);
+      hipLaunchKernelGGL((norm_backward_kernel<BF(), VEC(), T(), K()>), dim3(P), dim3(T() * teams(T())), 0, s, a);
     });
   });
   if (grad_weight) {

@@ -762,7 +762,7 @@ int32_t spec_head_xent_backward(int32_t N, int32_t V, int32_t d, int32_t dtype, 
  *   each rounded once to `dtype`.  h is the stored sum (x where there was no
  *   residual), rstd the forward call's.  grad_x may be grad_y, h or grad_h itself.
  *   Sums over rows are fp32 within a workgroup's share (at most ceil(N / 1024)
- *   rows), then fp64 in a fixed order: results do not depend on scheduling.
+ *   rows or 4), then fp64 in a fixed order: results do not depend on scheduling.
  *   workspace    for grad_weight: at least
  *                spec_head_norm_backward_workspace_size(N, d) bytes, 256-byte aligned,
  *                owned by the caller, busy until the call's kernels finish on `stream`

@@ -53,6 +53,7 @@ def parse():
     p.add_argument("--no-overlap", action="store_true", help="skip the overlap-mass measurement")
     p.add_argument("--no-draft", action="store_true", help="skip the draft-sampler measurement")
     p.add_argument("--no-sts", action="store_true", help="skip the temperature-scaling measurement")
+    p.add_argument("--no-head", action="store_true", help="skip the measurement from hidden states to logits")
     p.add_argument("--two-calls", action="store_true",
                    help="scheduler and verification as two calls instead of spec_schedule_verify")
     p.add_argument("--left-to-right", action="store_true",
@@ -180,6 +181,7 @@ def main():
     if not args.no_draft:
         draft = draft_leg(sv, torch, oracle, dev, stream, with_cpu=not args.no_cpu)
     sts = None if args.no_sts else sts_leg(sv, torch, oracle, dev, stream, with_cpu=not args.no_cpu)
+    head = None if args.no_head or greedy else head_leg(sv, torch, w, stream)
 
     if args.calibrate_copy:
         a = torch.empty(1 << 30, dtype=torch.uint8, device=dev)
@@ -240,6 +242,7 @@ def main():
         "async_scheduler": async_sched,
         "draft_sampler": draft,
         "temperature_scaling": sts,
+        "hidden_states_to_logits": head,
         "device": {"name": props.name, "arch": getattr(props, "gcnArchName", None),
                    "compute_units": props.multi_processor_count, "hbm_bytes": props.total_memory},
         "ms_breakdown": {"stream_kernel": ms_stream, "rest_of_step": ms_step - ms_stream},
@@ -389,6 +392,50 @@ def overlap_leg(sv, torch, w, copies, lengths, stream, reps=20):
     return {"ms_per_call": ms, "positions": pos, "positions_per_s": pos / (ms * 1e-3),
             "rows_per_pass": 2 * pos, "bytes_read_per_call": 2 * once,
             "gbps_read": 2 * once / (ms * 1e-3) / 1e9, "algorithmic_bytes_once": once}
+
+
+def head_leg(sv, torch, w, stream, requests=64, d=4096, reps=10):
+    """From hidden states to verified tokens for `requests` blocks of the workload's shape: spec_head_norm (8-bit
+    output), spec_head_logits, spec_adjust_logits in place (histories of 2048 tokens), spec_verify.  Each call's time
+    by HIP events, not part of the step."""
+    from draft_verification_04_amd.hipevents import HipEvent
+    dev, V, G = w.target.device, w.V, w.gamma
+    B = min(requests, w.B)
+    R, N = G + 1, B * (G + 1)
+    g = torch.Generator(device=dev)
+    g.manual_seed(4242)
+    x, r = (torch.randn((N, d), generator=g, device=dev).to(torch.bfloat16) for _ in range(2))
+    weight = torch.ones(d, dtype=torch.bfloat16, device=dev)
+    full = torch.empty((V, d), dtype=torch.bfloat16, device=dev).normal_(0.0, 3.0 / d ** 0.5, generator=g)
+    k = sv.head_quantize(full)
+    del full
+    logits = torch.empty((B, R, V), dtype=torch.bfloat16, device=dev)
+    hist = torch.randint(V, (B, 2048), generator=g, device=dev).to(torch.int32)
+    ones = torch.ones(B, device=dev)
+    repetition, frequency = 1.1 * ones, 0.1 * ones
+    draft, toks = w.draft[:B].contiguous(), w.draft_tokens[:B].contiguous()
+    norm = sv.head_norm(x, weight, r, quantize=True)
+    steps = {
+        "norm_to_8_bits": lambda: sv.head_norm(x, weight, r, quantize=True, out=norm, stream=stream),
+        "logits": lambda: sv.head_logits(norm["codes"], norm["scales"], k["codes"], k["scales"], out=logits.view(N, V),
+                                         stream=stream),
+        "adjust_in_place": lambda: sv.adjust_logits(logits, toks, history=hist, repetition=repetition,
+                                                    frequency=frequency, in_place=True, stream=stream),
+        "verify": lambda: sv.verify(logits, draft, toks, None, ones, None, None, stream=stream),
+    }
+    ms = dict.fromkeys(steps, 0.0)
+    for rep in range(reps + 2):
+        for name, call in steps.items():
+            e0, e1 = HipEvent(), HipEvent()
+            e0.record(stream)
+            call()
+            e1.record(stream)
+            torch.cuda.synchronize()
+            if rep >= 2:
+                ms[name] += e0.elapsed_ms(e1) / reps
+    total = sum(ms.values())
+    return {"requests": B, "rows": N, "V": V, "d": d, "ms": ms, "ms_total": total, "rows_per_s": N / (total * 1e-3),
+            "logits_tflops": 2.0 * N * V * d / (ms["logits"] * 1e-3) / 1e12}
 
 
 def draft_leg(sv, torch, oracle, dev, stream, reps=10, with_cpu=True):

@@ -90,12 +90,14 @@ __device__ __forceinline__ f32x4 product(const Frag<true>& a, const Frag<true>& 
 
 // 16 (or 4) bytes per lane from base + off to LDS at dst, a wave's lanes side by side.  The caller waits for it (vmcnt)
 // before the bytes are read: behind the builtin of this instruction the compiler would have the next LDS read wait for
-// all loads in flight, which left a step's loads no time (2048 rows x 151936, d = 4096: 1429 us, so 1228).
+// all loads in flight, which left a step's loads no time (2048 rows x 151936, d = 4096: 1429 us, so 1228).  The
+// base comes from the scalar unit: one that the vector unit wrote could be used five instructions later at the earliest,
+// which the compiler does not see to here.
 template <int BYTES, bool ONCE = false>
 __device__ __forceinline__ void load_lds(const void* base, uint32_t off, SPEC_LDS char* dst) {
   static_assert(BYTES == 16 || BYTES == 4, "dwords");
   const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)dst);
-  const uint64_t b = (uint64_t)base;   // in scalar registers, whichever unit it was computed in
+  const uint64_t b = (uint64_t)base;   // in scalar registers
   const uint64_t sb = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32 |
                       (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b);
   if constexpr (BYTES == 16 && ONCE)   // past the caches' ordinary replacement: read by no other workgroup
@@ -150,7 +152,8 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
   // bands of up to 8 tiles of rows: the workgroups of an XCD share a few strips of either operand in its L2
   const int tile = xcd_tile((int)blockIdx.x, ti * tj), band = tile / (8 * ti), in = tile - band * 8 * ti;
   const int bw = min(8, tj - band * 8);
-  const int i0 = __builtin_amdgcn_readfirstlane(in / bw * BM), j0 = __builtin_amdgcn_readfirstlane((band * 8 + in % bw) * BN);
+  int i0 = __builtin_amdgcn_readfirstlane(in / bw * BM), j0 = __builtin_amdgcn_readfirstlane((band * 8 + in % bw) * BN);
+  asm volatile("s_nop 4" : "+s"(i0), "+s"(j0));   // the vector unit's part in the loads' bases ends here
   const int nk = a.groups, full = a.d / kStepBytes, rem = a.d % kStepBytes;
 
   const int lr = lane >> 3, lc = ((lane & 7) ^ lr) * 16;
@@ -386,7 +389,7 @@ extern "C" int32_t spec_head_logits(int32_t N, int32_t V, int32_t d, int32_t dty
       overlap(logits_out, out, weight_scales, ceil_div(V, 128) * groups * sizeof(float)))
     return SPEC_ERR_INVALID_ARG;
   // the dispatch packet counts a launch's work-items in 32 bits
-  if ((long long)ceil_div(V, 64) * ceil_div(N, 32) * 128 > 0xffffffffll) return SPEC_ERR_UNSUPPORTED;
+  if (logit_work_items(pick_logit_tile(dtype == SPEC_F32, N, V, d), N, V) > 0xffffffffll) return SPEC_ERR_UNSUPPORTED;
   const LogitArgs a{codes, scales, weight_codes, weight_scales, logits_out, N, V, d, (int)groups};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (dtype == SPEC_BF16) run_logits<false>(a, s);

@@ -41,6 +41,12 @@ inline LogitTile logit_tile(int t, bool f32) {
   return f32 ? fp32[t] : bf16[t];
 }
 
+inline long long logit_work_items(int t, int N, int V) {
+  constexpr int threads[kLogitTiles] = {512, 512, 256, 256, 256, 256, 128};
+  const LogitTile p = logit_tile(t, false);
+  return (long long)ceil_div(V, p.bm) * ceil_div(N, p.bn) * threads[t];
+}
+
 inline double logit_us(int t, bool f32, int N, int V, int d) {
   const LogitTile p = logit_tile(t, f32);
   const long long tj = ceil_div(N, p.bn), tiles = ceil_div(V, p.bm) * tj, rounds = tiles / p.slots, rest = tiles % p.slots;

@@ -326,10 +326,11 @@ void launch(const AdjustArgs& a, int B, hipStream_t s) {
   hipLaunchKernelGGL((adjust_kernel<BF16, BIAS, MODE, S, T, U>), grid, dim3(T), 0, s, a);
 }
 
-// Slices of 4096 tokens, one row of it in LDS at a time (two: 98 in place of 91 us out of place on 64 blocks of 17 rows
-// of 151936 bf16, half of them live; slices of 2048: 100, of 8192: 109): 24 waves a CU or more.  Every slice's workgroup reads the
-// whole history, and from some 8000 tokens on half as many slices are faster, where their LDS leaves two workgroups
-// to a CU (96 x 8 rows of 129280 after 30011 tokens: 120 -> 108 us; after 1000: 74 -> 77).
+// Slices of 4096 tokens by 512 threads, one row of it in LDS at a time: 24 waves a CU or more (64 blocks of 17 rows of
+// 151936 bf16, half of them live, out of place: 90 us; two rows at a time 98; slices of 2048 by 256 threads 96, of
+// 8192 by 1024 118).  Every slice's workgroup reads the whole history, and from some 8000 tokens on half as many
+// slices are faster, where their LDS leaves two workgroups to a CU (96 x 8 rows of 129280 after 30011 tokens:
+// 120 -> 108 us; after 1000: 74 -> 77).
 // In place, listed tokens cost 30 ps a row where they lie in memory, and a row's slice through LDS 1 ps a token: where
 // the history can name a thirtieth of the vocabulary the row goes through LDS.
 template <bool BF16, bool BIAS>
@@ -380,8 +381,8 @@ extern "C" int32_t spec_adjust_logits(int32_t B, int32_t R, int32_t V, int32_t d
                       {mask, (size_t)masks * R * words * sizeof(uint32_t)}, {mask_index, per}})
     if (overlap(logits_out, bytes, p, m) || overlap(status, per, p, m)) return SPEC_ERR_INVALID_ARG;
   if (overlap(status, per, logits_out, bytes) || overlap(status, per, logits, bytes)) return SPEC_ERR_INVALID_ARG;
-  // a launch's work-items are counted in 32 bits
-  if ((long long)ceil_div(V, kSlice) * B * 512 > 0xffffffffll) return SPEC_ERR_UNSUPPORTED;
+  // a launch's work-items are counted in 32 bits; the larger slices have the more of them
+  if ((long long)ceil_div(V, 2 * kSlice) * B * 1024 > 0xffffffffll) return SPEC_ERR_UNSUPPORTED;
   const AdjustArgs a{reinterpret_cast<const char*>(logits), reinterpret_cast<char*>(logits_out), draft_tokens, lengths,
                      history, history_len, prompt_len, repetition, frequency, presence, bias_offsets, bias_tokens,
                      bias_values, mask, mask_index, status, R, V, gamma, H, bias_count, masks, (int)words};

@@ -118,6 +118,10 @@ def test_adjust(sv, p):
     far = [ctypes.c_void_p(k << 52) for k in range(1, 4)]
     assert lib.spec_adjust_logits((1 << 31) - 1, 1, 524288, 1, far[0], 0, None, None, None, 0, None, None, None, None,
                                   None, None, None, None, 0, None, 0, None, far[1], far[2], None) == 3
+    # so do 2^22 requests of one slice each, where long histories make it a slice of 1024 threads
+    far = [ctypes.c_void_p(k << 52) for k in range(1, 6)]
+    assert lib.spec_adjust_logits(1 << 22, 1, 4096, 1, far[0], 0, None, None, far[3], 9000, None, None, far[4], None,
+                                  None, None, None, None, 0, None, 0, None, far[1], far[2], None) == 3
 
 
 def test_binding_refuses_before_the_device(sv):

@@ -30,7 +30,7 @@ typedef unsigned int v2u32 __attribute__((ext_vector_type(2)));
 
 constexpr float kCodeMax = 448.f;        // e4m3's largest value
 constexpr float kAmaxFloor = 0x1p-100f;  // so that 448 / amax stays in range (and a block of zeros has a scale)
-constexpr int kBackGroups = 1024;        // workgroups of the backward kernel, at most
+constexpr int kBackThreads = 1 << 18;    // of the backward kernel, at most
 constexpr int kSumSlices = 32, kSumCols = 32;
 
 struct NormArgs {
@@ -413,10 +413,19 @@ bool norm_ok(int N, int d, int dtype) {
 
 bool vector_rows(int d, int dtype) { return d * (dtype == SPEC_BF16 ? 2 : 4) % 16 == 0; }
 
-// Workgroups of the backward kernel: what its rows need, at most kBackGroups (512: 8192 x 4096 bf16 54 us, 1024: 51).
+// Workgroups of the backward kernel: what its rows need, at most kBackThreads threads of them.  With fewer the memory is
+// not kept busy, with more the weight's share of each (d fp32) is written and read for fewer rows: 8192 x 4096 bf16 at
+// 512, 1024 and 2048 workgroups of 256 threads 77, 54 and 63 us; 2048 x 8192 at 256, 512 and 1024 of 512 threads
+// 33, 29 and 35; 2048 x 16384 at 128, 256 and 512 of 1024 threads 89, 58 and 65.  (fp32 rows do with fewer: 8192 x 4096
+// at 256 and 1024 98 and 105 us, 8192 x 2048 at 512 and 1024 45 and 47.)
 int back_groups(int N, int d) {
-  const int rows = d <= 1024 ? teams(64) : d <= 2048 ? teams(128) : 1, groups = ceil_div(N, rows);
-  return groups < kBackGroups ? groups : kBackGroups;
+  int groups = 0;
+  with_shape(d, [&](auto T, auto) {
+    constexpr int rows = teams(T()), most = kBackThreads / (T() * rows);
+    groups = ceil_div(N, rows);
+    if (groups > most) groups = most;
+  });
+  return groups;
 }
 
 int32_t launched() { return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ERR_HIP; }

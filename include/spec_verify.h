@@ -740,7 +740,7 @@ int32_t spec_head_xent_backward(int32_t N, int32_t V, int32_t d, int32_t dtype, 
  * spec_head_norm -- root-mean-square norm with the residual's addition:
  *   h = x + residual;  rstd = 1 / sqrt(mean(h^2) + eps);  y = h * rstd * weight
  *   over each row, in fp32 from the unrounded h.  A row whose squares leave fp32's
- *   range is scaled by a power of two first.
+ *   range is scaled by a power of two first.  A row of zeros with eps = 0 is NaN.
  * Arguments (device pointers)
  *   1 <= N <= SPEC_MAX_HEAD_ROWS, 1 <= d <= SPEC_MAX_HEAD_WIDTH
  *   dtype        SPEC_BF16 or SPEC_F32: x, residual, weight, h_out and y_out
@@ -761,8 +761,9 @@ int32_t spec_head_xent_backward(int32_t N, int32_t V, int32_t d, int32_t dtype, 
  *   grad_weight = sum over the rows of grad_y * xh     (may be NULL)
  *   each rounded once to `dtype`.  h is the stored sum (x where there was no
  *   residual), rstd the forward call's.  grad_x may be grad_y, h or grad_h itself.
- *   Sums over rows are fp32 within a workgroup's share (at most ceil(N / 1024)
- *   rows or 4), then fp64 in a fixed order: results do not depend on scheduling.
+ *   Sums over rows are fp32 within a workgroup's share (N / 1024 rows, N / 512 for
+ *   d > 4096, N / 256 for d > 8192, and at most 4 more), then fp64 in a fixed order:
+ *   results do not depend on scheduling.
  *   workspace    for grad_weight: at least
  *                spec_head_norm_backward_workspace_size(N, d) bytes, 256-byte aligned,
  *                owned by the caller, busy until the call's kernels finish on `stream`

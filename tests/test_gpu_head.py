@@ -191,6 +191,48 @@ def test_norm_backward(sv, shape, dtype):
     assert torch.equal(again["grad_x"], b["grad_x"])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(2100, 1032), (1100, 8192), (600, 16384), (515, 9001)])
+def test_norm_backward_of_several_rows_each(sv, shape, dtype):
+    """More rows than workgroups: a workgroup adds ceil(N / 1024) rows of its share in fp32 (2048 values or fewer: of
+    each of its two teams), ceil(N / 512) where d > 4096 and ceil(N / 256) where d > 8192."""
+    N, d = shape
+    x, r, w = _norm_inputs(N + d, N, d, dtype)
+    gy = _norm_inputs(N + d + 1, N, d, dtype)[0]
+    o = sv.head_norm(x, w, r)
+    print(f"norm backward {shape} {dtype}", flush=True)
+    b = sv.head_norm_backward(gy, o["h"], w, o["rstd"])
+    torch.cuda.synchronize()
+    ref = oracle.head_norm_grad(gy, o["h"], w, o["rstd"], None)
+    rs, g = _np(o["rstd"])[:, None], np.abs(_np(gy) * _np(w))
+    xh = np.abs(_np(o["h"]) * rs)
+    tol = U * (rs * (5 * g + 46 * xh * (g * xh).mean(axis=1, keepdims=True)) + 3 * np.abs(ref["grad_x"]))
+    _near(b["grad_x"], ref["grad_x"], tol + _half(gy) * np.abs(ref["grad_x"]))
+    rows = -(-N // (256 if d > 8192 else 512 if d > 4096 else 1024))
+    tol = U * (6 + rows) * (np.abs(_np(gy)) * xh).sum(axis=0) + _half(gy) * np.abs(ref["grad_weight"])
+    _near(b["grad_weight"], ref["grad_weight"], tol)
+
+
+def test_float32_arrays_on_any_boundary(sv):
+    """Scales and rstd need no more than their own 4 bytes' alignment."""
+    off = lambda *s: torch.empty(int(np.prod(s)) + 1, device=DEV)[1:].view(*s)
+    N, V, d = 37, 700, 1040
+    x, r, w = _norm_inputs(31, N, d, "bf16")
+    head = _norm_inputs(32, V, d, "bf16", False)[0]
+    k, q = sv.head_quantize(head), sv.head_norm(x, w, r, quantize=True)
+    k2 = sv.head_quantize(head, out=dict(codes=torch.empty_like(k["codes"]), scales=off(*k["scales"].shape)))
+    q2 = sv.head_norm(x, w, r, quantize=True, out=dict(codes=torch.empty_like(q["codes"]), scales=off(N, 9),
+                                                       h=torch.empty_like(x), rstd=off(N)))
+    z, z2 = sv.head_logits(q["codes"], q["scales"], k["codes"], k["scales"]), \
+        sv.head_logits(q2["codes"], q2["scales"], k2["codes"], k2["scales"])
+    o = sv.head_norm(x, w, r)
+    b, b2 = sv.head_norm_backward(x, o["h"], w, o["rstd"]), sv.head_norm_backward(x, q2["h"], w, q2["rstd"])
+    torch.cuda.synchronize()
+    assert torch.equal(q["scales"], q2["scales"]) and torch.equal(k["scales"], k2["scales"]) and torch.equal(z, z2)
+    assert torch.equal(o["rstd"], q2["rstd"]) and torch.equal(b["grad_x"], b2["grad_x"])
+    assert torch.equal(b["grad_weight"], b2["grad_weight"])
+
+
 def test_norm_backward_against_differences(sv):
     """The formula's gradient against central differences of the forward call, in fp32.
 

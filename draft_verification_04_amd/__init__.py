@@ -1192,7 +1192,7 @@ def head_logits(codes: torch.Tensor, scales: torch.Tensor, weight_codes: torch.T
 
     codes [N, d] and scales [N, ceil(d / 128)] as head_norm(quantize=True) gives them, weight_codes [V, d] and
     weight_scales [ceil(V / 128), ceil(d / 128)] as head_quantize does.  `out` is written where given (the view of a
-    [B, gamma + 1, V] block as [B * (gamma + 1), V], say).
+    [B, gamma + 1, V] block as [B * (gamma + 1), V], say), in its own type.
     """
     lib = load_library()
     N, d = _rows(codes, "codes")
@@ -1205,7 +1205,8 @@ def head_logits(codes: torch.Tensor, scales: torch.Tensor, weight_codes: torch.T
         raise TypeError(f"logits are float32 or bfloat16, got {dtype}")
     if not (codes.is_cuda and scales is not None and weight_scales is not None and
             _ready(dev, (codes, _E4M3, (N, d)), (scales, f32, (N, G)), (weight_codes, _E4M3, (V, d)),
-                   (weight_scales, f32, (_blocks(V), G)), (out, torch.bfloat16, (N, V)))):
+                   (weight_scales, f32, (_blocks(V), G)), (out, None if out is None else out.dtype, (N, V))) and
+            (out is None or out.dtype in _FLOATS)):
         _shape(scales, "scales", (N, G))
         _shape(weight_scales, "weight_scales", (_blocks(V), G))
         _shape(out, "out", (N, V))
@@ -1240,8 +1241,8 @@ def adjust_logits(logits: torch.Tensor, draft_tokens: Optional[torch.Tensor] = N
     target rows) are adjusted.  history [B, H] int32 (-1 holes count for nothing), history_len and prompt_len [B]
     int32; repetition, frequency and presence [B] float32; bias = (offsets [B + 1] int32, tokens int32, values
     float32); mask [M, R, ceil(V / 32)] int32 bits (set: allowed) and mask_index [B] int32 (-1: none; None: mask i).
-    in_place writes over `logits` (only the values that change), unseen by autograd; otherwise `out`, or a new tensor
-    whose rows past a length or with a status are undefined.  Returns dict(logits, status [B] int32).
+    in_place writes over `logits` (16 bytes at most around a value that changes), unseen by autograd; otherwise `out`,
+    or a new tensor whose rows past a length or with a status are undefined.  Returns dict(logits, status [B] int32).
     """
     lib = load_library()
     if not isinstance(logits, torch.Tensor) or logits.dim() != 3:

@@ -269,3 +269,39 @@ def test_streams_and_a_captured_graph(sv):
         torch.cuda.synchronize()
         print(f"graph replay {rep}", flush=True)
         assert np.array_equal(_bits(outs[0]), _bits(ref)) and status.tolist() == [0] * 20
+
+
+def test_arrays_on_any_boundary_and_unsigned_masks(sv):
+    """Everything but the logits needs no more than its own 4 bytes' alignment."""
+    B, G, V, H = 7, 4, 2503, 333
+    for place in (False, True):
+        z, toks, L, kw, g = _inputs(10, B, G, G + 1, V, H, "bf16")
+        kw.update(bias=_bias(g, B, V, 20), mask=_mask(g, 3, G + 1, V, [0.5, 0.99]))
+        kw["mask_index"] = torch.randint(-1, 3, (B,), generator=g, dtype=torch.int32).to(DEV)
+        off = lambda t: torch.cat([t.new_zeros(1), t.reshape(-1)])[1:].view(t.shape)
+        moved = {k: tuple(map(off, t)) if k == "bias" else off(t) for k, t in kw.items()}
+        moved["mask"] = moved["mask"].view(torch.uint32)
+        a = _check(sv, z, toks, L, **kw)
+        y = z.clone()
+        b = sv.adjust_logits(y, off(toks), off(L), **moved, **(dict(in_place=True) if place else dict(out=z.clone())))
+        few = sv.adjust_logits(z.clone(), off(toks), off(L), in_place=True, **{k: t for k, t in moved.items() if "mask" not in k})
+        ref = sv.adjust_logits(z, toks, L, out=z.clone(), **{k: t for k, t in kw.items() if "mask" not in k})
+        torch.cuda.synchronize()
+        for i in range(B):
+            n = int(L[i]) + 1
+            assert np.array_equal(_bits(b["logits"][i, :n]), _bits(a[i, :n]))
+        assert np.array_equal(_bits(few["logits"]), _bits(ref["logits"])) and b["status"].tolist() == [0] * B
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_requests_of_a_small_vocabulary(sv, dtype):
+    """More requests than a grid's second dimension would hold, in place and out of place."""
+    B, V, H = 70001, 5, 9
+    z, _, _, kw, g = _inputs(11, B, 0, 1, V, H, dtype)
+    ref = oracle.adjust_logits(z[-50:], None, None, *(kw[k][-50:] for k in ("history", "history_len", "prompt_len")),
+                               repetition=kw["repetition"][-50:], frequency=kw["frequency"][-50:], presence=kw["presence"][-50:])
+    o, y = sv.adjust_logits(z, **kw), sv.adjust_logits(z.clone(), in_place=True, **kw)
+    torch.cuda.synchronize()
+    assert int(o["status"].abs().max()) == 0 and np.array_equal(_bits(o["logits"]), _bits(y["logits"]))
+    err = np.abs(o["logits"][-50:].cpu().double().numpy() - ref["logits"])
+    assert (err <= 5 * U * ref["mass"] + torch.finfo(z.dtype).eps / 2 * (1 + 2 ** -10) * np.abs(ref["logits"]) + 1e-40).all()

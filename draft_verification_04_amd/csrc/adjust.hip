@@ -4,15 +4,16 @@
 //   z = z > 0 ? z / repetition : z * repetition   (a token of the prompt, or of count > 0)
 //   z = z - frequency * count;  z = z - presence (count > 0);  z = z + bias;  z = -inf where the mask's bit is 0
 //
-// Nearly all of a row stays as it is: a history names a few thousand tokens of the vocabulary.  A workgroup takes a
-// request and a slice of the vocabulary.  It counts the slice's tokens of the history in LDS (a word per token; the
-// first to count a token puts it on a list), and then goes through the block's rows, which share one count; the draft
-// tokens before a row are compared with the listed token one by one.
-//   Out of place, under a mask, or where much may be listed: the slice of a row goes through LDS, where
-//   lanes take the listed tokens (adjusted in the registers that carry the rows, a lane here and there of every wave,
-//   it took as long as the copy itself).  Masks are applied on the way out.  In place, pieces without a count are
-//   written only where the mask forbids a value, and read only where it forbids some.
-//   In place without a mask and with few tokens: lanes take pairs of listed token and row in memory.
+// Nearly all of a row stays as it is: a history names a few thousand tokens of the vocabulary.  Workgroups count the
+// history's tokens in LDS (a word per token; the first to count a token puts it on a list) and then go through the
+// block's rows, which share one count; the draft tokens before a row are compared with the listed token one by one.
+//   Out of place, under a mask, or where much may be listed: a workgroup takes a request and a slice of the
+//   vocabulary.  The slice of a row goes through LDS, where lanes take the listed tokens (adjusted in the registers
+//   that carry the rows, a lane here and there of every wave, it took as long as the copy itself).  Masks are applied on
+//   the way out.  In place, pieces without a count are written only where the mask forbids a value, and read only where
+//   it forbids some.
+//   In place without a mask and with few tokens: a workgroup takes a request and a class of its tokens, found through a
+//   hash table; lanes take pairs of listed token and row in memory.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -28,6 +29,7 @@ namespace spec {
 namespace {
 
 constexpr int kSlice = 4096, kLongHistory = 8192;
+constexpr int kSlotBits = 12, kSlots = 1 << kSlotBits, kProbes = 64, kFewThreads = 512, kFewGroups = 512, kMaxBits = 4;
 constexpr uint32_t kInPrompt = 1u << 30, kDrafted = 1u << 31, kBiased = 1u << 29, kCount = kBiased - 1;
 
 struct AdjustArgs {
@@ -62,70 +64,60 @@ __device__ __forceinline__ void store_elem(char* row, int64_t v, float z) {
   else reinterpret_cast<float*>(row)[v] = z;
 }
 
-// S tokens of the vocabulary and T threads per workgroup.
-enum { kCopy = 0, kPlace = 1, kFew = 2 };   // out of place; in place; in place without a mask, few tokens
+// A request's own numbers; every workgroup of the request comes to the same verdict.
+struct Request {
+  int st = 0, live, hl, pl, need, bo = 0, bn = 0, mi;
+  float rep, freq, pres;
+  bool penal;   // else neither history nor drafts matter
+};
 
-template <bool BF16, bool BIAS, int MODE, int S, int T, int U>
-__global__ __launch_bounds__(T) void adjust_kernel(AdjustArgs a) {
-  constexpr bool COPY = MODE == kCopy;
-  constexpr int ES = BF16 ? 2 : 4, VE = 16 / ES, NV = S / VE / T;   // pieces of a row per lane; U rows at a time
-  static_assert(S % (VE * T) == 0 && S <= 65536, "slice");
-  __shared__ __attribute__((aligned(16))) uint32_t count[S];
-  __shared__ __attribute__((aligned(16))) uint32_t bias_at[BIAS ? S : 4];   // entry of the list + 1 (the last one of a token named twice)
-  __shared__ __attribute__((aligned(16))) char rows[MODE == kFew ? 1 : U][MODE == kFew ? 16 : S * ES];
-  __shared__ uint16_t list[S];
-  __shared__ int32_t drafts[SPEC_MAX_GAMMA];
-  __shared__ int listed, bad;
-  const int tid = threadIdx.x, V = a.V, R = a.R, slices = (V + S - 1) / S;
-  const int b = (int)(blockIdx.x / (unsigned)slices), slice = (int)(blockIdx.x % (unsigned)slices);
-  const int v0 = slice * S, n = min(S, V - v0);
-
-  // the request's own numbers; every workgroup of the request comes to the same verdict
-  int st = 0;
+template <bool BIAS>
+__device__ __forceinline__ Request request(const AdjustArgs& a, int b) {
+  Request q;
   const int L = a.lengths ? a.lengths[b] : a.gamma;
-  if (L < 0 || L > a.gamma) st |= SPEC_REQ_BAD_LENGTH;
-  const int live = st ? 0 : L + (R - a.gamma);
-  int hl = a.history ? (a.history_len ? a.history_len[b] : a.H) : 0, pl = a.history && a.prompt_len ? a.prompt_len[b] : 0;
-  if (hl < 0 || hl > a.H || pl < 0 || pl > hl) {
-    st |= SPEC_REQ_BAD_LENGTH;
-    hl = pl = 0;
+  if (L < 0 || L > a.gamma) q.st |= SPEC_REQ_BAD_LENGTH;
+  q.live = q.st ? 0 : L + (a.R - a.gamma);
+  q.hl = a.history ? (a.history_len ? a.history_len[b] : a.H) : 0;
+  q.pl = a.history && a.prompt_len ? a.prompt_len[b] : 0;
+  if (q.hl < 0 || q.hl > a.H || q.pl < 0 || q.pl > q.hl) {
+    q.st |= SPEC_REQ_BAD_LENGTH;
+    q.hl = q.pl = 0;
   }
-  const float rep = a.repetition ? a.repetition[b] : 1.f, freq = a.frequency ? a.frequency[b] : 0.f,
-              pres = a.presence ? a.presence[b] : 0.f;
-  if (!(rep > 0.f && rep < INFINITY && fabsf(freq) < INFINITY && fabsf(pres) < INFINITY)) st |= SPEC_REQ_BAD_PENALTY;
-  const bool penal = rep != 1.f || freq != 0.f || pres != 0.f;   // else neither history nor drafts matter
-  int bo = 0, bn = 0;
+  q.rep = a.repetition ? a.repetition[b] : 1.f;
+  q.freq = a.frequency ? a.frequency[b] : 0.f;
+  q.pres = a.presence ? a.presence[b] : 0.f;
+  if (!(q.rep > 0.f && q.rep < INFINITY && fabsf(q.freq) < INFINITY && fabsf(q.pres) < INFINITY))
+    q.st |= SPEC_REQ_BAD_PENALTY;
+  q.penal = q.rep != 1.f || q.freq != 0.f || q.pres != 0.f;
   if constexpr (BIAS) {
-    bo = a.bias_offsets[b];
+    q.bo = a.bias_offsets[b];
     const int be = a.bias_offsets[b + 1];
-    if (bo < 0 || be < bo || be > a.bias_count) st |= SPEC_REQ_BAD_LIST;
-    else bn = be - bo;
+    if (q.bo < 0 || be < q.bo || be > a.bias_count) q.st |= SPEC_REQ_BAD_LIST;
+    else q.bn = be - q.bo;
   }
-  const int mi = a.mask ? (a.mask_index ? a.mask_index[b] : b) : -1;
-  if (mi < -1 || mi >= a.masks) st |= SPEC_REQ_BAD_MASK;
+  q.mi = a.mask ? (a.mask_index ? a.mask_index[b] : b) : -1;
+  if (q.mi < -1 || q.mi >= a.masks) q.st |= SPEC_REQ_BAD_MASK;
+  q.need = q.penal ? min(q.live - 1, a.gamma) : 0;   // draft tokens that precede a live row
+  return q;
+}
 
-  for (int i = tid; i < S / 4; i += T) {
-    reinterpret_cast<v4u32*>(count)[i] = v4u32{};
-    if constexpr (BIAS) reinterpret_cast<v4u32*>(bias_at)[i] = v4u32{};
-  }
-  if (tid == 0) listed = bad = 0;
-  const int need = penal ? min(live - 1, a.gamma) : 0;   // draft tokens that precede a live row
-  if (tid < need) drafts[tid] = a.draft_tokens[(size_t)b * a.gamma + tid];
-  __syncthreads();
+// What a request's rows count and add, put into a workgroup's tables: slot_of names a token's slot (past `slots`:
+// none).  `note` is told the slot and what its count was.  Returns whether a token is out of range.
+template <bool BIAS, int T, class Slot, class Note>
+__device__ __forceinline__ bool gather(const AdjustArgs& a, const Request& q, int b, const int32_t* drafts, uint32_t* count,
+                                       uint32_t* bias_at, unsigned slots, Slot slot_of, Note note) {
+  const int tid = threadIdx.x;
   bool off = false;
-  auto note = [&](unsigned i, uint32_t old) {
-    if (old == 0) list[atomicAdd(&listed, 1)] = (uint16_t)i;
-  };
-  if (penal && live > 0) {
+  if (q.penal && q.live > 0) {
     const int32_t* h = a.history + (size_t)b * a.H;
     // four tokens a load, F loads in flight per thread
     constexpr int F = 4;
-    const int quads = hl >> 2;
+    const int quads = q.hl >> 2;
     uint32_t most = 0;   // of t + 1: -1 is a hole
     auto count_in = [&](int t, int i) {
-      const unsigned at = (unsigned)t - (unsigned)v0;
       most = max(most, (unsigned)t + 1u);
-      if (at < (unsigned)n) note(at, i < pl ? atomicOr(&count[at], kInPrompt) : atomicAdd(&count[at], 1u));
+      const unsigned at = slot_of(t);
+      if (at < slots) note(at, t, i < q.pl ? atomicOr(&count[at], kInPrompt) : atomicAdd(&count[at], 1u));
     };
     for (int i0 = tid; i0 < quads; i0 += F * T) {
       v4u32 t[F];
@@ -139,67 +131,244 @@ __global__ __launch_bounds__(T) void adjust_kernel(AdjustArgs a) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) count_in((int)t[u][x], 4 * (i0 + u * T) + x);
     }
-    if (tid < (hl & 3)) count_in(h[4 * quads + tid], 4 * quads + tid);
-    off |= most > (unsigned)V;
-    if (tid < need) {
-      const unsigned t = (unsigned)drafts[tid], at = t - (unsigned)v0;
-      off |= t >= (unsigned)V;
-      if (at < (unsigned)n) note(at, atomicOr(&count[at], kDrafted));
+    if (tid < (q.hl & 3)) count_in(h[4 * quads + tid], 4 * quads + tid);
+    off |= most > (unsigned)a.V;
+    if (tid < q.need) {
+      const int t = drafts[tid];
+      const unsigned at = slot_of(t);
+      off |= (unsigned)t >= (unsigned)a.V;
+      if (at < slots) note(at, t, atomicOr(&count[at], kDrafted));
     }
   }
   if constexpr (BIAS) {
-    for (int i = tid; i < bn && live > 0; i += T) {
-      const unsigned t = (unsigned)a.bias_tokens[bo + i], at = t - (unsigned)v0;
-      off |= t >= (unsigned)V;
-      if (at < (unsigned)n) {
-        note(at, atomicOr(&count[at], kBiased));
+    for (int i = tid; i < q.bn && q.live > 0; i += T) {
+      const int t = a.bias_tokens[q.bo + i];
+      const unsigned at = slot_of(t);
+      off |= (unsigned)t >= (unsigned)a.V;
+      if (at < slots) {
+        note(at, t, atomicOr(&count[at], kBiased));
         atomicMax(&bias_at[at], (uint32_t)i + 1);
       }
     }
   }
-  if (off) bad = 1;
+  return off;
+}
+
+// A listed token: what is the same for every row.
+struct Token {
+  int id, c;
+  bool prompt, drafted, biased;
+  float bias;
+};
+
+template <bool BIAS>
+__device__ __forceinline__ Token token(const AdjustArgs& a, const Request& q, int id, uint32_t w, const uint32_t* bias_at, int at) {
+  Token t{id, (int)(w & kCount), (w & kInPrompt) != 0, (w & kDrafted) != 0, BIAS && (w & kBiased), 0.f};
+  if constexpr (BIAS)
+    if (t.biased) t.bias = a.bias_values[q.bo + (int)bias_at[at] - 1];
+  return t;
+}
+
+__device__ __forceinline__ float adjusted(const Request& q, const int32_t* drafts, float z, const Token& t, int r) {
+  int c = t.c;
+  if (t.drafted)
+    for (int k = 0; k < min(r, q.need); ++k) c += drafts[k] == t.id;
+  if (c > 0 || t.prompt) z = z > 0.f ? z / q.rep : z * q.rep;
+  if (c > 0) {
+    z = z - q.freq * (float)c;
+    z = z - q.pres;
+  }
+  if (t.biased) z = z + t.bias;
+  return z;
+}
+
+// S tokens of the vocabulary and T threads per workgroup.
+template <bool BF16, bool BIAS, bool COPY, int S, int T>
+__global__ __launch_bounds__(T) void adjust_kernel(AdjustArgs a) {
+  constexpr int ES = BF16 ? 2 : 4, VE = 16 / ES, NV = S / VE / T;   // pieces of a row per lane
+  static_assert(S % (VE * T) == 0 && S <= 65536, "slice");
+  __shared__ __attribute__((aligned(16))) uint32_t count[S];
+  __shared__ __attribute__((aligned(16))) uint32_t bias_at[BIAS ? S : 4];   // entry of the list + 1 (the last one of a token named twice)
+  __shared__ __attribute__((aligned(16))) char part[S * ES];
+  __shared__ uint16_t list[S];
+  __shared__ int32_t drafts[SPEC_MAX_GAMMA];
+  __shared__ int listed, bad;
+  const int tid = threadIdx.x, V = a.V, R = a.R, slices = (V + S - 1) / S;
+  const int b = (int)(blockIdx.x / (unsigned)slices), slice = (int)(blockIdx.x % (unsigned)slices);
+  const int v0 = slice * S, n = min(S, V - v0);
+  const Request q = request<BIAS>(a, b);
+  int st = q.st;
+
+  // row r's allowed values of the lane's pieces (0 where there is none)
+  constexpr uint32_t kAll = (1u << VE) - 1;
+  const uint32_t* mask = q.mi >= 0 && !q.st ? a.mask + (size_t)q.mi * R * a.words : nullptr;
+  const size_t row0 = (size_t)b * R * V + v0;
+  uint32_t some[NV] = {};   // in place: a lane's values with a count
+  auto load_on = [&](int r, uint32_t(&on)[NV]) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = (tid + k * T) * VE, left = n - i;
+      on[k] = left >= VE ? kAll : left > 0 ? (1u << left) - 1 : 0u;
+      if (mask && left > 0) on[k] &= mask[(size_t)r * a.words + ((v0 + i) >> 5)] >> ((v0 + i) & 31);
+    }
+  };
+  // in place only what changes is read: a value with a count, or one beside a forbidden one
+  auto moves = [&](int k, uint32_t on) {
+    const int i = (tid + k * T) * VE;
+    const uint32_t whole = i + VE <= n ? kAll : (1u << max(n - i, 0)) - 1;
+    return COPY ? on != 0 : (on & some[k]) != 0 || (on != 0 && on != whole);
+  };
+  auto load_row = [&](int r, const uint32_t(&on)[NV], v4u32(&z)[NV]) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = (tid + k * T) * VE;
+      if (!moves(k, on[k])) continue;
+      const size_t at = row0 + (size_t)r * V + i;
+      if (i + VE <= n) {
+        z[k] = __builtin_nontemporal_load(&reinterpret_cast<const Piece<ES>*>(a.logits + at * ES)->v);
+      } else {   // the row's last values
+        z[k] = v4u32{};
+        for (int x = 0; i + x < n; ++x) {
+          const uint32_t h = BF16 ? reinterpret_cast<const uint16_t*>(a.logits)[at + x] : reinterpret_cast<const uint32_t*>(a.logits)[at + x];
+          if constexpr (BF16) {
+            if (x < 2) z[k].x |= h << (16 * x);
+            else if (x < 4) z[k].y |= h << (16 * (x - 2));
+            else if (x < 6) z[k].z |= h << (16 * (x - 4));
+            else z[k].w |= h << (16 * (x - 6));
+          } else {
+            if (x == 0) z[k].x = h;
+            else if (x == 1) z[k].y = h;
+            else z[k].z = h;
+          }
+        }
+      }
+    }
+  };
+  uint32_t next_on[NV] = {};
+  v4u32 next[NV] = {};
+  // the first row comes while the history is counted, the others while the one before is adjusted (90 -> 83 us)
+  if (COPY && q.live > 0) {
+    load_on(0, next_on);
+    load_row(0, next_on, next);
+  }
+
+  for (int i = tid; i < S / 4; i += T) {
+    reinterpret_cast<v4u32*>(count)[i] = v4u32{};
+    if constexpr (BIAS) reinterpret_cast<v4u32*>(bias_at)[i] = v4u32{};
+  }
+  if (tid == 0) listed = bad = 0;
+  if (tid < q.need) drafts[tid] = a.draft_tokens[(size_t)b * a.gamma + tid];
+  __syncthreads();
+  if (gather<BIAS, T>(a, q, b, drafts, count, bias_at, (unsigned)n, [&](int t) { return (unsigned)t - (unsigned)v0; },
+                      [&](unsigned at, int, uint32_t old) {
+                        if (old == 0) list[atomicAdd(&listed, 1)] = (uint16_t)at;
+                      }))
+    bad = 1;
   __syncthreads();
   if (bad) st |= SPEC_REQ_BAD_TOKEN;
   if (slice == 0 && tid == 0 && a.status) a.status[b] = st;
-  if (st) return;
+  if (st || q.live == 0) return;
 
-  const int E = listed;
-  const uint32_t* mask = mi >= 0 ? a.mask + (size_t)mi * R * a.words : nullptr;
-  const size_t row0 = (size_t)b * R * V + v0;
-  // a listed token: what is the same for every row
-  struct Token {
-    int i, c;
-    bool prompt, drafted, biased;
-    float bias;
-  };
-  auto token = [&](int e) {
-    Token t;
-    t.i = list[e];
-    const uint32_t w = count[t.i];
-    t.c = (int)(w & kCount);
-    t.prompt = w & kInPrompt;
-    t.drafted = w & kDrafted;
-    t.biased = BIAS && (w & kBiased);
-    t.bias = 0.f;
-    if constexpr (BIAS)
-      if (t.biased) t.bias = a.bias_values[bo + (int)bias_at[t.i] - 1];
-    return t;
-  };
-  auto adjusted = [&](float z, const Token& t, int r) {
-    int c = t.c;
-    if (t.drafted)
-      for (int k = 0; k < min(r, need); ++k) c += drafts[k] == v0 + t.i;
-    if (c > 0 || t.prompt) z = z > 0.f ? z / rep : z * rep;
-    if (c > 0) {
-      z = z - freq * (float)c;
-      z = z - pres;
+  const int E = listed, live = q.live;
+  auto entry = [&](int e) { return token<BIAS>(a, q, v0 + list[e], count[list[e]], bias_at, list[e]); };
+
+  if (!COPY) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int x = 0; x < VE; ++x) some[k] |= (count[(tid + k * T) * VE + x] ? 1u : 0u) << x;
+    load_on(0, next_on);
+    load_row(0, next_on, next);
+  }
+  Token mine{};   // the lane's first listed token
+  if (tid < E) mine = entry(tid);
+  for (int r = 0; r < live; ++r) {
+    v4u32 z[NV];
+    uint32_t on[NV];
+    bool move[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      z[k] = next[k];
+      on[k] = next_on[k];
+      move[k] = moves(k, on[k]);
     }
-    if (t.biased) z = z + t.bias;
-    return z;
-  };
+    if (r + 1 < live) {
+      load_on(r + 1, next_on);
+      load_row(r + 1, next_on, next);
+    }
+    if (E > 0) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (move[k]) *reinterpret_cast<v4u32*>(&part[(tid + k * T) * 16]) = z[k];
+      __syncthreads();
+      for (int e = tid; e < E; e += T) {
+        const Token t = e == tid ? mine : entry(e);
+        store_elem<BF16>(part, t.id - v0, adjusted(q, drafts, load_elem<BF16>(part, t.id - v0), t, r));
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (move[k]) z[k] = *reinterpret_cast<const v4u32*>(&part[(tid + k * T) * 16]);
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = (tid + k * T) * VE;
+      if (i >= n || (!COPY && !move[k] && on[k] != 0)) continue;
+      const size_t at = row0 + (size_t)r * V + i;
+      v4u32 y = move[k] ? z[k] : v4u32{};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if constexpr (BF16) {
+          const uint32_t p = on[k] >> (2 * x) & 3u, keep = (p & 1u ? 0xffffu : 0u) | (p & 2u ? 0xffff0000u : 0u);
+          y[x] = (y[x] & keep) | (0xff80ff80u & ~keep);
+        } else {
+          y[x] = on[k] >> x & 1u ? y[x] : 0xff800000u;
+        }
+      }
+      if (i + VE <= n) {
+        __builtin_nontemporal_store(y, &reinterpret_cast<Piece<ES>*>(a.out + at * ES)->v);
+      } else {
+#pragma unroll
+        for (int x = 0; x < VE; ++x) {
+          if (i + x >= n) break;
+          if constexpr (BF16) reinterpret_cast<uint16_t*>(a.out)[at + x] = (uint16_t)(y[x / 2] >> (x & 1 ? 16 : 0));
+          else reinterpret_cast<uint32_t*>(a.out)[at + x] = y[x];
+        }
+      }
+    }
+  }
+}
 
-  if constexpr (MODE == kFew) {
-    const unsigned pairs = (unsigned)E * (unsigned)live;
+// In place and without a mask: the listed tokens alone, where they lie.  A workgroup takes the tokens of a class, every
+// 2^bits-th block of 64 (lines of memory belong to one class), counts them in a table of kSlots that a token's hash
+// leads into, and its lanes take pairs of listed token and row.  A class of more tokens than the table takes is gone
+// through again, kSlots of the class at a time, in order.
+template <bool BF16, bool BIAS>
+__global__ __launch_bounds__(kFewThreads) void adjust_few_kernel(AdjustArgs a, int bits) {
+  constexpr int T = kFewThreads, U = 4;   // pairs in flight per lane
+  __shared__ int32_t key[kSlots];
+  __shared__ uint32_t count[kSlots];
+  __shared__ uint32_t bias_at[BIAS ? kSlots : 1];
+  __shared__ uint16_t list[kSlots];
+  __shared__ int32_t drafts[SPEC_MAX_GAMMA];
+  __shared__ int listed, bad, over;
+  const int tid = threadIdx.x, V = a.V, R = a.R;
+  const int classes = 1 << bits, b = (int)(blockIdx.x >> bits), mine = (int)blockIdx.x & (classes - 1);
+  const Request q = request<BIAS>(a, b);
+  int st = q.st;
+  auto clear = [&] {
+    for (int i = tid; i < kSlots; i += T) {
+      key[i] = -1;
+      count[i] = 0;
+      if constexpr (BIAS) bias_at[i] = 0;
+    }
+    if (tid == 0) listed = 0;
+  };
+  auto in_class = [&](int t) { return (unsigned)t < (unsigned)V && ((t >> 6) & (classes - 1)) == mine; };
+  const size_t row0 = (size_t)b * R * V;
+  auto entry = [&](int e) { return token<BIAS>(a, q, key[list[e]], count[list[e]], bias_at, list[e]); };
+  auto write = [&] {
+    const unsigned E = (unsigned)listed, pairs = E * (unsigned)q.live;
     for (unsigned p0 = tid; p0 < pairs; p0 += U * T) {
       float z[U];
       Token t[U];
@@ -207,148 +376,104 @@ __global__ __launch_bounds__(T) void adjust_kernel(AdjustArgs a) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const unsigned p = min(p0 + u * T, pairs - 1);
-        r[u] = (int)(p / (unsigned)E);
-        t[u] = token((int)(p % (unsigned)E));
-        z[u] = load_elem<BF16>(a.logits, (int64_t)(row0 + (size_t)r[u] * V + t[u].i));
+        r[u] = (int)(p / E);
+        t[u] = entry((int)(p % E));
+        z[u] = load_elem<BF16>(a.logits, (int64_t)(row0 + (size_t)r[u] * V + t[u].id));
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (p0 + u * T < pairs) store_elem<BF16>(a.out, (int64_t)(row0 + (size_t)r[u] * V + t[u].i), adjusted(z[u], t[u], r[u]));
+        if (p0 + u * T < pairs)
+          store_elem<BF16>(a.out, (int64_t)(row0 + (size_t)r[u] * V + t[u].id), adjusted(q, drafts, z[u], t[u], r[u]));
     }
-  } else {
+  };
 
-    constexpr uint32_t kAll = (1u << VE) - 1;
-    uint32_t some[NV];   // in place: a lane's values with a count
-#pragma unroll
-    for (int q = 0; q < NV; ++q) {
-      some[q] = 0;
-      if (!COPY)
-#pragma unroll
-        for (int x = 0; x < VE; ++x) some[q] |= (count[(tid + q * T) * VE + x] ? 1u : 0u) << x;
-    }
-    Token mine{};   // the lane's first listed token
-    if (tid < E) mine = token(tid);
-    for (int r0 = 0; r0 < live; r0 += U) {
-      v4u32 z[U][NV];
-      uint32_t on[U][NV];   // allowed values of the piece (0 where there is none)
-      bool move[U][NV];     // in place only what changes is read: a value with a count, or one beside a forbidden one
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int q = 0; q < NV; ++q) {
-          const int i = (tid + q * T) * VE, left = r0 + u < live ? n - i : 0;
-          on[u][q] = left >= VE ? kAll : left > 0 ? (1u << left) - 1 : 0u;
-          if (mask && left > 0) on[u][q] &= mask[(size_t)(r0 + u) * a.words + ((v0 + i) >> 5)] >> ((v0 + i) & 31);
-        }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int q = 0; q < NV; ++q) {
-          const int i = (tid + q * T) * VE;
-          const uint32_t whole = i + VE <= n ? kAll : (1u << max(n - i, 0)) - 1;
-          move[u][q] = COPY ? on[u][q] != 0 : (on[u][q] & some[q]) != 0 || (on[u][q] != 0 && on[u][q] != whole);
-          if (!move[u][q]) continue;
-          const size_t at = row0 + (size_t)(r0 + u) * V + i;
-          if (i + VE <= n) {
-            z[u][q] = __builtin_nontemporal_load(&reinterpret_cast<const Piece<ES>*>(a.logits + at * ES)->v);
-          } else {   // the row's last values
-            z[u][q] = v4u32{};
-            for (int x = 0; i + x < n; ++x) {
-              const uint32_t h = BF16 ? reinterpret_cast<const uint16_t*>(a.logits)[at + x] : reinterpret_cast<const uint32_t*>(a.logits)[at + x];
-              if constexpr (BF16) {
-                if (x < 2) z[u][q].x |= h << (16 * x);
-                else if (x < 4) z[u][q].y |= h << (16 * (x - 2));
-                else if (x < 6) z[u][q].z |= h << (16 * (x - 4));
-                else z[u][q].w |= h << (16 * (x - 6));
-              } else {
-                if (x == 0) z[u][q].x = h;
-                else if (x == 1) z[u][q].y = h;
-                else z[u][q].z = h;
-              }
-            }
-          }
-        }
-      if (E > 0) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int q = 0; q < NV; ++q)
-            if (move[u][q]) *reinterpret_cast<v4u32*>(&rows[u][(tid + q * T) * 16]) = z[u][q];
-        __syncthreads();
-        for (int e = tid; e < E; e += T) {
-          const Token t = e == tid ? mine : token(e);
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (r0 + u < live) store_elem<BF16>(rows[u], t.i, adjusted(load_elem<BF16>(rows[u], t.i), t, r0 + u));
-        }
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int q = 0; q < NV; ++q)
-            if (move[u][q]) z[u][q] = *reinterpret_cast<const v4u32*>(&rows[u][(tid + q * T) * 16]);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int q = 0; q < NV; ++q) {
-          const int i = (tid + q * T) * VE;
-          if (r0 + u >= live || i >= n || (!COPY && !move[u][q] && on[u][q] != 0)) continue;
-          const size_t at = row0 + (size_t)(r0 + u) * V + i;
-          v4u32 y = move[u][q] ? z[u][q] : v4u32{};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            if constexpr (BF16) {
-              const uint32_t p = on[u][q] >> (2 * x) & 3u, keep = (p & 1u ? 0xffffu : 0u) | (p & 2u ? 0xffff0000u : 0u);
-              y[x] = (y[x] & keep) | (0xff80ff80u & ~keep);
-            } else {
-              y[x] = on[u][q] >> x & 1u ? y[x] : 0xff800000u;
-            }
-          }
-          if (i + VE <= n) {
-            __builtin_nontemporal_store(y, &reinterpret_cast<Piece<ES>*>(a.out + at * ES)->v);
-          } else {
-#pragma unroll
-            for (int x = 0; x < VE; ++x) {
-              if (i + x >= n) break;
-              if constexpr (BF16) reinterpret_cast<uint16_t*>(a.out)[at + x] = (uint16_t)(y[x / 2] >> (x & 1 ? 16 : 0));
-              else reinterpret_cast<uint32_t*>(a.out)[at + x] = y[x];
-            }
-          }
-        }
-    }
+  clear();
+  if (tid == 0) bad = over = 0;
+  if (tid < q.need) drafts[tid] = a.draft_tokens[(size_t)b * a.gamma + tid];
+  __syncthreads();
+  if (gather<BIAS, T>(a, q, b, drafts, count, bias_at, (unsigned)kSlots,
+                      [&](int t) {
+                        if (!in_class(t)) return ~0u;
+                        unsigned at = (unsigned)t * 2654435761u >> (32 - kSlotBits);
+                        for (int probe = 0; probe < kProbes; ++probe, at = (at + 1) & (kSlots - 1)) {
+                          const int old = atomicCAS(&key[at], -1, t);
+                          if (old == -1 || old == t) return at;
+                        }
+                        over = 1;
+                        return ~0u;
+                      },
+                      [&](unsigned at, int, uint32_t old) {
+                        if (old == 0) list[atomicAdd(&listed, 1)] = (uint16_t)at;
+                      }))
+    bad = 1;
+  __syncthreads();
+  if (bad) st |= SPEC_REQ_BAD_TOKEN;
+  if (mine == 0 && tid == 0 && a.status) a.status[b] = st;
+  if (st) return;
+  if (!over) {
+    write();
+    return;
+  }
+  for (int c0 = 0; c0 < ((V - 1) >> (6 + bits) << 6) + 64; c0 += kSlots) {
+    __syncthreads();   // the table is read no more
+    clear();
+    __syncthreads();
+    gather<BIAS, T>(a, q, b, drafts, count, bias_at, (unsigned)kSlots,
+                    [&](int t) { return in_class(t) ? (unsigned)((t >> (6 + bits) << 6 | (t & 63)) - c0) : ~0u; },
+                    [&](unsigned at, int t, uint32_t old) {
+                      if (old == 0) {
+                        key[at] = t;
+                        list[atomicAdd(&listed, 1)] = (uint16_t)at;
+                      }
+                    });
+    __syncthreads();
+    write();
   }
 }
 
-template <bool BF16, bool BIAS, int MODE, int S, int T, int U>
+template <bool BF16, bool BIAS, bool COPY, int S, int T>
 void launch(const AdjustArgs& a, int B, hipStream_t s) {
   const dim3 grid((unsigned)ceil_div(a.V, S) * (unsigned)B);
-  hipLaunchKernelGGL((adjust_kernel<BF16, BIAS, MODE, S, T, U>), grid, dim3(T), 0, s, a);
+  hipLaunchKernelGGL((adjust_kernel<BF16, BIAS, COPY, S, T>), grid, dim3(T), 0, s, a);
 }
 
-// Slices of 4096 tokens by 512 threads, one row of it in LDS at a time: 24 waves a CU or more (64 blocks of 17 rows of
-// 151936 bf16, half of them live, out of place: 90 us; two rows at a time 98; slices of 2048 by 256 threads 96, of
-// 8192 by 1024 118).  Every slice's workgroup reads the whole history, and from some 8000 tokens on half as many
-// slices are faster, where their LDS leaves two workgroups to a CU (96 x 8 rows of 129280 after 30011 tokens:
-// 120 -> 108 us; after 1000: 74 -> 77).
-// In place, listed tokens cost 30 ps a row where they lie in memory, and a row's slice through LDS 1 ps a token: where
-// the history can name a thirtieth of the vocabulary the row goes through LDS.
+// 2^bits classes: as many as give kFewGroups workgroups while each still has some 256 pairs, and no more tokens to a
+// class than fill its table to two thirds (as far as a launch's work-items can be counted).  256 single tokens of
+// 151936 after 4096: 256 and 512 workgroups 17.7 us, 1024 21.6, 2048 31; 64 blocks of 17 rows: 256 workgroups 23.9,
+// 512 and more 22.
+int few_bits(int B, int R, long long named) {
+  int bits = 0;
+  while (bits < kMaxBits && (2ll * B << bits) <= kFewGroups && named * R >= 512ll << bits) ++bits;
+  while (bits < kMaxBits && 3 * named > 2ll * kSlots << bits && (2ll * B * kFewThreads << bits) <= 0xffffffffll) ++bits;
+  return bits;
+}
+
+// Slices of 4096 tokens, 16 bytes of a row per thread: two workgroups a CU or more (64 blocks of 17 rows of 151936
+// bf16, half of them live, out of place: 83 us; slices of 2048 91; fp32, half as many blocks: by 512 threads 81, by
+// 1024 77).  Every slice's workgroup reads the whole history, and from some 8000 tokens on half as many slices are
+// faster (96 x 8 rows of 129280 after 30011 tokens: 115 -> 103 us; after 1000: 70 -> 71).
+// In place without a mask a row's slice through LDS is only ahead where much of the vocabulary is listed: 64 blocks of
+// 17 rows as above, histories of a 32nd of the vocabulary 70 us, of a 16th 81, of an 8th 98; the listed tokens where
+// they lie 38, 81 and 141.  256 single tokens likewise: 71, 80 and 106; 21, 36 and 77.
 template <bool BF16, bool BIAS>
 void run_adjust(const AdjustArgs& a, int B, hipStream_t s) {
   const bool copy = a.logits != a.out;
-  if (!copy && !a.mask && a.H <= a.V / 32) {
-    launch<BF16, BIAS, kFew, kSlice, 512, 4>(a, B, s);
+  const long long named = (long long)a.H + a.gamma + a.bias_count / B;   // tokens of a request at most, or so
+  if (!copy && !a.mask && named <= a.V / (a.R == 1 ? 8 : 16)) {
+    const int bits = few_bits(B, a.R, named);
+    hipLaunchKernelGGL((adjust_few_kernel<BF16, BIAS>), dim3((unsigned)B << bits), dim3(kFewThreads), 0, s, a, bits);
     return;
   }
   if constexpr (BF16 && !BIAS) {
     if (a.H > kLongHistory) {
-      if (copy) launch<BF16, BIAS, kCopy, 2 * kSlice, 1024, 1>(a, B, s);
-      else launch<BF16, BIAS, kPlace, 2 * kSlice, 1024, 1>(a, B, s);
+      if (copy) launch<BF16, BIAS, true, 2 * kSlice, 1024>(a, B, s);
+      else launch<BF16, BIAS, false, 2 * kSlice, 1024>(a, B, s);
       return;
     }
   }
-  if (copy) launch<BF16, BIAS, kCopy, kSlice, 512, 1>(a, B, s);
-  else launch<BF16, BIAS, kPlace, kSlice, 512, 1>(a, B, s);
+  constexpr int T = BF16 ? 512 : 1024;
+  if (copy) launch<BF16, BIAS, true, kSlice, T>(a, B, s);
+  else launch<BF16, BIAS, false, kSlice, T>(a, B, s);
 }
 
 }  // namespace

@@ -305,3 +305,26 @@ def test_many_requests_of_a_small_vocabulary(sv, dtype):
     assert int(o["status"].abs().max()) == 0 and np.array_equal(_bits(o["logits"]), _bits(y["logits"]))
     err = np.abs(o["logits"][-50:].cpu().double().numpy() - ref["logits"])
     assert (err <= 5 * U * ref["mass"] + torch.finfo(z.dtype).eps / 2 * (1 + 2 ** -10) * np.abs(ref["logits"]) + 1e-40).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_more_tokens_of_one_kind_than_a_table_takes(sv, dtype):
+    """Thousands of different tokens whose ids agree in bits 6 to 9, in the history, the biases or both, beside
+    requests with few."""
+    B, G, V, H = 3, 2, 262144, 7000
+    z, toks, L, kw, g = _inputs(12, B, G, G + 1, V, H, dtype, ragged=False)
+    kind = (torch.arange(V // 1024)[:, None] * 1024 + torch.arange(64) + 5 * 64).reshape(-1)[torch.randperm(V // 16, generator=g)]
+    kw["history_len"][:] = torch.tensor([H, 40, H - 3])
+    kw["prompt_len"][:] = torch.tensor([500, 10, 0])
+    kw["repetition"][:], kw["frequency"][:] = 1.5, 0.25
+    kw["history"][0] = kind[:H].to(torch.int32).to(DEV)
+    toks[0, 0] = int(kind[0])
+    n = 9000
+    off = torch.tensor([0, 5, 5 + n, 5 + n], dtype=torch.int32, device=DEV)
+    t = torch.cat([torch.arange(5), kind[:n]]).to(torch.int32).to(DEV)
+    t[-40:] = t[10:50]
+    bias = (off, t, torch.randn(5 + n, generator=g).to(DEV))
+    for name, more in (("history", {}), ("bias", dict(bias=bias))):
+        print(f"one kind {dtype} {name}", flush=True)
+        _check(sv, z, toks, L, **kw, **more)
+    _check(sv, z, toks, L, bias=bias)

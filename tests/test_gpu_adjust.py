@@ -328,3 +328,32 @@ def test_more_tokens_of_one_kind_than_a_table_takes(sv, dtype):
         print(f"one kind {dtype} {name}", flush=True)
         _check(sv, z, toks, L, **kw, **more)
     _check(sv, z, toks, L, bias=bias)
+
+
+def test_in_place_on_streams_and_in_a_captured_graph(sv):
+    """Different requests in place on three streams at once, and replays of one graph on rows put back before each."""
+    z, toks, L, kw, g = _inputs(13, 24, 4, 5, 60013, 700, "bf16")
+    kw["bias"] = _bias(g, 24, 60013, 30)
+    ref = _check(sv, z, toks, L, **kw)
+    rows = torch.arange(5, device=DEV)[None] <= L[:, None]
+    work = [z.clone() for _ in range(3)]
+    torch.cuda.synchronize()
+    for w in work:
+        sv.adjust_logits(w, toks, L, **kw, in_place=True, stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    for w in work:
+        assert np.array_equal(_bits(w[rows]), _bits(ref[rows])) and np.array_equal(_bits(w[~rows]), _bits(z[~rows]))
+    status = torch.zeros(24, dtype=torch.int32, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        sv.adjust_logits(work[0], toks, L, **kw, in_place=True, status=status)
+    for rep in range(3):
+        work[0].copy_(z)
+        status.fill_(-1)
+        sv.adjust_logits(work[1].copy_(z), toks, L, **kw, in_place=True)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        print(f"in place, replay {rep}", flush=True)
+        assert np.array_equal(_bits(work[0]), _bits(work[1])) and status.tolist() == [0] * 24
+        assert np.array_equal(_bits(work[0][rows]), _bits(ref[rows]))

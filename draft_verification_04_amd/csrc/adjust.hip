@@ -20,16 +20,15 @@
 
 #include <utility>
 
+#include "adjust_plan.hpp"
 #include "common.hpp"
 #include "rowseg.hpp"
 #include "spec_verify.h"
-#include "xent_plan.hpp"
 
 namespace spec {
 namespace {
 
-constexpr int kSlice = 4096, kLongHistory = 8192;
-constexpr int kSlotBits = 12, kSlots = 1 << kSlotBits, kProbes = 64, kFewThreads = 512, kFewGroups = 512, kMaxBits = 4;
+constexpr int kProbes = 64;
 constexpr uint32_t kInPrompt = 1u << 30, kDrafted = 1u << 31, kBiased = 1u << 29, kCount = kBiased - 1;
 
 struct AdjustArgs {
@@ -432,48 +431,27 @@ __global__ __launch_bounds__(kFewThreads) void adjust_few_kernel(AdjustArgs a, i
 }
 
 template <bool BF16, bool BIAS, bool COPY, int S, int T>
-void launch(const AdjustArgs& a, int B, hipStream_t s) {
-  const dim3 grid((unsigned)ceil_div(a.V, S) * (unsigned)B);
+void launch(const AdjustArgs& a, dim3 grid, hipStream_t s) {
   hipLaunchKernelGGL((adjust_kernel<BF16, BIAS, COPY, S, T>), grid, dim3(T), 0, s, a);
 }
 
-// 2^bits classes: as many as give kFewGroups workgroups while each still has some 256 pairs, and no more tokens to a
-// class than fill its table to two thirds (as far as a launch's work-items can be counted).  256 single tokens of
-// 151936 after 4096: 256 and 512 workgroups 17.7 us, 1024 21.6, 2048 31; 64 blocks of 17 rows: 256 workgroups 23.9,
-// 512 and more 22.
-int few_bits(int B, int R, long long named) {
-  int bits = 0;
-  while (bits < kMaxBits && (2ll * B << bits) <= kFewGroups && named * R >= 512ll << bits) ++bits;
-  while (bits < kMaxBits && 3 * named > 2ll * kSlots << bits && (2ll * B * kFewThreads << bits) <= 0xffffffffll) ++bits;
-  return bits;
-}
-
-// Slices of 4096 tokens, 16 bytes of a row per thread: two workgroups a CU or more (64 blocks of 17 rows of 151936
-// bf16, half of them live, out of place: 83 us; slices of 2048 91; fp32, half as many blocks: by 512 threads 81, by
-// 1024 77).  Every slice's workgroup reads the whole history, and from some 8000 tokens on half as many slices are
-// faster (96 x 8 rows of 129280 after 30011 tokens: 115 -> 103 us; after 1000: 70 -> 71).
-// In place without a mask a row's slice through LDS is only ahead where much of the vocabulary is listed: 64 blocks of
-// 17 rows as above, histories of a 32nd of the vocabulary 70 us, of a 16th 81, of an 8th 98; the listed tokens where
-// they lie 38, 81 and 141.  256 single tokens likewise: 71, 80 and 106; 21, 36 and 77.
 template <bool BF16, bool BIAS>
-void run_adjust(const AdjustArgs& a, int B, hipStream_t s) {
+void run_adjust(const AdjustArgs& a, int B, const AdjustPlan& p, hipStream_t s) {
   const bool copy = a.logits != a.out;
-  const long long named = (long long)a.H + a.gamma + a.bias_count / B;   // tokens of a request at most, or so
-  if (!copy && !a.mask && named <= a.V / (a.R == 1 ? 8 : 16)) {
-    const int bits = few_bits(B, a.R, named);
-    hipLaunchKernelGGL((adjust_few_kernel<BF16, BIAS>), dim3((unsigned)B << bits), dim3(kFewThreads), 0, s, a, bits);
+  const dim3 grid((unsigned)p.workgroups(B, a.V));
+  if (p.bits >= 0) {
+    hipLaunchKernelGGL((adjust_few_kernel<BF16, BIAS>), grid, dim3(kFewThreads), 0, s, a, p.bits);
     return;
   }
   if constexpr (BF16 && !BIAS) {
-    if (a.H > kLongHistory) {
-      if (copy) launch<BF16, BIAS, true, 2 * kSlice, 1024>(a, B, s);
-      else launch<BF16, BIAS, false, 2 * kSlice, 1024>(a, B, s);
+    if (p.slice == 2 * kSlice) {
+      if (copy) launch<BF16, BIAS, true, 2 * kSlice, 1024>(a, grid, s);
+      else launch<BF16, BIAS, false, 2 * kSlice, 1024>(a, grid, s);
       return;
     }
   }
-  constexpr int T = BF16 ? 512 : 1024;
-  if (copy) launch<BF16, BIAS, true, kSlice, T>(a, B, s);
-  else launch<BF16, BIAS, false, kSlice, T>(a, B, s);
+  if (copy) launch<BF16, BIAS, true, kSlice, slice_threads(BF16)>(a, grid, s);
+  else launch<BF16, BIAS, false, kSlice, slice_threads(BF16)>(a, grid, s);
 }
 
 }  // namespace
@@ -506,18 +484,18 @@ extern "C" int32_t spec_adjust_logits(int32_t B, int32_t R, int32_t V, int32_t d
                       {mask, (size_t)masks * R * words * sizeof(uint32_t)}, {mask_index, per}})
     if (overlap(logits_out, bytes, p, m) || overlap(status, per, p, m)) return SPEC_ERR_INVALID_ARG;
   if (overlap(status, per, logits_out, bytes) || overlap(status, per, logits, bytes)) return SPEC_ERR_INVALID_ARG;
-  // a launch's work-items are counted in 32 bits; the larger slices have the more of them
-  if ((long long)ceil_div(V, 2 * kSlice) * B * 1024 > 0xffffffffll) return SPEC_ERR_UNSUPPORTED;
+  const AdjustPlan p = plan_adjust(dtype == SPEC_BF16, logits_out != logits, bias_offsets, mask, B, R, V, H, gamma, bias_count);
+  if (p.workgroups(B, V) * p.threads > kMostItems) return SPEC_ERR_UNSUPPORTED;
   const AdjustArgs a{reinterpret_cast<const char*>(logits), reinterpret_cast<char*>(logits_out), draft_tokens, lengths,
                      history, history_len, prompt_len, repetition, frequency, presence, bias_offsets, bias_tokens,
                      bias_values, mask, mask_index, status, R, V, gamma, H, bias_count, masks, (int)words};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (dtype == SPEC_BF16) {
-    if (bias_offsets) run_adjust<true, true>(a, B, s);
-    else run_adjust<true, false>(a, B, s);
+    if (bias_offsets) run_adjust<true, true>(a, B, p, s);
+    else run_adjust<true, false>(a, B, p, s);
   } else {
-    if (bias_offsets) run_adjust<false, true>(a, B, s);
-    else run_adjust<false, false>(a, B, s);
+    if (bias_offsets) run_adjust<false, true>(a, B, p, s);
+    else run_adjust<false, false>(a, B, p, s);
   }
   return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
 }

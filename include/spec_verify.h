@@ -855,8 +855,8 @@ int32_t spec_head_logits(int32_t N, int32_t V, int32_t d, int32_t dtype, const u
  * Logits pointers are 16-byte aligned.  No workspace.
  * Errors: SPEC_ERR_INVALID_ARG (shape, dtype, alignment, null pointer, one of a
  * group of arrays without the others, an output that overlaps an input but for
- * logits_out = logits); SPEC_ERR_UNSUPPORTED (a launch past 2^32 work-items, 1024 for
- * each request and 8192 tokens of the vocabulary).
+ * logits_out = logits); SPEC_ERR_UNSUPPORTED (a launch past 2^32 work-items: at most
+ * 1024 for each request and 4096 tokens of the vocabulary).
  */
 int32_t spec_adjust_logits(int32_t B, int32_t R, int32_t V, int32_t dtype, const void* logits, int32_t gamma,
                            const int32_t* draft_tokens, const int32_t* lengths, const int32_t* history, int32_t H,

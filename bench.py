@@ -396,8 +396,8 @@ def overlap_leg(sv, torch, w, copies, lengths, stream, reps=20):
 
 def head_leg(sv, torch, w, stream, requests=64, d=4096, reps=10):
     """From hidden states to verified tokens for `requests` blocks of the workload's shape: spec_head_norm (8-bit
-    output), spec_head_logits, spec_adjust_logits in place (histories of 2048 tokens), spec_verify.  Each call's time
-    by HIP events, not part of the step."""
+    output), spec_head_logits (in the workload's type), spec_adjust_logits in place (histories of 2048 tokens),
+    spec_verify.  Each call's time by HIP events, not part of the step."""
     from draft_verification_04_amd.hipevents import HipEvent
     dev, V, G = w.target.device, w.V, w.gamma
     B = min(requests, w.B)
@@ -409,7 +409,7 @@ def head_leg(sv, torch, w, stream, requests=64, d=4096, reps=10):
     full = torch.empty((V, d), dtype=torch.bfloat16, device=dev).normal_(0.0, 3.0 / d ** 0.5, generator=g)
     k = sv.head_quantize(full)
     del full
-    logits = torch.empty((B, R, V), dtype=torch.bfloat16, device=dev)
+    logits = torch.empty((B, R, V), dtype=w.target.dtype, device=dev)   # verification takes both sides in one type
     hist = torch.randint(V, (B, 2048), generator=g, device=dev).to(torch.int32)
     ones = torch.ones(B, device=dev)
     repetition, frequency = 1.1 * ones, 0.1 * ones

@@ -117,6 +117,14 @@ __device__ __forceinline__ void wait_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// Between LDS accesses of a wave's lanes to one another's values: the compiler keeps their order (the wave's LDS accesses
+// are carried out in it; no instruction comes of this).
+__device__ __forceinline__ void wave_exchange() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Tile of block `bid` of `total`: each of the 8 XCDs takes a contiguous run of tiles.
 __device__ __forceinline__ int xcd_tile(int bid, int total) {
   const int x = bid & 7, i = bid >> 3, q = total >> 3, rem = total & 7;
@@ -330,6 +338,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
         *reinterpret_cast<SPEC_LDS bf16x4*>(p) = h;
       }
     }
+    wave_exchange();
 #pragma unroll
     for (int r = 0; r < 16; r += 64 / LANES) {
       const int row = r + lane / LANES, c = lane % LANES * VE, j = j0 + (wj * NT + n) * 16 + row, i = iw + c;
@@ -346,6 +355,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void logits_tile_kernel(LogitArgs 
           }
       }
     }
+    wave_exchange();
   }
 }
 

@@ -533,3 +533,23 @@ def test_from_hidden_states_to_verified_tokens(sv):
     assert at["status"].tolist() == [0] * B and ad["status"].tolist() == [0] * B
     h = HostInputs.of(target, draft, toks, L, None, None, seed)
     compare_verify(out, run_oracle_pooled(h), inputs=h)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", list(PLANS))
+def test_every_logit_in_its_place(sv, shape, dtype):
+    """Rows that pick one column of the weight each: every logit is one code of the weight, exactly, so that values that
+    change places between a wave's lanes on their way out cannot pass for rounding."""
+    N, V, d = shape
+    g = torch.Generator(device=DEV).manual_seed(N + V + d)
+    w = torch.randint(0, 256, (V, d), generator=g, device=DEV, dtype=torch.uint8)
+    w[(w & 0x7f) == 0x7f] = 0                                                      # not NaN
+    w = w.view(torch.float8_e4m3fn)
+    pick = torch.randint(0, d, (N,), generator=g, device=DEV)
+    x = torch.zeros((N, d), device=DEV)
+    x[torch.arange(N, device=DEV), pick] = 1.0
+    ones = lambda *s: torch.ones(s, device=DEV)
+    G = -(-d // 128)
+    z = sv.head_logits(x.to(torch.float8_e4m3fn), ones(N, G), w, ones(-(-V // 128), G), dtype=DT[dtype])
+    torch.cuda.synchronize()
+    assert torch.equal(z.float(), w.float().t()[pick])

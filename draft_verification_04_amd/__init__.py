@@ -1272,6 +1272,8 @@ def adjust_logits(logits: torch.Tensor, draft_tokens: Optional[torch.Tensor] = N
         if not isinstance(mask, torch.Tensor) or mask.dim() != 3 or tuple(mask.shape[1:]) != (R, words):
             raise ValueError(f"mask must be [M, {R}, {words}]")
         M = mask.shape[0]
+        if M == 0:   # no storage: the library would take its address for no mask
+            raise ValueError("mask holds no masks")
     elif mask_index is not None:
         raise ValueError("mask_index needs a mask")
     _int32(B=B, R=R, V=V, H=H, nb=nb, M=M)

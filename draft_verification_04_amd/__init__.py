@@ -1239,9 +1239,9 @@ def adjust_logits(logits: torch.Tensor, draft_tokens: Optional[torch.Tensor] = N
     logits [B, R, V] (float32 or bfloat16): target rows (R = gamma + 1) or draft rows (R = gamma) of blocks whose
     draft_tokens are [B, gamma] int32 (None: R = 1, single tokens); lengths [B] int32: only rows k < L_i (+ 1 for
     target rows) are adjusted.  history [B, H] int32 (-1 holes count for nothing), history_len and prompt_len [B]
-    int32; repetition, frequency and presence [B] float32; bias = (offsets [B + 1] int32, tokens int32, values
-    float32); mask [M, R, ceil(V / 32)] int32 bits (set: allowed) and mask_index [B] int32 (-1: none; None: mask i).
-    in_place writes over `logits` (16 bytes at most around a value that changes), unseen by autograd; otherwise `out`,
+    int32 (not read where H = 0); repetition, frequency and presence [B] float32; bias = (offsets [B + 1] int32, tokens
+    int32, values float32); mask [M, R, ceil(V / 32)] int32 bits (set: allowed) and mask_index [B] int32 (-1: none;
+    None: mask i).  in_place writes over `logits` (16 bytes at most around a value that changes), unseen by autograd; otherwise `out`,
     or a new tensor whose rows past a length or with a status are undefined.  Returns dict(logits, status [B] int32).
     """
     lib = load_library()
@@ -1262,8 +1262,6 @@ def adjust_logits(logits: torch.Tensor, draft_tokens: Optional[torch.Tensor] = N
         H = history.shape[1]
     elif history_len is not None or prompt_len is not None:
         raise ValueError("history_len and prompt_len need a history")
-    if history is not None and H == 0:   # of no tokens: the lengths can only be 0
-        history = history_len = prompt_len = None
     offsets, tokens, values = bias if bias is not None else (None, None, None)
     nb = 0 if bias is None else tokens.numel() if isinstance(tokens, torch.Tensor) else -1
     words = -(-V // 32)
@@ -1307,6 +1305,8 @@ def adjust_logits(logits: torch.Tensor, draft_tokens: Optional[torch.Tensor] = N
         _on(dev, mask=mask, out=out, **ints, **floats)
     if in_place and out is not None:
         raise ValueError("pass out or in_place, not both")
+    if H == 0:   # of no tokens: the lengths can only be 0
+        history = history_len = prompt_len = None
     mine = []
     if in_place:
         out = logits

@@ -30,3 +30,10 @@ def test_no_masks(sv, index):
     kw = dict(mask_index=_i(2) - 1) if index else {}
     with pytest.raises(ValueError, match="mask"):
         sv.adjust_logits(torch.zeros(2, 4, 50), _i(2, 3), mask=_i(0, 4, 2), **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(history_len=_i(3)), dict(prompt_len=_i(2, 1)), dict(history_len=[0, 0])])
+def test_lengths_of_a_history_of_no_tokens(sv, kw):
+    """They are checked like any others, though there is nothing to read."""
+    with pytest.raises(ValueError, match=next(iter(kw))):
+        sv.adjust_logits(torch.zeros(2, 4, 50), _i(2, 3), history=_i(2, 0), **kw)

@@ -1241,7 +1241,9 @@ def adjust_logits(logits: torch.Tensor, draft_tokens: Optional[torch.Tensor] = N
     target rows) are adjusted.  history [B, H] int32 (-1 holes count for nothing), history_len and prompt_len [B]
     int32 (not read where H = 0); repetition, frequency and presence [B] float32; bias = (offsets [B + 1] int32, tokens
     int32, values float32); mask [M, R, ceil(V / 32)] int32 bits (set: allowed) and mask_index [B] int32 (-1: none;
-    None: mask i).  in_place writes over `logits` (16 bytes at most around a value that changes), unseen by autograd; otherwise `out`,
+    None: mask i).
+
+    in_place writes over `logits` (16 bytes at most around a value that changes), unseen by autograd; otherwise `out`,
     or a new tensor whose rows past a length or with a status are undefined.  Returns dict(logits, status [B] int32).
     """
     lib = load_library()

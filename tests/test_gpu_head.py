@@ -553,3 +553,37 @@ def test_every_logit_in_its_place(sv, shape, dtype):
     z = sv.head_logits(x.to(torch.float8_e4m3fn), ones(N, G), w, ones(-(-V // 128), G), dtype=DT[dtype])
     torch.cuda.synchronize()
     assert torch.equal(z.float(), w.float().t()[pick])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(4099, 72), (8195, 9), (4101, 1000), (2100, 2001), (1030, 4096), (2051, 2999), (1100, 8001),
+                                   (300, 16384)])
+def test_norm_backward_over_several_turns(sv, shape, dtype):
+    """Teams of every size take more than one row each: both gradients, with the stream's own gradient and without it,
+    and written over each input that may be."""
+    N, d = shape
+    x, r, w = _norm_inputs(N + d, N, d, dtype)
+    gy, gh, _ = _norm_inputs(N + d + 1, N, d, dtype)
+    o = sv.head_norm(x, w, r)
+    rs, g = _np(o["rstd"])[:, None], np.abs(_np(gy) * _np(w))
+    xh = np.abs(_np(o["h"]) * rs)
+    rows = -(-N // (256 if d > 8192 else 512 if d > 4096 else 1024))
+    for g2 in (gh, None):
+        print(f"norm backward over turns {shape} {dtype} stream={g2 is not None}", flush=True)
+        b = sv.head_norm_backward(gy, o["h"], w, o["rstd"], g2)
+        torch.cuda.synchronize()
+        ref = oracle.head_norm_grad(gy, o["h"], w, o["rstd"], g2)
+        tol = U * (rs * (5 * g + 46 * xh * (g * xh).mean(axis=1, keepdims=True)) + 3 * np.abs(ref["grad_x"])
+                   + (0 if g2 is None else np.abs(_np(g2)))) + _half(gy) * np.abs(ref["grad_x"])
+        _near(b["grad_x"], ref["grad_x"], tol)
+        tol = U * (6 + rows) * (np.abs(_np(gy)) * xh).sum(axis=0) + _half(gy) * np.abs(ref["grad_weight"])
+        _near(b["grad_weight"], ref["grad_weight"], tol)
+        for name, t in (("grad_y", gy), ("h", o["h"]), ("grad_h", g2)):
+            if t is None:
+                continue
+            ins = dict(grad_y=gy, h=o["h"], grad_h=g2)
+            ins[name] = t.clone()
+            c = sv.head_norm_backward(ins["grad_y"], ins["h"], w, o["rstd"], ins["grad_h"],
+                                      out=dict(grad_x=ins[name], grad_weight=torch.empty_like(w)))
+            torch.cuda.synchronize()
+            assert torch.equal(c["grad_x"], b["grad_x"]) and torch.equal(c["grad_weight"], b["grad_weight"]), name

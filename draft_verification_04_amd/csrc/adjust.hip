@@ -140,13 +140,14 @@ __device__ __forceinline__ bool gather(const AdjustArgs& a, const Request& q, in
     }
   }
   if constexpr (BIAS) {
-    for (int i = tid; i < q.bn && q.live > 0; i += T) {
-      const int t = a.bias_tokens[q.bo + i];
+    // unsigned: the step behind the last entry may pass 2^31
+    for (unsigned i = tid; i < (unsigned)q.bn && q.live > 0; i += T) {
+      const int t = a.bias_tokens[(unsigned)q.bo + i];
       const unsigned at = slot_of(t);
       off |= (unsigned)t >= (unsigned)a.V;
       if (at < slots) {
         note(at, t, atomicOr(&count[at], kBiased));
-        atomicMax(&bias_at[at], (uint32_t)i + 1);
+        atomicMax(&bias_at[at], i + 1);
       }
     }
   }

@@ -357,3 +357,20 @@ def test_in_place_on_streams_and_in_a_captured_graph(sv):
         print(f"in place, replay {rep}", flush=True)
         assert np.array_equal(_bits(work[0]), _bits(work[1])) and status.tolist() == [0] * 24
         assert np.array_equal(_bits(work[0][rows]), _bits(ref[rows]))
+
+
+def test_as_many_biases_as_can_be_counted(sv):
+    """2^31 - 1 entries for one request: a thread's step behind its last one passes the largest int32.  The last entry of
+    every token counts, here the list's last 512."""
+    V, n = 512, 2 ** 31 - 1
+    t = torch.arange(n, dtype=torch.int32, device=DEV).bitwise_and_(V - 1)
+    v = torch.zeros(n, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(14)
+    v[-V:] = torch.randn(V, generator=g, device=DEV)
+    v[-V - 40:-V] = math.nan                                       # each of these is listed again
+    z = torch.randn((1, 1, V), generator=g, device=DEV)
+    ref = z.clone()
+    ref[0, 0, t[-V:].long()] += v[-V:]
+    o = sv.adjust_logits(z, bias=(torch.tensor([0, n], dtype=torch.int32, device=DEV), t, v))
+    torch.cuda.synchronize()
+    assert o["status"].tolist() == [0] and torch.equal(o["logits"], ref)

@@ -35,10 +35,17 @@ inline int few_bits(int B, int R, long long named) {
 // Slices of 4096 tokens, 16 bytes of a row per thread: two workgroups a CU or more (64 blocks of 17 rows of 151936
 // bf16, half of them live, out of place: 83 us; slices of 2048 91; fp32, half as many blocks: by 512 threads 81, by
 // 1024 77).  Every slice's workgroup reads the whole history, and from some 8000 tokens on half as many slices are
-// faster (96 x 8 rows of 129280 after 30011 tokens: 115 -> 103 us; after 1000: 70 -> 71).
+// faster (96 x 8 rows of 129280 after 30011 tokens: 115 -> 103 us; after 1000: 70 -> 71).  Not so with biases, whose
+// table leaves room for one such workgroup a CU (the same rows with 64 biases a request after 12000 and 30011 tokens: 125
+// -> 130 and 174 -> 181; under masks 128 -> 138 and 179 -> 191), nor in fp32, with twice the bytes of a row (48 x 8: 77 ->
+// 81 and 90 -> 94; under masks 76 -> 85 and 92 -> 103).
 // In place without a mask a row's slice through LDS is only ahead where much of the vocabulary is listed: 64 blocks of
 // 17 rows as above, histories of a 32nd of the vocabulary 70 us, of a 16th 81, of an 8th 98; the listed tokens where
 // they lie 38, 81 and 141.  256 single tokens likewise: 71, 80 and 106; 21, 36 and 77.
+// What the host knows is the histories' room H and the number of biases of all requests: short histories in a wide
+// array are taken for long ones (256 single tokens after 500: 13 us with H = 500, 15 with 16384, 51 with 32768; 64 blocks
+// of 17 rows: 17 and, from 9481 on, 72), and one request's long list for everybody's short one (100000 biases for one of
+// 256 single tokens: its classes do not fit their tables, 3.4 ms in place, 84 us out of place).
 inline AdjustPlan plan_adjust(bool bf16, bool copy, bool bias, bool mask, int B, int R, int V, int H, int gamma,
                               int bias_count) {
   const long long named = (long long)H + gamma + bias_count / B;   // tokens of a request at most, or so

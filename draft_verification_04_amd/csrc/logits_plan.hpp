@@ -8,20 +8,23 @@ namespace spec {
 // Tiles of `bm` tokens by `bn` rows; a workgroup's waves and the steps of its pipeline are the kernel's.  `slots` of
 // them fit the chip at once.  A step (a block of 128 of k) takes `full` microseconds where the chip is full of them
 // and `single` where there is one per CU at most, or as long as its part of the weight takes from memory; a
-// workgroup starts and stores in `ends`.  Measured, bf16 logits, us:
+// workgroup starts and stores in `ends`.  Measured in one run, bf16 logits, us with the launch:
 //                          256x256 256x128 128x128 128x64 128x32 64x64 64x32
-//   16 x   2048, d = 16384     155      91      83     57     52    35    34
-//  256 x   4096, d = 16384     156      91      89     60     55    36    53
-//  300 x  20011, d =  1024      17      12      13     19      -     -     -
-//  512 x  16384, d =  4096      44      35      37     59     95    57   110
-//  512 x  32768, d =  4096      68      78      94    114    184   142   210
-//   17 x 151936, d =  4096       -       -       -    113    112   112   109
-//   64 x 151936, d =  4096       -       -       -    118    160   134   190
-//  128 x 151936, d =  4096     178     144     160    179      -     -     -
-//  256 x 151936, d =  4096     197     196     234    290      -     -     -
-//  2048 x 151936, d = 4096    1133       -       -      -      -     -     -
-// 128 x 64 and 128 x 32 read the weight past the caches and are for at most as many rows.  fp32 logits, whose
-// products take twice the time, have no tile of 256.
+//   16 x   2048, d = 16384     155      91      83     54     49    36    30
+//  256 x   4096, d = 16384     157      92      88     60     54    37    38
+//  300 x  20011, d =  1024      17      13      12     18      -     -     -
+//  512 x  16384, d =  4096      44      35      37     60     94    58    72
+//  512 x  32768, d =  4096      65      73      81    115    181   122   147
+//    1 x 151936, d =  4096       -       -       -    110    110   113   115
+//   17 x 151936, d =  4096       -       -       -    116    116   119   119
+//   64 x 151936, d =  4096       -       -       -    122    162   138   157
+//  128 x 151936, d =  4096     185     154     167    182      -     -     -
+//  256 x 151936, d =  4096     198     202     238    290      -     -     -
+//  2048 x 151936, d = 4096    1187       -       -      -      -     -     -
+// The model gives the order, not the times: it has 103 us for the 116 of 17 rows, where the weight comes from memory,
+// 170 for the 198 of 256, and 145 and 118 for the 157 and 154 that 64 rows by 64 x 32 and 128 by 256 x 128 take; its picks
+// are within 4 % of the best above.  128 x 64 and 128 x 32 read the weight past the caches and are for at most as many
+// rows.  fp32 logits, whose products take twice the time, have no tile of 256.
 struct LogitTile {
   int bm, bn, slots;
   double full, single, ends;

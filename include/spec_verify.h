@@ -734,7 +734,8 @@ int32_t spec_head_xent_backward(int32_t N, int32_t V, int32_t d, int32_t dtype, 
  * Numbers in 8 bits are e4m3 (OCP: 4 exponent bits, 3 mantissa bits, largest
  * value 448, no infinities), with a float32 scale for each block:
  *   scale = max(amax, 2^-100) / 448, code = the block's values / scale rounded to
- *   nearest, ties to even.  A NaN or infinity in a block makes its codes or its
+ *   nearest, ties to even (the norm's values and quotients are fp32: within 64 2^-24 of
+ *   halfway between two codes it may be either).  A NaN or infinity in a block makes its codes or its
  *   scale NaN or infinite, and every logit formed from it NaN.
  *
  * spec_head_norm -- root-mean-square norm with the residual's addition:
@@ -787,7 +788,8 @@ int32_t spec_head_norm_backward(int32_t N, int32_t d, int32_t dtype, const void*
  *   last ones may be smaller).  weight [V, d] of `dtype`; 1 <= V <= SPEC_MAX_V, d a
  *   multiple of 16 up to SPEC_MAX_HEAD_WIDTH.  weight and codes_out are 16-byte
  *   aligned; outputs overlap nothing.  Codes are those of the exact quotients for
- *   bf16.  Errors: SPEC_ERR_INVALID_ARG.
+ *   bf16; an fp32 quotient within 4 2^-24 of halfway between two codes may take either.
+ *   Errors: SPEC_ERR_INVALID_ARG.
  *
  * spec_head_logits -- the logits of such a head:
  *   out[n, v] = sum over blocks g of 128 of scales[n, g] * weight_scales[v / 128, g] *
@@ -797,7 +799,8 @@ int32_t spec_head_norm_backward(int32_t N, int32_t d, int32_t dtype, const void*
  *   order and rounded once to `dtype`.  Within a block fp32 logits are fp32 sums of
  *   exact products; bf16 logits are summed by the matrix units' 8-bit form, which
  *   cuts 8 products at a time off at 2^-13 of the largest (off by less than 7 2^-13
- *   of the terms' magnitudes; 1.5e-5 of a logit for normal data, bf16's half step is 2^-9).
+ *   of the terms' magnitudes; 1.5e-5 of a logit for normal data, 5e-5 where magnitudes
+ *   spread over 2^14; bf16 rounds by up to 2^-8).
  *   logits_out   [N, V] of `dtype` (SPEC_BF16 or SPEC_F32): with N = B * (gamma + 1)
  *                rows, spec_verify's target_logits (within its limit on V)
  *   1 <= N <= SPEC_MAX_HEAD_ROWS; V and d as above.  codes, weight_codes and
@@ -834,7 +837,8 @@ int32_t spec_head_logits(int32_t N, int32_t V, int32_t d, int32_t dtype, const u
  *                are adjusted, the others neither read nor written
  *   history      [B, H] int32 or NULL (H = 0): the tokens so far, oldest first; -1 holes
  *                count for nothing (spec_verify's out_tokens can be appended as they are).
- *                H <= SPEC_MAX_HISTORY
+ *                H <= SPEC_MAX_HISTORY.  In place H also chooses between two kernels with
+ *                the same results: an array not much wider than its histories is faster
  *   history_len  [B] int32 in [0, H] or NULL (= H); prompt_len [B] int32 in [0,
  *                history_len] or NULL (= 0): the first prompt_len tokens are the prompt
  *   repetition (> 0), frequency, presence   [B] float32 or NULL (1, 0, 0).  Where all

@@ -363,18 +363,33 @@ __global__ __launch_bounds__(256) void quantize_kernel(const void* w, int V, int
 #pragma unroll
     for (int x = 0; x < 8; ++x) m = max(m, magnitude(v[u][x]));
   const float amax = __uint_as_float(team_amax<256>(m, sh));
-  // w 448 / amax to the nearest fp32 (a quotient of two bf16 values often lies halfway between two codes, where the
-  // last bit decides): both scaled to amax in [1, 2), one correction of the product with the reciprocal
+  // The code nearest to w 448 / amax, both scaled to amax in [1, 2): the product with the reciprocal, corrected once.
+  // Quotients of two bf16 values often lie halfway between two codes, where the last bit decides; else they are further
+  // from there than fp32's rounding.  Quotients of fp32 values can lie closer, and are off by up to 1.5 units here (448 w is
+  // rounded): those within 2 units of halfway (19 zero bits) are taken again with lo, what 448 w lost.  The sign of what is
+  // then left of 448 w says on which side of q the quotient is (the remainders are exact as far as their sign needs), and of
+  // the two fp32 values around it the odd one, which is never halfway between codes, rounds as the quotient does.
   const int e = ilogbf(amax);
   const float as = ldexpf(amax, -e), r = kCodeMax / as;
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
     float q[8];
+    bool near = false;
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
       const float ws = ldexpf(v[u][x], -e), p = ws * r;
       q[x] = fmaf(fmaf(-p, as, ws * kCodeMax), 1.f / as, p);
+      near |= ((__float_as_uint(q[x]) + 2u) & 0x7ffffu) <= 4u;
     }
+    if (!BF16 && near && c < d)
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const float ws = ldexpf(v[u][x], -e), hi = ws * kCodeMax, lo = fmaf(ws, kCodeMax, -hi);
+        q[x] = fmaf(fmaf(-q[x], as, hi) + lo, 1.f / as, q[x]);
+        const float rest = fmaf(-q[x], as, hi) + lo;
+        const uint32_t b = __float_as_uint(q[x]), past = (__float_as_uint(rest) ^ b) >> 31;
+        if (rest != 0.f) q[x] = __uint_as_float((b - past) | 1u);
+      }
     if (r0 + 16 * u < V && c < d)
       *reinterpret_cast<v2u32*>(codes + (size_t)(r0 + 16 * u) * d + c) =
           v2u32{codes4(q[0], q[1], q[2], q[3]), codes4(q[4], q[5], q[6], q[7])};

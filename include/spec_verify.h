@@ -787,8 +787,7 @@ int32_t spec_head_norm_backward(int32_t N, int32_t d, int32_t dtype, const void*
  *   [ceil(V / 128), ceil(d / 128)] float32, a scale for each block of 128 x 128 (the
  *   last ones may be smaller).  weight [V, d] of `dtype`; 1 <= V <= SPEC_MAX_V, d a
  *   multiple of 16 up to SPEC_MAX_HEAD_WIDTH.  weight and codes_out are 16-byte
- *   aligned; outputs overlap nothing.  Codes are those of the exact quotients for
- *   bf16; an fp32 quotient within 4 2^-24 of halfway between two codes may take either.
+ *   aligned; outputs overlap nothing.  Codes are those of the exact quotients.
  *   Errors: SPEC_ERR_INVALID_ARG.
  *
  * spec_head_logits -- the logits of such a head:

@@ -587,3 +587,47 @@ def test_norm_backward_over_several_turns(sv, shape, dtype):
                                       out=dict(grad_x=ins[name], grad_weight=torch.empty_like(w)))
             torch.cuda.synchronize()
             assert torch.equal(c["grad_x"], b["grad_x"]) and torch.equal(c["grad_weight"], b["grad_weight"]), name
+
+
+def _e4m3_values():
+    v = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    return np.unique(v[np.isfinite(v)])
+
+
+@pytest.mark.parametrize("kind", ["normal", "bf16 values", "next to halfway", "small and large"])
+@pytest.mark.parametrize("shape", [(257, 4096), (1000, 1040)])
+def test_codes_of_fp32_weights_are_the_nearest(sv, shape, kind):
+    """Every code is the one nearest to w 448 / amax, the even one halfway between two.  Exact: 448 w and code * amax have at
+    most 33 and 28 bits, and their difference is exact in fp64 for the code and its neighbours."""
+    print(f"nearest codes {shape} {kind}", flush=True)
+    V, d = shape
+    rng = np.random.default_rng(V + d)
+    w = (0.05 * rng.standard_normal((V, d))).astype(np.float32)
+    if kind == "bf16 values":
+        w = torch.from_numpy(w).to(torch.bfloat16).float().numpy()
+    if kind == "small and large":
+        w *= np.exp2(rng.integers(-120, 120, (-(-V // 128), -(-d // 128))).repeat(128, 0)[:V].repeat(128, 1)[:, :d]).astype(np.float32)
+    spread = lambda m: m.repeat(128, 0)[:V].repeat(128, 1)[:, :d]
+    pad = lambda a: np.pad(np.abs(a), ((0, -V % 128), (0, -d % 128))).reshape(-(-V // 128), 128, -(-d // 128), 128)
+    values = _e4m3_values()
+    if kind == "next to halfway":
+        top = pad(w).max((1, 3))
+        m = spread(top.astype(np.float64))
+        k = rng.integers(0, len(values) - 1, (V, d))
+        near = ((values[k] + values[k + 1]) / 2 * m / 448).astype(np.float32)
+        step = rng.integers(-1, 2, (V, d))
+        near = np.where(step == 0, near, np.nextafter(near, np.where(step > 0, np.inf, -np.inf).astype(np.float32)))
+        w = np.where(np.abs(w) == m, w, near.astype(np.float32))
+    m = spread(np.maximum(pad(w).max((1, 3)).astype(np.float64), 2.0 ** -100))
+    o = sv.head_quantize(torch.from_numpy(w).to(DEV))
+    torch.cuda.synchronize()
+    c = _np(o["codes"])
+    at = np.searchsorted(values, c)
+    assert (values[at] == c).all()
+    a = 448.0 * w.astype(np.float64)
+    here = np.abs(a - c * m)
+    even = (o["codes"].view(torch.uint8).cpu().numpy() & 1) == 0
+    for by in (-1, 1):
+        other = np.abs(a - values[np.clip(at + by, 0, len(values) - 1)] * m)
+        ok = (at + by < 0) | (at + by >= len(values)) | (here < other) | ((here == other) & even)
+        assert ok.all(), (int((~ok).sum()), np.argwhere(~ok)[:3].tolist())
